@@ -261,6 +261,82 @@ int gemm_bf16f32_batched(int trans_b, int M, int N, int K, float alpha,
                          float beta, float *C, int ldc, int64_t stride_c,
                          int batch, void *stream);
 
+/*
+ * Microscaled 4-bit floating point (MX4). A matrix of rows x K values is held
+ * as codes and scales. Each row is cut into blocks of 32 values (the last one
+ * may be shorter). A value is a 4-bit code: bit 3 the sign, bits 2..1 an
+ * exponent, bit 0 a fraction, standing for 0, 0.5, 1, 1.5, 2, 3, 4 or 6. Two
+ * codes share a byte, the earlier value in bits 3..0; a row has ceil(K/2)
+ * bytes, and bits past its K values are written 0 and never used. A block has
+ * one scale byte s, and its values are the codes' times 2^(s - 127); s = 255
+ * makes all of them NaN. A row has ceil(K/32) scale bytes. This is the
+ * element and scale encoding that the OCP Microscaling Formats specification
+ * calls MXFP4 (E2M1 elements, E8M0 scales, blocks of 32).
+ *
+ * Leading dimensions of codes and scales are in BYTES; neither needs any
+ * alignment.
+ */
+
+/* Element types of mx4_quantize, mx4_dequantize and the residual norms. */
+#define LL_TYPE_F32 0
+#define LL_TYPE_F16 1
+#define LL_TYPE_BF16 2
+
+/*
+ * mx4_quantize — X (M-by-K, `type`, ldx >= max(1, K) elements) into MX4.
+ * A block whose largest magnitude is t gets the scale 2^e with
+ * e = floor(log2(t)) - 2, at least -127 (t = 0: -127), and each value v the
+ * code nearest to v / 2^e, ties to the even code, magnitudes past 6 to 6. A
+ * block that holds an infinity or a NaN gets the scale byte 255 and codes 0.
+ *
+ *   trans 0   codes: M rows of ceil(K/2) bytes, ldq >= max(1, that) apart;
+ *             scales: M rows of ceil(K/32) bytes, lds >= max(1, that) apart.
+ *   trans 1   the transposed matrix is quantised: K rows of M values, blocks
+ *             along X's columns. A layer's backward products contract over
+ *             other axes than its forward product and need their operands so.
+ * The outputs must not overlap X or each other. M == 0 or K == 0: LL_OK,
+ * touches nothing.
+ */
+int mx4_quantize(int M, int K, int type, const void *X, int ldx, int trans,
+                 uint8_t *codes, int ldq, uint8_t *scales, int lds, void *stream);
+
+/*
+ * mx4_dequantize — Y (M-by-K, `type`, ldy >= max(1, K)) = the values that
+ * codes and scales stand for. FP32 and bfloat16 hold each of them exactly, up
+ * to their largest finite value; binary16 rounds those below 2^-24 steps and
+ * overflows to infinity past 65504. Y must not overlap codes or scales.
+ */
+int mx4_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *scales, int lds,
+                   int type, void *Y, int ldy, void *stream);
+
+/*
+ * gemm_mx4f32_nt — C = alpha * A * B^T + beta * C with A (M-by-K) and B
+ * (N-by-K, the [out][in] layout of a weight) in MX4, FP32 sums and FP32 C.
+ * gemm_f16mx4f32_nt, gemm_bf16mx4f32_nt — the same with A in binary16 or
+ * bfloat16 (bit patterns; lda >= max(1, K) elements) and B in MX4: every
+ * decoded value of B enters its products exactly, whatever its scale.
+ *
+ *   SA, SB    the scales of A and B; ldsa, ldsb >= max(1, ceil(K/32)) bytes.
+ *   lda, ldb  bytes between rows of codes, >= max(1, ceil(K/2)).
+ * Other arguments, rules and errors as gemm_f32: with beta == 0 C is not
+ * read, K == 0 or alpha == 0 gives C = beta*C and reads neither operand, C
+ * must not overlap an input. One launch, nothing allocated; the summation
+ * order is fixed by the shape, so equal calls give equal results.
+ * Rows (of A, of B) 16 bytes aligned, with K a multiple of 32, take the
+ * direct-to-LDS tile kernels when the product is large; other operands are
+ * streamed through registers at any alignment.
+ */
+int gemm_mx4f32_nt(int M, int N, int K, float alpha,
+                   const uint8_t *A, int lda, const uint8_t *SA, int ldsa,
+                   const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
+                   float beta, float *C, int ldc, void *stream);
+int gemm_f16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int lda,
+                      const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
+                      float beta, float *C, int ldc, void *stream);
+int gemm_bf16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int lda,
+                       const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
+                       float beta, float *C, int ldc, void *stream);
+
 /* A static, human-readable string for a status code (never NULL). */
 const char *ll_status_string(int status);
 

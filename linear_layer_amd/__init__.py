@@ -23,6 +23,12 @@ Entry points (same names as the C ABI in ``include/linear_layer.h``):
   ``(A, B, C, alpha=1.0, beta=0.0, trans_b=False)`` — C[i] = alpha*A[i]*op(B[i])
   + beta*C[i] over 3-D tensors whose first axis is the batch; its stride is the
   batch stride (0, e.g. from ``expand``, shares one matrix among all items).
+* ``mx4_quantize(X, codes, scales, trans=False)``, ``mx4_dequantize(codes, scales, Y)``
+  — microscaled 4-bit floating point (blocks of 32 values along a row, two 4-bit
+  codes a byte, one scale byte a block; ``mx4_shapes`` gives the tensors' shapes).
+* ``gemm_mx4f32_nt(A, SA, B, SB, C, alpha=1.0, beta=0.0, K=None)`` — C = alpha*A*B^T
+  + beta*C, both operands in that format; ``gemm_f16mx4f32_nt`` and
+  ``gemm_bf16mx4f32_nt(A, B, SB, C, alpha=1.0, beta=0.0)`` — the same with 16-bit A.
 
 Matrices are 2-D, row-major with unit column stride (a row stride larger than
 the width is a leading dimension), on the current CUDA/HIP device. The calls
@@ -39,6 +45,8 @@ __all__ = [
     "gemm_f32_batched", "gemm_f16f32_batched", "gemm_bf16f32_batched",
     "linear_bias_act_ws", "linear_workspace_size", "linear_bias_act_noalloc", "NOALLOC_SCRATCH_BYTES",
     "set_noalloc_limit",
+    "mx4_quantize", "mx4_dequantize", "mx4_shapes", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
+    "TYPE_F32", "TYPE_F16", "TYPE_BF16",
     "library_path", "load", "set_tile", "num_tiles", "tile_name", "chosen_tile",
     "set_split_k", "chosen_split_k", "set_stream_k", "chosen_stream_k",
     "ACT_NONE", "ACT_RELU", "DTYPE_F32", "DTYPE_F16", "PLAN_RELU", "PLAN_B_NK", "PLAN_UNALIGNED",
@@ -48,6 +56,7 @@ __all__ = [
 OK, ERR_INVALID_VALUE, ERR_NO_DEVICE, ERR_UNSUPPORTED_ARCH, ERR_LAUNCH = 0, 1, 2, 3, 4
 ACT_NONE, ACT_RELU = 0, 1
 DTYPE_F32, DTYPE_F16 = 0, 1
+TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2   # element types of mx4_quantize, mx4_dequantize and the residual norms
 PLAN_RELU, PLAN_B_NK, PLAN_UNALIGNED = 0x100, 0x200, 0x400   # flags OR-ed into dtype for chosen_*
 NOALLOC_SCRATCH_BYTES = 65 << 20   # the static workspace of linear_bias_act_noalloc
 
@@ -65,7 +74,8 @@ EXPORTED = ("gemm_f32", "gemm_f16f32", "gemm_bf16f32", "linear_bias_act", "ll_st
             "ll_num_tiles", "ll_tile_name", "ll_set_tile", "ll_chosen_tile",
             "ll_set_split_k", "ll_chosen_split_k", "ll_set_stream_k", "ll_chosen_stream_k",
             "linear_bias_act_ws", "ll_linear_workspace_size", "linear_bias_act_noalloc",
-            "ll_set_noalloc_limit")
+            "ll_set_noalloc_limit",
+            "mx4_quantize", "mx4_dequantize", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt")
 
 
 class LinearLayerError(RuntimeError):
@@ -110,6 +120,14 @@ def load():
     for f in (lib.gemm_f32, lib.gemm_f16f32, lib.gemm_bf16f32, lib.linear_bias_act,
               lib.gemm_f32_nt, lib.gemm_f16f32_nt, lib.gemm_bf16f32_nt, lib.linear_bias_act_nt,
               lib.gemm_f32_batched, lib.gemm_f16f32_batched, lib.gemm_bf16f32_batched):
+        f.restype = i32
+    lib.mx4_quantize.argtypes = [i32, i32, i32, vp, i32, i32, vp, i32, vp, i32, vp]
+    lib.mx4_dequantize.argtypes = [i32, i32, vp, i32, vp, i32, i32, vp, i32, vp]
+    lib.gemm_mx4f32_nt.argtypes = [i32, i32, i32, f32, vp, i32, vp, i32, vp, i32, vp, i32, f32, vp, i32, vp]
+    lib.gemm_f16mx4f32_nt.argtypes = [i32, i32, i32, f32, vp, i32, vp, i32, vp, i32, f32, vp, i32, vp]
+    lib.gemm_bf16mx4f32_nt.argtypes = lib.gemm_f16mx4f32_nt.argtypes
+    for f in (lib.mx4_quantize, lib.mx4_dequantize, lib.gemm_mx4f32_nt, lib.gemm_f16mx4f32_nt,
+              lib.gemm_bf16mx4f32_nt):
         f.restype = i32
     lib.ll_status_string.argtypes = [i32]
     lib.ll_status_string.restype = ctypes.c_char_p
@@ -419,3 +437,103 @@ def _linear(fn_name, X, W, bias, act, Y, stream, wt=False, ws=None):
                                       _stream(stream, X, W, Y, bias))
     _check(st, fn_name)
     return Y
+
+
+# ---- microscaled 4-bit floating point ---------------------------------------
+
+def mx4_shapes(rows: int, K: int):
+    """The shapes of the codes and of the scales of a rows x K matrix (both uint8)."""
+    return (rows, (K + 1) // 2), (rows, (K + 31) // 32)
+
+
+_TYPES = None
+
+
+def _type_of(t, name):
+    """The LL_TYPE_* value of a tensor's dtype."""
+    global _TYPES
+    torch = _torch()
+    if _TYPES is None:
+        _TYPES = {torch.float32: TYPE_F32, torch.float16: TYPE_F16, torch.bfloat16: TYPE_BF16}
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _TYPES:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _packed(codes, scales, K, what):
+    """(rows, codes pointer, ld, scales pointer, ld) of a packed matrix of K values a row."""
+    torch = _torch()
+    pq, rows, nq, ldq = _mat(codes, torch.uint8, f"{what} codes")
+    ps, rows2, ns, lds = _mat(scales, torch.uint8, f"{what} scales")
+    want, want_s = mx4_shapes(rows, K)
+    if (rows, nq) != want or (rows2, ns) != want_s:
+        raise ValueError(f"{what}: {K} values a row need codes {want} and scales {want_s}, got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    return rows, pq, ldq, ps, lds
+
+
+def mx4_quantize(X, codes, scales, trans: bool = False, stream=None):
+    """Quantise X (float32, float16 or bfloat16; M x K) into uint8 codes and scales,
+    along its rows, or with ``trans`` along its columns into the packed transposed
+    matrix (K rows of M values). Returns (codes, scales)."""
+    t = _type_of(X, "X")
+    px, M, K, ldx = _mat(X, X.dtype, "X")
+    rows, pq, ldq, ps, lds = _packed(codes, scales, M if trans else K, "X")
+    if rows != (K if trans else M):
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, codes {tuple(codes.shape)}")
+    _check(load().mx4_quantize(M, K, t, px, ldx, int(bool(trans)), pq, ldq, ps, lds,
+                               _stream(stream, X, codes, scales)), "mx4_quantize")
+    return codes, scales
+
+
+def mx4_dequantize(codes, scales, Y, stream=None):
+    """Y (float32, float16 or bfloat16; M x K) = the values codes and scales stand for."""
+    t = _type_of(Y, "Y")
+    py, M, K, ldy = _mat(Y, Y.dtype, "Y")
+    rows, pq, ldq, ps, lds = _packed(codes, scales, K, "Y")
+    if rows != M:
+        raise ValueError(f"shape mismatch: Y {tuple(Y.shape)}, codes {tuple(codes.shape)}")
+    _check(load().mx4_dequantize(M, K, pq, ldq, ps, lds, t, py, ldy, _stream(stream, Y, codes, scales)),
+           "mx4_dequantize")
+    return Y
+
+
+def gemm_mx4f32_nt(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, K: int | None = None, stream=None):
+    """C = alpha*A*B^T + beta*C with A (M x K) and B (N x K) as uint8 codes and scales;
+    K is twice the codes' width unless given (an odd K has to be)."""
+    torch = _torch()
+    if K is None:
+        K = 2 * A.shape[1] if getattr(A, "ndim", 0) == 2 else 0
+    K = int(K)
+    M, pa, lda, psa, ldsa = _packed(A, SA, K, "A")
+    N, pb, ldb, psb, ldsb = _packed(B, SB, K, "B")
+    pc, M2, N2, ldc = _mat(C, torch.float32, "C")
+    if M2 != M or N2 != N:
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+    _check(load().gemm_mx4f32_nt(M, N, K, float(alpha), pa, lda, psa, ldsa, pb, ldb, psb, ldsb, float(beta), pc,
+                                 ldc, _stream(stream, A, SA, B, SB, C)), "gemm_mx4f32_nt")
+    return C
+
+
+def _gemm_16mx4(fn_name, in_dtype, A, B, SB, C, alpha, beta, stream):
+    torch = _torch()
+    pa, M, K, lda = _mat(A, in_dtype, "A")
+    N, pb, ldb, psb, ldsb = _packed(B, SB, K, "B")
+    pc, M2, N2, ldc = _mat(C, torch.float32, "C")
+    if M2 != M or N2 != N:
+        raise ValueError(f"shape mismatch: A {tuple(A.shape)}, B {tuple(B.shape)}, C {tuple(C.shape)}")
+    _check(getattr(load(), fn_name)(M, N, K, float(alpha), pa, lda, pb, ldb, psb, ldsb, float(beta), pc, ldc,
+                                    _stream(stream, A, B, SB, C)), fn_name)
+    return C
+
+
+def gemm_f16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
+    """C = alpha*A*B^T + beta*C with fp16 A and B (N x K) as uint8 codes and scales."""
+    return _gemm_16mx4("gemm_f16mx4f32_nt", _torch().float16, A, B, SB, C, alpha, beta, stream)
+
+
+def gemm_bf16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
+    """C = alpha*A*B^T + beta*C with bf16 A and B (N x K) as uint8 codes and scales."""
+    return _gemm_16mx4("gemm_bf16mx4f32_nt", _torch().bfloat16, A, B, SB, C, alpha, beta, stream)

@@ -1,0 +1,33 @@
+// Host-side launchers of the 4-bit format, its products and the residual norms.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ll {
+
+hipError_t launch_mx4_quantize(int type, const void *X, int64_t ldx, bool trans, uint8_t *codes, int64_t ldq,
+                               uint8_t *scales, int64_t lds, int M, int K, hipStream_t s);
+hipError_t launch_mx4_dequantize(int type, const uint8_t *codes, int64_t ldq, const uint8_t *scales,
+                                 int64_t lds, void *Y, int64_t ldy, int M, int K, hipStream_t s);
+
+// The first operand of a product: MX4 codes, or 16-bit values.
+enum MxA : int { MXA_MX4 = 0, MXA_F16 = 1, MXA_BF16 = 2 };
+
+// C = alpha * A * B^T + beta * C, B in MX4 (N rows of K), A in MX4 or 16 bits.
+struct MxParams {
+    const uint8_t *A;        // codes, or 16-bit values as bytes
+    const uint8_t *SA;       // A's scales (MXA_MX4)
+    const uint8_t *B, *SB;   // B's codes and scales
+    float *C;
+    int64_t lda, ldb;        // bytes between rows
+    int64_t ldsa, ldsb;      // bytes between rows of scales
+    int64_t ldc;             // elements
+    int M, N, K;
+    float alpha, beta;
+    int tiles_m, tiles_n;
+};
+
+hipError_t launch_gemm_mx4(MxParams p, int a, int cus, hipStream_t s);
+
+}  // namespace ll
