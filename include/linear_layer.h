@@ -337,6 +337,53 @@ int gemm_bf16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int 
                        const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
                        float beta, float *C, int ldc, void *stream);
 
+/*
+ * rmsnorm_residual — the residual step between two blocks of a network, the
+ * norm after the one and the norm before the other in one pass. For each row,
+ * with r(v) = 1 / sqrt(mean(v^2) + eps):
+ *
+ *   x' = x + alpha * gate * (y * r(y) * w_post)
+ *   h  = x' * r(x') * w_pre
+ *
+ *   Y       the block's output, M-by-N fp32 as every product here writes it,
+ *           ldy >= max(1, N); NULL: x' = x (the norm before the first block).
+ *   X       the residual stream, M-by-N of `type` (LL_TYPE_*).
+ *   XO, H   x' and h, M-by-N of `type`; either may be NULL (not both). XO may
+ *           be X itself (same ld); no other overlap of an output is allowed.
+ *   w_post, gate, w_pre   N fp32 values each; NULL stands for ones.
+ *   alpha   the residual scale; eps >= 0, finite.
+ * Arithmetic is FP32; h is computed from x' before its rounding. Any ld,
+ * alignment (to the element) and N. M == 0 or N == 0: LL_OK.
+ */
+int rmsnorm_residual(int M, int N, int type, const float *Y, int ldy,
+                     const float *w_post, const float *gate, float alpha,
+                     const void *X, int ldx, const float *w_pre, float eps,
+                     void *XO, int ldxo, void *H, int ldh, void *stream);
+
+/*
+ * rmsnorm_residual_grad — its gradient. DXO and DH (M-by-N of `type`) are the
+ * gradients that reach x' and h; either may be NULL for zero (not both). The
+ * forward inputs are given again (X before any in-place update). Outputs, each
+ * of which may be NULL: DY (M-by-N fp32), DX (M-by-N of `type`; may be DXO
+ * itself, same ld), and the sums over rows dgate, dw_post, dw_pre (N fp32
+ * values). Without Y, DY, dgate and dw_post must be NULL.
+ *
+ *   workspace   at least ll_rmsnorm_grad_workspace_size(M, N) bytes, 16-byte
+ *               aligned, overlapping nothing; its contents need no
+ *               preparation. Calls that share one must not overlap in time.
+ * The order of the sums is fixed by the shape. M == 0 with N > 0 writes zeros
+ * to dgate, dw_post and dw_pre.
+ */
+int rmsnorm_residual_grad(int M, int N, int type, const void *DXO, int lddxo, const void *DH, int lddh,
+                          const float *Y, int ldy, const float *w_post, const float *gate, float alpha,
+                          const void *X, int ldx, const float *w_pre, float eps,
+                          float *DY, int lddy, void *DX, int lddx,
+                          float *dgate, float *dw_post, float *dw_pre,
+                          void *workspace, int64_t workspace_bytes, void *stream);
+/* Bytes of workspace rmsnorm_residual_grad needs (at most 8 * 512 * N for N up
+ * to 16384); -1 for a negative size. */
+int64_t ll_rmsnorm_grad_workspace_size(int M, int N);
+
 /* A static, human-readable string for a status code (never NULL). */
 const char *ll_status_string(int status);
 

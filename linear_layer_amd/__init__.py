@@ -29,6 +29,10 @@ Entry points (same names as the C ABI in ``include/linear_layer.h``):
 * ``gemm_mx4f32_nt(A, SA, B, SB, C, alpha=1.0, beta=0.0, K=None)`` — C = alpha*A*B^T
   + beta*C, both operands in that format; ``gemm_f16mx4f32_nt`` and
   ``gemm_bf16mx4f32_nt(A, B, SB, C, alpha=1.0, beta=0.0)`` — the same with 16-bit A.
+* ``rmsnorm_residual(Y, w_post, gate, alpha, X, w_pre, XO, H, eps=1e-5)`` — the residual
+  step between two blocks: XO = X + alpha*gate*rms(Y)*w_post, H = rms(XO)*w_pre;
+  ``rmsnorm_residual_grad`` — its gradient (``rmsnorm_grad_workspace_size`` bytes of
+  workspace).
 
 Matrices are 2-D, row-major with unit column stride (a row stride larger than
 the width is a leading dimension), on the current CUDA/HIP device. The calls
@@ -46,6 +50,7 @@ __all__ = [
     "linear_bias_act_ws", "linear_workspace_size", "linear_bias_act_noalloc", "NOALLOC_SCRATCH_BYTES",
     "set_noalloc_limit",
     "mx4_quantize", "mx4_dequantize", "mx4_shapes", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
+    "rmsnorm_residual", "rmsnorm_residual_grad", "rmsnorm_grad_workspace_size",
     "TYPE_F32", "TYPE_F16", "TYPE_BF16",
     "library_path", "load", "set_tile", "num_tiles", "tile_name", "chosen_tile",
     "set_split_k", "chosen_split_k", "set_stream_k", "chosen_stream_k",
@@ -75,7 +80,8 @@ EXPORTED = ("gemm_f32", "gemm_f16f32", "gemm_bf16f32", "linear_bias_act", "ll_st
             "ll_set_split_k", "ll_chosen_split_k", "ll_set_stream_k", "ll_chosen_stream_k",
             "linear_bias_act_ws", "ll_linear_workspace_size", "linear_bias_act_noalloc",
             "ll_set_noalloc_limit",
-            "mx4_quantize", "mx4_dequantize", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt")
+            "mx4_quantize", "mx4_dequantize", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
+            "rmsnorm_residual", "rmsnorm_residual_grad", "ll_rmsnorm_grad_workspace_size")
 
 
 class LinearLayerError(RuntimeError):
@@ -126,6 +132,12 @@ def load():
     lib.gemm_mx4f32_nt.argtypes = [i32, i32, i32, f32, vp, i32, vp, i32, vp, i32, vp, i32, f32, vp, i32, vp]
     lib.gemm_f16mx4f32_nt.argtypes = [i32, i32, i32, f32, vp, i32, vp, i32, vp, i32, f32, vp, i32, vp]
     lib.gemm_bf16mx4f32_nt.argtypes = lib.gemm_f16mx4f32_nt.argtypes
+    lib.rmsnorm_residual.argtypes = [i32, i32, i32, vp, i32, vp, vp, f32, vp, i32, vp, f32, vp, i32, vp, i32, vp]
+    lib.rmsnorm_residual_grad.argtypes = [i32, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, f32, vp, i32, vp, f32,
+                                          vp, i32, vp, i32, vp, vp, vp, vp, i64, vp]
+    lib.rmsnorm_residual.restype = lib.rmsnorm_residual_grad.restype = i32
+    lib.ll_rmsnorm_grad_workspace_size.argtypes = [i32, i32]
+    lib.ll_rmsnorm_grad_workspace_size.restype = i64
     for f in (lib.mx4_quantize, lib.mx4_dequantize, lib.gemm_mx4f32_nt, lib.gemm_f16mx4f32_nt,
               lib.gemm_bf16mx4f32_nt):
         f.restype = i32
@@ -537,3 +549,79 @@ def gemm_f16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream
 def gemm_bf16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     """C = alpha*A*B^T + beta*C with bf16 A and B (N x K) as uint8 codes and scales."""
     return _gemm_16mx4("gemm_bf16mx4f32_nt", _torch().bfloat16, A, B, SB, C, alpha, beta, stream)
+
+
+# ---- residual norms ------------------------------------------------------------
+
+def _opt_mat(t, dtype, name, M, N):
+    """(pointer, ld) of an M x N matrix, or (None, 0) for None."""
+    if t is None:
+        return None, max(N, 1)
+    p, rows, cols, ld = _mat(t, dtype, name)
+    if (rows, cols) != (M, N):
+        raise ValueError(f"{name} must be {(M, N)}, got {tuple(t.shape)}")
+    return p, ld
+
+
+def _opt_vec(t, name, N):
+    """Pointer of a contiguous fp32 vector of N values, or None."""
+    torch = _torch()
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != N or not t.is_cuda:
+        raise ValueError(f"{name} must be a 1-D fp32 device tensor of length {N}")
+    if N > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def rmsnorm_residual(Y, w_post, gate, alpha, X, w_pre, XO, H, eps: float = 1e-5, stream=None):
+    """XO = X + alpha*gate*rms(Y)*w_post and H = rms(XO)*w_pre over the rows, rms(v) =
+    v / sqrt(mean(v^2) + eps). Y is fp32, X, XO and H of one type; Y, the vectors and
+    one of XO and H may be None. XO may be X. Returns (XO, H)."""
+    torch = _torch()
+    t = _type_of(X, "X")
+    px, M, N, ldx = _mat(X, X.dtype, "X")
+    py, ldy = _opt_mat(Y, torch.float32, "Y", M, N)
+    pxo, ldxo = _opt_mat(XO, X.dtype, "XO", M, N)
+    ph, ldh = _opt_mat(H, X.dtype, "H", M, N)
+    _check(load().rmsnorm_residual(M, N, t, py, ldy, _opt_vec(w_post, "w_post", N), _opt_vec(gate, "gate", N),
+                                   float(alpha), px, ldx, _opt_vec(w_pre, "w_pre", N), float(eps), pxo, ldxo, ph, ldh,
+                                   _stream(stream, X, Y, XO, H, w_post, gate, w_pre)), "rmsnorm_residual")
+    return XO, H
+
+
+def rmsnorm_grad_workspace_size(M: int, N: int) -> int:
+    """Bytes of workspace rmsnorm_residual_grad needs for M x N."""
+    n = load().ll_rmsnorm_grad_workspace_size(int(M), int(N))
+    if n < 0:
+        raise ValueError("negative size")
+    return n
+
+
+def rmsnorm_residual_grad(DXO, DH, Y, w_post, gate, alpha, X, w_pre, DY, DX, dgate, dw_post, dw_pre, workspace,
+                          eps: float = 1e-5, stream=None):
+    """The gradient of rmsnorm_residual: DXO and DH (either may be None) are those of XO
+    and H; DY, DX, dgate, dw_post and dw_pre are written (each may be None). workspace:
+    a contiguous device tensor of rmsnorm_grad_workspace_size(M, N) bytes or more.
+    Returns (DY, DX, dgate, dw_post, dw_pre)."""
+    torch = _torch()
+    t = _type_of(X, "X")
+    px, M, N, ldx = _mat(X, X.dtype, "X")
+    pdxo, lddxo = _opt_mat(DXO, X.dtype, "DXO", M, N)
+    pdh, lddh = _opt_mat(DH, X.dtype, "DH", M, N)
+    py, ldy = _opt_mat(Y, torch.float32, "Y", M, N)
+    pdy, lddy = _opt_mat(DY, torch.float32, "DY", M, N)
+    pdx, lddx = _opt_mat(DX, X.dtype, "DX", M, N)
+    pws, nws = None, 0
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous device tensor")
+        pws, nws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load().rmsnorm_residual_grad(
+        M, N, t, pdxo, lddxo, pdh, lddh, py, ldy, _opt_vec(w_post, "w_post", N), _opt_vec(gate, "gate", N), float(alpha),
+        px, ldx, _opt_vec(w_pre, "w_pre", N), float(eps), pdy, lddy, pdx, lddx, _opt_vec(dgate, "dgate", N),
+        _opt_vec(dw_post, "dw_post", N), _opt_vec(dw_pre, "dw_pre", N), pws, nws,
+        _stream(stream, X, DXO, DH, Y, w_post, gate, w_pre, DY, DX, dgate, dw_post, dw_pre, workspace)),
+        "rmsnorm_residual_grad")
+    return DY, DX, dgate, dw_post, dw_pre

@@ -30,4 +30,31 @@ struct MxParams {
 
 hipError_t launch_gemm_mx4(MxParams p, int a, int cus, hipStream_t s);
 
+// The residual step between two blocks (rmsnorm.hip); null pointers leave parts out.
+struct NormParams {
+    const float *Y;                        // the block's output, or null
+    const float *w_post, *gate, *w_pre;    // N values each, or null: ones
+    const void *X;
+    void *XO, *H;
+    int64_t ldy, ldx, ldxo, ldh;           // elements
+    int M, N;
+    float alpha, eps;
+};
+hipError_t launch_rmsnorm_residual(int type, const NormParams &p, hipStream_t s);
+
+struct NormGradParams {
+    const float *Y, *w_post, *gate, *w_pre;
+    const void *X, *DXO, *DH;
+    float *DY;
+    void *DX;
+    float *DGATE, *DWPOST, *DWPRE;
+    float *part;                           // partial column sums (set by the launcher)
+    int64_t ldy, ldx, lddxo, lddh, lddy, lddx;
+    int M, N;
+    float alpha, eps;
+};
+// Bytes of the workspace launch_rmsnorm_grad uses.
+int64_t rmsnorm_grad_workspace(int M, int N);
+hipError_t launch_rmsnorm_grad(int type, const NormGradParams &p, void *ws, hipStream_t s);
+
 }  // namespace ll

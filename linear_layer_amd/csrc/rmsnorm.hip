@@ -1,0 +1,527 @@
+// The residual step between two blocks of a network and its gradient:
+//   x' = x + alpha * gate * (y * r_y * w_post),  r_y = (mean(y^2)  + eps)^(-1/2)
+//   h  = x' * r_x * w_pre,                       r_x = (mean(x'^2) + eps)^(-1/2)
+// per row of N values: y is the block's product (FP32), x the residual stream,
+// gate, w_post, w_pre vectors over the columns. Sums, means and x' between the
+// two norms are FP32; x' and h are rounded once each.
+//
+// Gradient, given dx' and dh. With u = y * r_y, n = x' * r_x and
+// t = alpha * gate * w_post:
+//   T  = dx' + r_x * (dh * w_pre - n * mean(dh * w_pre * n))   (all that reaches x')
+//   dx = T,  dy = r_y * (T * t - u * mean(T * t * u))
+//   dgate = alpha * w_post * S,  dw_post = alpha * gate * S,  S = sum over rows of T * u
+//   dw_pre = sum over rows of dh * n
+//
+// Both are bound by HBM: a row is read once into registers and its sums go
+// through one workgroup. Rows too long for the registers are read again.
+#include "linear_layer.h"
+#include "lowp.hpp"
+#include "mx4.hpp"
+
+namespace ll {
+
+// The sums of V values over a workgroup of NT threads, in every thread. The
+// order is fixed: lanes by halving distance, then waves in turn. `lds` is used
+// again by the next call: two barriers.
+template <int NT, int V>
+__device__ __forceinline__ void block_sum(float (&v)[V], float *lds)
+{
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int d = 32; d >= 1; d >>= 1)
+            v[i] += __shfl_xor(v[i], d);
+    }
+    if constexpr (NT > 64) {
+        constexpr int NW = NT / 64;
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                lds[i * NW + wave] = v[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            v[i] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w)
+                v[i] += lds[i * NW + w];
+        }
+        __syncthreads();
+    }
+}
+
+__device__ __forceinline__ float inv_rms(float sum, int n, float eps)
+{
+    return 1.0f / sqrtf(sum / (float)n + eps);
+}
+
+// E values of a column vector from c on; `one` where there is no vector.
+template <int E>
+__device__ __forceinline__ void load_vec(const float *v, int64_t c, int64_t n, float one, float (&o)[E])
+{
+    if (v == nullptr) {
+#pragma unroll
+        for (int j = 0; j < E; ++j)
+            o[j] = one;
+    } else {
+        load_row<LL_TYPE_F32, E>(v + c, n - c, o);
+    }
+}
+
+// A thread holds C groups of 8 neighbouring values, 8 * NT columns apart.
+// LONG: rows longer than 8 * NT * C, walked in several passes over memory,
+// each sum in passes of its own.
+template <int TYPE, int NT, int C, bool LONG>
+__global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
+{
+    using T = typename Elem<TYPE>::type;
+    __shared__ float lds[2 * (NT / 64)];
+    const int N = p.N;
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        const float *y = p.Y != nullptr ? p.Y + m * p.ldy : nullptr;
+        const T *x = static_cast<const T *>(p.X) + m * p.ldx;
+        T *xo = p.XO != nullptr ? static_cast<T *>(p.XO) + m * p.ldxo : nullptr;
+        T *h = p.H != nullptr ? static_cast<T *>(p.H) + m * p.ldh : nullptr;
+        const int span = 8 * NT * C, passes = LONG ? cdiv(N, span) : 1;
+        float yv[C][8], xv[C][8];
+        auto load = [&](int pass) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + threadIdx.x);
+                load_row<TYPE, 8>(x + col, N - col, xv[c]);
+                if (y != nullptr)
+                    load_row<LL_TYPE_F32, 8>(y + col, N - col, yv[c]);
+            }
+        };
+        float ry = 0.0f;
+        if (!LONG)
+            load(0);
+        if (y != nullptr) {
+            float s[1] = {0.0f};
+            for (int pass = 0; pass < passes; ++pass) {
+                if (LONG)
+                    load(pass);
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        s[0] = __builtin_fmaf(yv[c][j], yv[c][j], s[0]);
+            }
+            block_sum<NT>(s, lds);
+            ry = inv_rms(s[0], N, p.eps);
+        }
+        // x' in xv; written where asked for
+        auto residual = [&](int pass, bool store) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + threadIdx.x);
+                if (col >= N)
+                    continue;
+                if (y != nullptr) {
+                    float w[8], g[8];
+                    load_vec<8>(p.w_post, col, N, 1.0f, w);
+                    load_vec<8>(p.gate, col, N, 1.0f, g);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        xv[c][j] = __builtin_fmaf(p.alpha * g[j], yv[c][j] * ry * w[j], xv[c][j]);
+                }
+                if (store && xo != nullptr)
+                    store_row<TYPE, 8>(xo + col, N - col, xv[c]);
+            }
+        };
+        float s[1] = {0.0f};
+        for (int pass = 0; pass < passes; ++pass) {
+            if (LONG)
+                load(pass);
+            // in place (XO = X) a long row is written by its last pass only
+            residual(pass, !LONG || h == nullptr);
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    s[0] = __builtin_fmaf(xv[c][j], xv[c][j], s[0]);
+        }
+        if (h == nullptr)
+            continue;
+        block_sum<NT>(s, lds);
+        const float rx = inv_rms(s[0], N, p.eps);
+        for (int pass = 0; pass < passes; ++pass) {
+            if (LONG) {
+                load(pass);
+                residual(pass, true);
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + threadIdx.x);
+                if (col >= N)
+                    continue;
+                float w[8];
+                load_vec<8>(p.w_pre, col, N, 1.0f, w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    xv[c][j] = xv[c][j] * rx * w[j];
+                store_row<TYPE, 8>(h + col, N - col, xv[c]);
+            }
+        }
+    }
+}
+
+template <int TYPE>
+static hipError_t norm_t(const NormParams &p, hipStream_t s)
+{
+    const int64_t most = 1 << 20;
+    const dim3 grid((unsigned)(p.M < most ? p.M : most));
+#define LL_NORM(NT, C, LONG) \
+    hipLaunchKernelGGL((rmsnorm_residual_kernel<TYPE, NT, C, LONG>), grid, dim3(NT), 0, s, p)
+    if (p.N <= 512)
+        LL_NORM(64, 1, false);
+    else if (p.N <= 2048)
+        LL_NORM(256, 1, false);
+    else if (p.N <= 4096)
+        LL_NORM(256, 2, false);
+    else if (p.N <= 8192)
+        LL_NORM(512, 2, false);
+    else if (p.N <= 16384)
+        LL_NORM(1024, 2, false);
+    else
+        LL_NORM(1024, 1, true);
+#undef LL_NORM
+    return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_residual(int type, const NormParams &p, hipStream_t s)
+{
+    if (type == LL_TYPE_F32)
+        return norm_t<LL_TYPE_F32>(p, s);
+    if (type == LL_TYPE_F16)
+        return norm_t<LL_TYPE_F16>(p, s);
+    return norm_t<LL_TYPE_BF16>(p, s);
+}
+
+// ---- gradient ---------------------------------------------------------------
+//
+// A workgroup walks rows blockIdx.x, blockIdx.x + grid, .. and keeps its
+// columns' shares of S and of dw_pre's sum; it writes them once, as row
+// blockIdx.x of `part` ([grid][2][N] floats), and a second launch adds the
+// rows in order. No atomics: the result does not depend on the run.
+
+template <int TYPE, int NT, int C>
+__global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradParams p)
+{
+    using T = typename Elem<TYPE>::type;
+    __shared__ float lds[2 * (NT / 64)];
+    const int N = p.N;
+    float sS[C][8], sP[C][8], t[C][8], wp[C][8];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+        float g[8];
+        load_vec<8>(p.w_post, col, N, 1.0f, t[c]);
+        load_vec<8>(p.gate, col, N, 1.0f, g);
+        load_vec<8>(p.w_pre, col, N, 1.0f, wp[c]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sS[c][j] = sP[c][j] = 0.0f;
+            t[c][j] *= p.alpha * g[j];
+        }
+    }
+    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+        float yv[C][8], xv[C][8], dv[C][8], kv[C][8];
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+            if (p.Y != nullptr)
+                load_row<LL_TYPE_F32, 8>(p.Y + m * p.ldy + col, N - col, yv[c]);
+            load_row<TYPE, 8>(static_cast<const T *>(p.X) + m * p.ldx + col, N - col, xv[c]);
+            if (p.DXO != nullptr)
+                load_row<TYPE, 8>(static_cast<const T *>(p.DXO) + m * p.lddxo + col, N - col, dv[c]);
+            if (p.DH != nullptr)
+                load_row<TYPE, 8>(static_cast<const T *>(p.DH) + m * p.lddh + col, N - col, kv[c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (p.Y == nullptr)
+                    yv[c][j] = 0.0f;
+                if (p.DXO == nullptr)
+                    dv[c][j] = 0.0f;
+                if (p.DH == nullptr)
+                    kv[c][j] = 0.0f;
+                s[0] = __builtin_fmaf(yv[c][j], yv[c][j], s[0]);
+            }
+        }
+        block_sum<NT>(s, lds);
+        const float ry = inv_rms(s[0], N, p.eps);
+        float q[2] = {0.0f, 0.0f};   // sums of x'^2 and of dh * w_pre * x'
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                yv[c][j] *= ry;   // u
+                xv[c][j] = __builtin_fmaf(t[c][j], yv[c][j], xv[c][j]);
+                q[0] = __builtin_fmaf(xv[c][j], xv[c][j], q[0]);
+                q[1] = __builtin_fmaf(kv[c][j] * wp[c][j], xv[c][j], q[1]);
+            }
+        block_sum<NT>(q, lds);
+        const float rx = inv_rms(q[0], N, p.eps), mean_kn = q[1] * rx / (float)N;
+        float z[1] = {0.0f};
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float n = xv[c][j] * rx;
+                sP[c][j] = __builtin_fmaf(kv[c][j], n, sP[c][j]);
+                dv[c][j] += rx * (kv[c][j] * wp[c][j] - n * mean_kn);   // T
+                sS[c][j] = __builtin_fmaf(dv[c][j], yv[c][j], sS[c][j]);
+                z[0] = __builtin_fmaf(dv[c][j] * t[c][j], yv[c][j], z[0]);
+            }
+        block_sum<NT>(z, lds);
+        const float mean_z = z[0] / (float)N;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+            if (col >= N)
+                continue;
+            if (p.DX != nullptr)
+                store_row<TYPE, 8>(static_cast<T *>(p.DX) + m * p.lddx + col, N - col, dv[c]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                dv[c][j] = ry * (dv[c][j] * t[c][j] - yv[c][j] * mean_z);
+            if (p.DY != nullptr)
+                store_row<LL_TYPE_F32, 8>(p.DY + m * p.lddy + col, N - col, dv[c]);
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+        if (col >= N)
+            continue;
+        float *row = p.part + (int64_t)blockIdx.x * 2 * N + col;
+        store_row<LL_TYPE_F32, 8>(row, N - col, sS[c]);
+        store_row<LL_TYPE_F32, 8>(row + N, N - col, sP[c]);
+    }
+}
+
+// Rows too long for a workgroup's registers, in two launches. First each row's
+// four numbers (r_y, r_x, mean(dh * w_pre * n), mean(T * t * u)), reading the
+// row once for each sum.
+struct RowStats {
+    float ry, rx, mean_kn, mean_z;
+};
+
+// One group of 8 columns of a row, as the formulas name its values.
+template <int TYPE>
+struct GradCols {
+    using T = typename Elem<TYPE>::type;
+    float y[8], x[8], d[8], k[8], t[8], wp[8];
+    __device__ __forceinline__ void vectors(const NormGradParams &p, int64_t col)
+    {
+        float g[8];
+        load_vec<8>(p.w_post, col, p.N, 1.0f, t);
+        load_vec<8>(p.gate, col, p.N, 1.0f, g);
+        load_vec<8>(p.w_pre, col, p.N, 1.0f, wp);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            t[j] *= p.alpha * g[j];
+    }
+    __device__ __forceinline__ void row(const NormGradParams &p, int64_t m, int64_t col)
+    {
+        const int64_t n = p.N - col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            y[j] = d[j] = k[j] = 0.0f;
+        if (p.Y != nullptr)
+            load_row<LL_TYPE_F32, 8>(p.Y + m * p.ldy + col, n, y);
+        load_row<TYPE, 8>(static_cast<const T *>(p.X) + m * p.ldx + col, n, x);
+        if (p.DXO != nullptr)
+            load_row<TYPE, 8>(static_cast<const T *>(p.DXO) + m * p.lddxo + col, n, d);
+        if (p.DH != nullptr)
+            load_row<TYPE, 8>(static_cast<const T *>(p.DH) + m * p.lddh + col, n, k);
+    }
+};
+
+template <int TYPE, int NT>
+__global__ void __launch_bounds__(NT) rmsnorm_grad_stats_kernel(NormGradParams p, RowStats *stats)
+{
+    __shared__ float lds[2 * (NT / 64)];
+    const int64_t m = blockIdx.x;
+    GradCols<TYPE> v;
+    RowStats r;
+    float s[1] = {0.0f}, q[2] = {0.0f, 0.0f}, z[1] = {0.0f};
+    for (int64_t col = 8 * (int64_t)threadIdx.x; col < p.N; col += 8 * NT) {
+        v.row(p, m, col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            s[0] = __builtin_fmaf(v.y[j], v.y[j], s[0]);
+    }
+    block_sum<NT>(s, lds);
+    r.ry = inv_rms(s[0], p.N, p.eps);
+    for (int64_t col = 8 * (int64_t)threadIdx.x; col < p.N; col += 8 * NT) {
+        v.row(p, m, col);
+        v.vectors(p, col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = __builtin_fmaf(v.t[j], v.y[j] * r.ry, v.x[j]);
+            q[0] = __builtin_fmaf(x, x, q[0]);
+            q[1] = __builtin_fmaf(v.k[j] * v.wp[j], x, q[1]);
+        }
+    }
+    block_sum<NT>(q, lds);
+    r.rx = inv_rms(q[0], p.N, p.eps);
+    r.mean_kn = q[1] * r.rx / (float)p.N;
+    for (int64_t col = 8 * (int64_t)threadIdx.x; col < p.N; col += 8 * NT) {
+        v.row(p, m, col);
+        v.vectors(p, col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float u = v.y[j] * r.ry, n = __builtin_fmaf(v.t[j], u, v.x[j]) * r.rx;
+            const float total = v.d[j] + r.rx * (v.k[j] * v.wp[j] - n * r.mean_kn);
+            z[0] = __builtin_fmaf(total * v.t[j], u, z[0]);
+        }
+    }
+    block_sum<NT>(z, lds);
+    r.mean_z = z[0] / (float)p.N;
+    if (threadIdx.x == 0)
+        stats[m] = r;
+}
+
+// Then every column group on its own: 2048 columns and the rows
+// blockIdx.y, blockIdx.y + grid y, .. to a workgroup.
+template <int TYPE>
+__global__ void __launch_bounds__(256) rmsnorm_grad_cols_kernel(NormGradParams p, const RowStats *stats)
+{
+    using T = typename Elem<TYPE>::type;
+    const int64_t col = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (col >= p.N)
+        return;
+    GradCols<TYPE> v;
+    v.vectors(p, col);
+    float sS[8], sP[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        sS[j] = sP[j] = 0.0f;
+    for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
+        const RowStats r = stats[m];
+        v.row(p, m, col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float u = v.y[j] * r.ry, n = __builtin_fmaf(v.t[j], u, v.x[j]) * r.rx;
+            sP[j] = __builtin_fmaf(v.k[j], n, sP[j]);
+            v.d[j] += r.rx * (v.k[j] * v.wp[j] - n * r.mean_kn);
+            sS[j] = __builtin_fmaf(v.d[j], u, sS[j]);
+            v.y[j] = r.ry * (v.d[j] * v.t[j] - u * r.mean_z);
+        }
+        if (p.DX != nullptr)
+            store_row<TYPE, 8>(static_cast<T *>(p.DX) + m * p.lddx + col, p.N - col, v.d);
+        if (p.DY != nullptr)
+            store_row<LL_TYPE_F32, 8>(p.DY + m * p.lddy + col, p.N - col, v.y);
+    }
+    float *row = p.part + (int64_t)blockIdx.y * 2 * p.N + col;
+    store_row<LL_TYPE_F32, 8>(row, p.N - col, sS);
+    store_row<LL_TYPE_F32, 8>(row + p.N, p.N - col, sP);
+}
+
+// The columns' sums over `rows` partial rows, then dgate, dw_post and dw_pre.
+// 64 columns to a workgroup; its 16 waves take every 16th row, and their sums
+// are added in wave order.
+__global__ void __launch_bounds__(1024) rmsnorm_grad_finish_kernel(NormGradParams p, int rows)
+{
+    __shared__ float sums[2][16][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
+    float a = 0.0f, b = 0.0f;
+    if (col < p.N)
+        for (int r = wave; r < rows; r += 16) {
+            a += p.part[(int64_t)r * 2 * p.N + col];
+            b += p.part[(int64_t)r * 2 * p.N + p.N + col];
+        }
+    sums[0][wave][lane] = a;
+    sums[1][wave][lane] = b;
+    __syncthreads();
+    if (wave != 0 || col >= p.N)
+        return;
+    a = b = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+        a += sums[0][w][lane];
+        b += sums[1][w][lane];
+    }
+    if (p.DGATE != nullptr)
+        p.DGATE[col] = p.alpha * (p.w_post != nullptr ? p.w_post[col] : 1.0f) * a;
+    if (p.DWPOST != nullptr)
+        p.DWPOST[col] = p.alpha * (p.gate != nullptr ? p.gate[col] : 1.0f) * a;
+    if (p.DWPRE != nullptr)
+        p.DWPRE[col] = b;
+}
+
+// Rows the registers of 1024 threads hold.
+constexpr int kGradRegCols = 16384;
+// Workgroups (rows of partial sums) of a gradient: two for each CU.
+constexpr int kGradGroups = 512;
+
+static int grad_groups(int M) { return M < kGradGroups ? M : kGradGroups; }
+static int64_t grad_stats_bytes(int M, int N)
+{
+    return N > kGradRegCols ? ((int64_t)M * (int64_t)sizeof(RowStats) + 255) / 256 * 256 : 0;
+}
+
+int64_t rmsnorm_grad_workspace(int M, int N)
+{
+    return M <= 0 || N <= 0 ? 0 : grad_stats_bytes(M, N) + (int64_t)grad_groups(M) * 2 * N * 4;
+}
+
+template <int TYPE>
+static hipError_t norm_grad_t(NormGradParams p, void *ws, hipStream_t s)
+{
+    p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + grad_stats_bytes(p.M, p.N));
+    const int groups = grad_groups(p.M);
+    const dim3 grid((unsigned)groups);
+#define LL_GRAD(NT, C) hipLaunchKernelGGL((rmsnorm_grad_kernel<TYPE, NT, C>), grid, dim3(NT), 0, s, p)
+    if (p.M <= 0)
+        ;   // no rows: the finishing launch writes zeros
+    else if (p.N <= 512)
+        LL_GRAD(64, 1);
+    else if (p.N <= 2048)
+        LL_GRAD(256, 1);
+    else if (p.N <= 4096)
+        LL_GRAD(256, 2);
+    else if (p.N <= 8192)
+        LL_GRAD(1024, 1);
+    else if (p.N <= kGradRegCols)
+        LL_GRAD(1024, 2);
+    else {
+        RowStats *stats = static_cast<RowStats *>(ws);
+        const int slab = 1 << 20;   // rows of a launch: work items fit 32 bits
+        for (int64_t m = 0; m < p.M; m += slab) {
+            NormGradParams q = p;
+            using T = typename Elem<TYPE>::type;
+            q.Y = p.Y != nullptr ? p.Y + m * p.ldy : nullptr;
+            q.X = static_cast<const T *>(p.X) + m * p.ldx;
+            q.DXO = p.DXO != nullptr ? static_cast<const T *>(p.DXO) + m * p.lddxo : nullptr;
+            q.DH = p.DH != nullptr ? static_cast<const T *>(p.DH) + m * p.lddh : nullptr;
+            const int64_t rows = p.M - m < slab ? p.M - m : slab;
+            hipLaunchKernelGGL((rmsnorm_grad_stats_kernel<TYPE, 1024>), dim3((unsigned)rows), dim3(1024), 0, s, q,
+                               stats + m);
+        }
+        hipLaunchKernelGGL((rmsnorm_grad_cols_kernel<TYPE>),
+                           dim3((unsigned)(((int64_t)p.N + 2047) / 2048), (unsigned)groups), dim3(256), 0, s, p,
+                           stats);
+    }
+#undef LL_GRAD
+    if (p.DGATE != nullptr || p.DWPOST != nullptr || p.DWPRE != nullptr)
+        hipLaunchKernelGGL(rmsnorm_grad_finish_kernel, dim3((unsigned)(((int64_t)p.N + 63) / 64)), dim3(1024), 0, s,
+                           p, groups);
+    return hipGetLastError();
+}
+
+hipError_t launch_rmsnorm_grad(int type, const NormGradParams &p, void *ws, hipStream_t s)
+{
+    if (type == LL_TYPE_F32)
+        return norm_grad_t<LL_TYPE_F32>(p, ws, s);
+    if (type == LL_TYPE_F16)
+        return norm_grad_t<LL_TYPE_F16>(p, ws, s);
+    return norm_grad_t<LL_TYPE_BF16>(p, ws, s);
+}
+
+}  // namespace ll
