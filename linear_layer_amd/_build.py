@@ -17,7 +17,7 @@ LIB = os.path.join(PKG, "liblinear_layer.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "gemm_f32.hip", "gemm_f32_nt.hip", "gemm_f16.hip", "elementwise.hip",
-           "api_mx4.hip", "mx4.hip", "gemm_mx4.hip", "api_norm.hip", "rmsnorm.hip"]
+           "api_mx4.hip", "mx4.hip", "gemm_mx4.hip", "gemm_mx4_tile.hip", "api_norm.hip", "rmsnorm.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

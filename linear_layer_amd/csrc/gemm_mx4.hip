@@ -19,83 +19,11 @@
 // into two bfloat16 parts instead (11 bits of fraction into 8 and 3) and
 // multiplies twice, which is exact for every scale.
 #include "linear_layer.h"
-#include "launch.hpp"
-#include "lowp.hpp"
-#include "mx4.hpp"
+#include "gemm_mx4.hpp"
+
+#include <type_traits>
 
 namespace ll {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-
-__device__ __forceinline__ f32x4 mma_mx4(const u32x4 &a, const u32x4 &b, const f32x4 &c, int sa, int sb)
-{
-    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-    const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, 0, sa, 0, sb);
-}
-
-__device__ __forceinline__ f32x4 mma_f16(const u32x4 &a, const u32x4 &b, const f32x4 &c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
-                                                  0, 0, 0);
-}
-
-__device__ __forceinline__ f32x4 mma_bf16(const u32x4 &a, const u32x4 &b, const f32x4 &c)
-{
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
-// Eight codes (one dword) as 16-bit values; `sc` carries the scale byte in an
-// FP32 exponent field.
-template <bool BF16>
-__device__ __forceinline__ u32x4 decode8(uint32_t q, float sc)
-{
-    u32x4 r;
-    if constexpr (BF16) {
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 0));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 1));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 2));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 3));
-    } else {
-        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 0));
-        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 1));
-        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 2));
-        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 3));
-    }
-    return r;
-}
-
-// Eight binary16 values as two bfloat16 parts, hi + lo exactly: hi is the
-// value's top 8 bits of fraction, the rest has 3. An infinity or a NaN stays
-// in hi alone.
-__device__ __forceinline__ void split8(const u32x4 &a, u32x4 &hi, u32x4 &lo)
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t h[2], l[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float v = (float)__builtin_bit_cast(_Float16, (uint16_t)(a[j] >> (16 * e)));
-            const uint32_t b = __builtin_bit_cast(uint32_t, v), t = b & 0xffff0000u;
-            const float d = v - __builtin_bit_cast(float, t);
-            h[e] = t >> 16;
-            l[e] = (b & 0x7f800000u) == 0x7f800000u ? 0u : __builtin_bit_cast(uint32_t, d) >> 16;
-        }
-        hi[j] = h[0] | h[1] << 16;
-        lo[j] = l[0] | l[1] << 16;
-    }
-}
-
-// Whether a scale byte keeps the decoded values exact in binary16.
-__device__ __forceinline__ bool f16_scale_ok(uint32_t s) { return s - 104u <= 36u; }
-
-// One value through the epilogue.
-__device__ __forceinline__ float finish(const MxParams &p, float v, const float *dst)
-{
-    return p.beta == 0.0f ? p.alpha * v : __builtin_fmaf(p.alpha, v, p.beta * *dst);
-}
 
 // ---------------------------------------------------------------------------
 // Streaming kernel: operands go from memory (or L2) straight into registers.
@@ -110,48 +38,11 @@ __device__ __forceinline__ float finish(const MxParams &p, float v, const float 
 //
 // Rows past M or N read the last row instead; their sums are not stored.
 
-// The 16 bytes of codes of block `blk` of a row of K values; values past K
-// are 0.
-__device__ __forceinline__ u32x4 load_block(const uint8_t *row, int64_t blk, int K)
-{
-    const int64_t k = blk * kMxBlock;
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (k + kMxBlock <= K) {
-        v = load16<u32x4>(row + k / 2);
-    } else if (k < K) {
-        const int n = (int)(K - k);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            if (2 * j < n) {
-                const uint32_t b = row[k / 2 + j] & (2 * j + 1 < n ? 0xffu : 0x0fu);
-                v[j / 4] |= b << (8 * (j % 4));
-            }
-        }
-    }
-    return v;
-}
-
-// 16-bit values k .. k+7 of a row of K; 0 past K.
-__device__ __forceinline__ u32x4 load_halves(const uint8_t *row, int64_t k, int K)
-{
-    u32x4 v = {0u, 0u, 0u, 0u};
-    if (k + 8 <= K) {
-        v = load16<u32x4>(row + 2 * k);
-    } else if (k < K) {
-        const uint16_t *h = reinterpret_cast<const uint16_t *>(row) + k;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (k + j < K)
-                v[j / 2] |= (uint32_t)h[j] << (16 * (j % 2));
-    }
-    return v;
-}
-
-template <int A, int FM, int FN, int J, int W>
+template <int A, int FM, int FN, int J, int W, bool LONG>
 __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
 {
+    constexpr bool MX = A == MXA_MX4;
     constexpr int BM = 16 * FM, BN = 16 * FN;
-    constexpr int AC = A == MXA_MX4 ? 1 : 4;   // 16-byte chunks of A per lane and block
     __shared__ float part[W][BM * BN];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -160,8 +51,8 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
     const int tm = id % p.tiles_m, tn = id / p.tiles_m;
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int K = p.K;
-    const int64_t nblk = (int64_t)(K - 1) / kMxBlock + 1;
-    const int64_t nunit = (nblk + 4 * J - 1) / (4 * J);
+    const int nblk = (K - 1) / kMxBlock + 1;
+    const int nunit = (nblk + 4 * J - 1) / (4 * J);
 
     const uint8_t *arow[FM], *sarow[FM], *brow[FN], *sbrow[FN];
 #pragma unroll
@@ -169,7 +60,7 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
         int64_t m = m0 + 16 * i + r16;
         m = m < p.M ? m : p.M - 1;
         arow[i] = p.A + m * p.lda;
-        sarow[i] = A == MXA_MX4 ? p.SA + m * p.ldsa : nullptr;
+        sarow[i] = MX ? p.SA + m * p.ldsa : nullptr;
     }
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
@@ -179,28 +70,55 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
         sbrow[i] = p.SB + n * p.ldsb;
     }
 
+    // J times four blocks. Lane group g has block g's codes of B, and of A in MX4;
+    // of 16-bit A piece t is values 8 g .. +7 of block t, so that the four groups
+    // read 64 bytes of a row at a time.
     struct Unit {
-        u32x4 a[J][FM][AC], b[J][FN];
-        uint32_t sa[J][A == MXA_MX4 ? FM : 1], sb[J][FN];
+        u32x4 a[J][FM][MX ? 1 : 4], b[J][FN];
+        uint32_t sa[J][MX ? FM : 1], sb[J][FN];
     };
-    auto fetch = [&](Unit &u, int64_t unit) {
+    // The unit that K ends in.
+    auto fetch_ragged = [&](Unit &u, int unit) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int64_t blk = (unit * J + j) * 4 + g;
+            const int first = (unit * J + j) * 4, blk = first + g;
 #pragma unroll
             for (int i = 0; i < FN; ++i) {
-                u.b[j][i] = load_block(brow[i], blk, K);
+                u.b[j][i] = load_block<LONG>(brow[i], blk, K);
                 u.sb[j][i] = blk < nblk ? sbrow[i][blk] : 127u;
             }
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
-                if constexpr (A == MXA_MX4) {
-                    u.a[j][i][0] = load_block(arow[i], blk, K);
+                if constexpr (MX) {
+                    u.a[j][i][0] = load_block<LONG>(arow[i], blk, K);
                     u.sa[j][i] = blk < nblk ? sarow[i][blk] : 127u;
                 } else {
 #pragma unroll
                     for (int t = 0; t < 4; ++t)
-                        u.a[j][i][t] = load_halves(arow[i], blk * kMxBlock + 8 * t, K);
+                        u.a[j][i][t] = load_halves<LONG>(arow[i], (int64_t)(first + t) * kMxBlock + 8 * g, K);
+                }
+            }
+        }
+    };
+    // A whole one, without a branch between its loads.
+    auto fetch = [&](Unit &u, int unit) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int first = (unit * J + j) * 4;
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                u.b[j][i] = load16<u32x4>(brow[i] + (int64_t)first * 16 + g * 16);
+                u.sb[j][i] = sbrow[i][first + g];
+            }
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                if constexpr (MX) {
+                    u.a[j][i][0] = load16<u32x4>(arow[i] + (int64_t)first * 16 + g * 16);
+                    u.sa[j][i] = sarow[i][first + g];
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        u.a[j][i][t] = load16<u32x4>(arow[i] + (int64_t)(first + t) * 64 + 16 * g);
                 }
             }
         }
@@ -213,57 +131,88 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
         for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto multiply = [&](const Unit &u) {
+    // (WIDE: binary16 A against scales it cannot take, A's values in two parts)
+    auto multiply = [&](const Unit &u, int j, auto w) __attribute__((always_inline)) {
+        constexpr bool WIDE = decltype(w)::value;
+        if constexpr (MX) {
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-            if constexpr (A == MXA_MX4) {
+            for (int n = 0; n < FN; ++n)
 #pragma unroll
-                for (int n = 0; n < FN; ++n)
+                for (int m = 0; m < FM; ++m)
+                    acc[m][n] = mma_mx4<0, 0>(u.a[j][m][0], u.b[j][n], acc[m][n], (int)u.sa[j][m], (int)u.sb[j][n]);
+        } else {
 #pragma unroll
-                    for (int m = 0; m < FM; ++m)
-                        acc[m][n] = mma_mx4(u.a[j][m][0], u.b[j][n], acc[m][n], (int)u.sa[j][m], (int)u.sb[j][n]);
-            } else {
-                bool wide = false;   // scales binary16 cannot take
-                if constexpr (A == MXA_F16) {
+            for (int n = 0; n < FN; ++n) {
+                u32x4 q = u.b[j][n], sc = {u.sb[j][n] << 23, u.sb[j][n] << 23, u.sb[j][n] << 23, u.sb[j][n] << 23};
+                turn4(q);    // piece t: values 8 g .. +7 of block t
+                turn4(sc);   // and its scale
 #pragma unroll
-                    for (int n = 0; n < FN; ++n)
-                        wide |= !f16_scale_ok(u.sb[j][n]);
-                    wide = __any(wide);
-                }
+                for (int t = 0; t < 4; ++t) {
+                    const u32x4 b = decode8<A == MXA_BF16 || WIDE>(q[t], __uint_as_float(sc[t]));
 #pragma unroll
-                for (int n = 0; n < FN; ++n) {
-                    const float sc = __builtin_bit_cast(float, u.sb[j][n] << 23);
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) {
-                        if (A == MXA_F16 && !wide) {
-                            const u32x4 b = decode8<false>(u.b[j][n][t], sc);
-#pragma unroll
-                            for (int m = 0; m < FM; ++m)
-                                acc[m][n] = mma_f16(u.a[j][m][t], b, acc[m][n]);
+                    for (int m = 0; m < FM; ++m) {
+                        if constexpr (WIDE) {
+                            u32x4 hi, lo;
+                            split8(u.a[j][m][t], hi, lo);
+                            acc[m][n] = mma_bf16(lo, b, acc[m][n]);
+                            acc[m][n] = mma_bf16(hi, b, acc[m][n]);
                         } else {
-                            const u32x4 b = decode8<true>(u.b[j][n][t], sc);
-#pragma unroll
-                            for (int m = 0; m < FM; ++m) {
-                                if constexpr (A == MXA_F16) {
-                                    u32x4 hi, lo;
-                                    split8(u.a[j][m][t], hi, lo);
-                                    acc[m][n] = mma_bf16(lo, b, acc[m][n]);
-                                    acc[m][n] = mma_bf16(hi, b, acc[m][n]);
-                                } else {
-                                    acc[m][n] = mma_bf16(u.a[j][m][t], b, acc[m][n]);
-                                }
-                            }
+                            acc[m][n] = A == MXA_BF16 ? mma_bf16(u.a[j][m][t], b, acc[m][n])
+                                                      : mma_f16(u.a[j][m][t], b, acc[m][n]);
                         }
                     }
                 }
             }
         }
     };
+    // The products of a unit; false, and none made, where a scale is past binary16.
+    auto products = [&](const Unit &u) __attribute__((always_inline)) {
+        if constexpr (A == MXA_F16) {
+            bool wide = false;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+#pragma unroll
+                for (int n = 0; n < FN; ++n)
+                    wide |= !f16_scale_ok(u.sb[j][n]);
+            if (__any(wide))
+                return false;
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            multiply(u, j, std::false_type{});
+        return true;
+    };
 
-    for (int64_t unit = wave; unit < nunit; unit += W) {
-        Unit u;
-        fetch(u, unit);
-        multiply(u);
+    // whole units, two in flight
+    const int whole = K / (128 * J);
+    Unit u0, u1;
+    int unit = wave, left = nunit;   // units from `left` on are still to do
+    if (unit < whole)
+        fetch(u0, unit);
+    while (unit < whole) {
+        const int second = unit + W;
+        if (second < whole)
+            fetch(u1, second);
+        if (!products(u0)) {
+            left = unit;
+            break;
+        }
+        unit = second + W;
+        if (unit < whole)
+            fetch(u0, unit);
+        if (second < whole && !products(u1)) {
+            left = second;
+            break;
+        }
+    }
+    // the one that K ends in, and for binary16 A what its wave left
+    if (left == nunit && whole < nunit && whole % W == wave)
+        left = whole;
+    for (; left < nunit; left += W) {
+        fetch_ragged(u0, left);
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            multiply(u0, j, std::bool_constant<A == MXA_F16>{});
     }
 
     // lane l holds column l % 16 and rows 4 * (l / 16) .. +3 of a block
@@ -289,7 +238,7 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
     }
 }
 
-template <int A, int FM, int FN, int J, int W>
+template <int A, int FM, int FN, int J, int W, bool LONG = true>
 static hipError_t launch_stream(MxParams p, hipStream_t s)
 {
     p.tiles_m = cdiv(p.M, 16 * FM);
@@ -297,15 +246,42 @@ static hipError_t launch_stream(MxParams p, hipStream_t s)
     const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
     if (tiles > max_grid_x(64 * W))
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gemm_mx4_stream_kernel<A, FM, FN, J, W>), dim3((unsigned)tiles), dim3(64 * W), 0, s, p);
+    hipLaunchKernelGGL((gemm_mx4_stream_kernel<A, FM, FN, J, W, LONG>), dim3((unsigned)tiles), dim3(64 * W), 0, s, p);
     return hipGetLastError();
+}
+
+// Which tile: 256 x 256, one to a CU, or 128 x 128, two to a CU, in rounds. A round
+// of the small one takes 0.57 of the large one's time (0.5 with one tile to a CU),
+// a large last round done in halves 0.62. Measured at K 4096 with both operands in
+// 4 bits: 4096^2 (one full round) 47 against 54 us, 2047 x 4096 30.1 against 28.9,
+// 1024 x 4096 23.6 against 20.8, 1024 x 11008 39 against 43, 2047 x 11008 68
+// against 70; with bfloat16 A 61.8/65.0, 52.9/46.9, 92/97 and 155/174.
+static int choose_tile(const MxParams &p, bool dma, int cus)
+{
+    if (!dma || p.M < 256 || p.N < 256)
+        return MX_TILE_128;
+    const int64_t large = (int64_t)cdiv(p.M, 256) * cdiv(p.N, 256), small = (int64_t)cdiv(p.M, 128) * cdiv(p.N, 128);
+    auto rounds = [](int64_t tiles, int slots, int few, double cost_few, double cost) {
+        const int64_t last = tiles % slots;
+        return (double)(tiles / slots) * cost + (last == 0 ? 0.0 : last <= few ? cost_few : cost);
+    };
+    return rounds(large, cus, cus / 2, 0.62, 1.0) <= rounds(small, 2 * cus, cus, 0.5, 0.57) ? MX_TILE_256 : MX_TILE_128;
 }
 
 template <int A>
 static hipError_t launch_a(const MxParams &p, int cus, hipStream_t s)
 {
+    if (p.K < 32)
+        return launch_stream<A, 1, 1, 1, 4, false>(p, s);
     if (p.M <= 16)
-        return launch_stream<A, 1, 1, 1, 4>(p, s);
+        return launch_stream<A, 1, 1, A == MXA_MX4 ? 2 : 1, 8>(p, s);
+    // copies take rows of whole 16-byte pieces and 32-bit offsets within a tile
+    const bool dma = ((uintptr_t)p.A | (uintptr_t)p.B | (uintptr_t)p.lda | (uintptr_t)p.ldb) % 16 == 0 &&
+                     p.lda < 1 << 24 && p.ldb < 1 << 24 && p.ldsa < 1 << 24 && p.ldsb < 1 << 24;
+    if (p.M >= 128 && p.N >= 128 && p.K >= 512)
+        return launch_gemm_mx4_tile(p, A, choose_tile(p, dma, cus), dma, cus, s);
+    if (p.M <= 64)
+        return launch_stream<A, 2, 2, 1, 8>(p, s);
     return launch_stream<A, 4, 4, 1, 4>(p, s);
 }
 

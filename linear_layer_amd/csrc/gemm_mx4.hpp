@@ -1,0 +1,189 @@
+// Device code shared by the kernels of the products with a 4-bit microscaled
+// operand: the matrix instructions, the decoding of codes, checked loads and
+// the epilogue.
+#pragma once
+
+#include "launch.hpp"
+#include "lowp.hpp"
+#include "mx4.hpp"
+
+namespace ll {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// Byte BA of sa scales a, byte BB of sb scales b.
+template <int BA, int BB>
+__device__ __forceinline__ f32x4 mma_mx4(const u32x4 &a, const u32x4 &b, const f32x4 &c, int sa, int sb)
+{
+    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 y = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, y, c, 4, 4, BA, sa, BB, sb);
+}
+
+__device__ __forceinline__ f32x4 mma_f16(const u32x4 &a, const u32x4 &b, const f32x4 &c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c,
+                                                  0, 0, 0);
+}
+
+__device__ __forceinline__ f32x4 mma_bf16(const u32x4 &a, const u32x4 &b, const f32x4 &c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Eight codes (one dword) as 16-bit values; `sc` carries the scale byte in an
+// FP32 exponent field.
+template <bool BF16>
+__device__ __forceinline__ u32x4 decode8(uint32_t q, float sc)
+{
+    u32x4 r;
+    if constexpr (BF16) {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, sc, 3));
+    } else {
+        r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 0));
+        r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 1));
+        r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 2));
+        r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, sc, 3));
+    }
+    return r;
+}
+
+// Eight binary16 values as two bfloat16 parts, hi + lo exactly: hi is the
+// value's top 8 bits of fraction, the rest has 3. An infinity or a NaN stays
+// in hi alone.
+__device__ __forceinline__ void split8(const u32x4 &a, u32x4 &hi, u32x4 &lo)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float v = (float)__builtin_bit_cast(_Float16, (uint16_t)(a[j] >> (16 * e)));
+            const uint32_t b = __builtin_bit_cast(uint32_t, v), t = b & 0xffff0000u;
+            const float d = v - __builtin_bit_cast(float, t);
+            h[e] = t >> 16;
+            l[e] = (b & 0x7f800000u) == 0x7f800000u ? 0u : __builtin_bit_cast(uint32_t, d) >> 16;
+        }
+        hi[j] = h[0] | h[1] << 16;
+        lo[j] = l[0] | l[1] << 16;
+    }
+}
+
+// Turns a 4 x 4 matrix of dwords around, v[i] of the 16 lanes of group g being its
+// element (g, i): afterwards v[i] of group g is element (i, g).
+__device__ __forceinline__ void turn4(u32x4 &v)
+{
+    const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    v = u32x4{c[0], c[1], d[0], d[1]};
+}
+
+// Whether a scale byte keeps the decoded values exact in binary16.
+__device__ __forceinline__ bool f16_scale_ok(uint32_t s) { return s - 104u <= 36u; }
+
+// One value through the epilogue.
+__device__ __forceinline__ float finish(const MxParams &p, float v, const float *dst)
+{
+    return p.beta == 0.0f ? p.alpha * v : __builtin_fmaf(p.alpha, v, p.beta * *dst);
+}
+
+// Those columns lo .. hi-1 of four neighbouring ones through the epilogue (lo <= 0,
+// hi >= 4: all).
+__device__ __forceinline__ void finish4(const MxParams &p, const f32x4 &v, float *dst, int64_t lo, int64_t hi)
+{
+    if (lo <= 0 && hi >= 4) {
+        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (p.beta != 0.0f)
+            __builtin_memcpy(&o, dst, 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            o[j] = p.beta == 0.0f ? p.alpha * v[j] : __builtin_fmaf(p.alpha, v[j], p.beta * o[j]);
+        __builtin_memcpy(dst, &o, 16);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (j >= lo && j < hi)
+                dst[j] = finish(p, v[j], dst + j);
+    }
+}
+
+// Tile `id` of the order that walks tiles in groups of p.group_m tile rows,
+// column by column, so that the tiles in work at a time share rows and columns.
+__device__ __forceinline__ void mx_tile_of(const MxParams &p, int id, int &tm, int &tn)
+{
+    const int group = p.group_m * p.tiles_n;
+    const int first = id / group * p.group_m, within = id % group;
+    const int rows = min(p.tiles_m - first, p.group_m);
+    tm = first + within % rows;
+    tn = within / rows;
+}
+
+// The first `have` (1 .. 15) of 16 bytes of which they are the last; 0 behind them.
+__device__ __forceinline__ u32x4 last_bytes(const u32x4 &v, int have)
+{
+    const uint64_t lo = v[0] | (uint64_t)v[1] << 32, hi = v[2] | (uint64_t)v[3] << 32;
+    const int s = 8 * (16 - have);   // 8 .. 120
+    const uint64_t l = s >= 64 ? hi >> (s & 63) : lo >> s | hi << (64 - s), h = s >= 64 ? 0 : hi >> s;
+    return u32x4{(uint32_t)l, (uint32_t)(l >> 32), (uint32_t)h, (uint32_t)(h >> 32)};
+}
+
+// The 16 bytes of codes of block `blk` of a row of K values; values past K
+// are 0. Where a row has less than a block left, the last 16 bytes of it are
+// read and shifted (LONG: K >= 32), or it is read byte by byte.
+template <bool LONG>
+__device__ __forceinline__ u32x4 load_block(const uint8_t *row, int64_t blk, int K)
+{
+    const int64_t k = blk * kMxBlock;
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (k + kMxBlock <= K) {
+        v = load16<u32x4>(row + k / 2);
+    } else if (k < K) {
+        const int n = (int)(K - k), bytes = (n + 1) / 2;
+        if constexpr (LONG) {
+            v = load16<u32x4>(row + ((int64_t)K + 1) / 2 - 16);
+            if (n & 1)
+                v[3] &= 0x0fffffffu;
+            if (bytes < 16)
+                v = last_bytes(v, bytes);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (j < bytes) {
+                    const uint32_t b = row[k / 2 + j] & (2 * j + 1 < n ? 0xffu : 0x0fu);
+                    v[j / 4] |= b << (8 * (j % 4));
+                }
+            }
+        }
+    }
+    return v;
+}
+
+// 16-bit values k .. k+7 of a row of K; 0 past K (LONG: K >= 8).
+template <bool LONG>
+__device__ __forceinline__ u32x4 load_halves(const uint8_t *row, int64_t k, int K)
+{
+    u32x4 v = {0u, 0u, 0u, 0u};
+    if (k + 8 <= K) {
+        v = load16<u32x4>(row + 2 * k);
+    } else if (k < K) {
+        if constexpr (LONG) {
+            v = last_bytes(load16<u32x4>(row + 2 * ((int64_t)K - 8)), 2 * (int)(K - k));
+        } else {
+            const uint16_t *h = reinterpret_cast<const uint16_t *>(row) + k;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j < K)
+                    v[j / 2] |= (uint32_t)h[j] << (16 * (j % 2));
+        }
+    }
+    return v;
+}
+
+}  // namespace ll

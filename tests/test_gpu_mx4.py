@@ -318,3 +318,51 @@ def test_quantized_products_of_a_training_step():
         # a code is off by at most a quarter of its value (6 for 8) or a twelfth of
         # its block's largest: the products' relative distance stays below a half
         assert (C.double() - exact).norm() < 0.5 * exact.norm()
+
+
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("M,N,K,alpha,beta", [(2100, 4200, 544, 1.0, 0.0), (4100, 4200, 1057, 1.5, 0.5), (4352, 4096, 512, 1.0, 0.0)])
+def test_product_in_large_tiles(M, N, K, alpha, beta, which):
+    """Sizes that fill the chip with 256 x 256 tiles, the last ones in halves, a
+    half past the last row, and what K leaves past whole stages."""
+    check(which, M, N, K, alpha, beta, seed=12)
+
+
+@pytest.mark.parametrize("M,N,K,lo,hi", [(2100, 4200, 544, 90, 110), (300, 400, 777, 0, 40), (300, 400, 1024, 130, 160)])
+@pytest.mark.parametrize("pad", [0, 3])
+def test_product_f16_with_far_scales_in_some_blocks(M, N, K, lo, hi, pad):
+    """Scales past binary16 in a few blocks only: in the first or last panel of a
+    row, and in what K leaves past whole stages."""
+    r = rng(13)
+    args, av = a_operand("f16", r, M, K, 13 + 16 * pad, 0)
+    c, s = packed_case(r, N, K)
+    nb = s.shape[1]
+    for n, b in ((0, 0), (N // 2, nb // 2), (N - 1, nb - 1)):
+        s[n, b] = r.integers(lo, hi + 1)
+    bv = values(c, s, K)
+    C = torch.full((M, N), float("nan"), device=DEV)
+    product("f16", args, torch.as_tensor(c).to(DEV), torch.as_tensor(s).to(DEV), C, 1.0, 0.0, K)
+    want, size = av @ bv.T, np.abs(av) @ np.abs(bv).T
+    assert (np.abs(C.double().cpu().numpy() - want) <= (K + 8) * (HALF_STEP * size + 2.0 ** -126)).all()
+
+
+@pytest.mark.parametrize("which", WHICH)
+def test_product_nan_scales_in_large_products(which):
+    """NaN blocks in panels of scales: their rows and columns, and no others."""
+    M, N, K = 300, 400, 1100
+    r = rng(14)
+    c, s = packed_case(r, N, K)
+    args, av = a_operand(which, r, M, K, 4 if which == "mx4" else 0, 0)
+    cols, rows = [0, 127, 399], []
+    for n, b in zip(cols, (0, 20, s.shape[1] - 1)):
+        s[n, b] = 255
+    if which == "mx4":
+        rows = [1, 130, 299]
+        for m, b in zip(rows, (s.shape[1] - 1, 0, 17)):
+            args[1][m, b] = 255
+    C = torch.zeros((M, N), device=DEV)
+    product(which, args, torch.as_tensor(c).to(DEV), torch.as_tensor(s).to(DEV), C, 1.0, 0.0, K)
+    want = torch.zeros((M, N), dtype=torch.bool)
+    want[:, cols] = True
+    want[rows, :] = True
+    assert torch.equal(~torch.isfinite(C).cpu(), want)
