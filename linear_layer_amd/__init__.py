@@ -216,29 +216,37 @@ def chosen_stream_k(dtype: int, M: int, N: int, K: int, num_cus: int = 0, batch:
 
 # ---- tensor marshalling ---------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:   # (an import statement costs a few tenths of a microsecond a call)
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _mat(t, dtype, name):
     """(pointer, rows, cols, ld) of a 2-D row-major device tensor."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got shape {tuple(t.shape)}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError(f"{name} must have unit column stride (row-major)")
-    ld = t.stride(0) if rows > 1 else max(cols, 1)
-    if rows > 1 and ld < cols:
+    if rows <= 1:
+        ld = cols
+    elif ld < cols:
         raise ValueError(f"{name}: row stride {ld} smaller than width {cols}")
-    return t.data_ptr(), rows, cols, max(ld, 1)
+    return t.data_ptr(), rows, cols, ld if ld > 1 else 1
 
 
 def _bmat(t, dtype, name):
@@ -319,15 +327,15 @@ def _raw_getters():
 
 def _stream(stream, *tensors):
     if stream is None:
-        dev = tensors[0].device
-        for t in tensors[1:]:
-            if t is not None and t.device != dev:
+        dev = tensors[0].get_device()
+        for t in tensors:
+            if t is not None and t.get_device() != dev:
                 raise ValueError("all tensors must be on the same device")
         get_dev, get_raw = _raw_getters()
-        if get_dev() != dev.index:
-            raise ValueError(f"tensors are on {dev}, but the current device is cuda:{get_dev()}")
-        return ctypes.c_void_p(get_raw(dev.index))
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        if get_dev() != dev:
+            raise ValueError(f"tensors are on {tensors[0].device}, but the current device is cuda:{get_dev()}")
+        return get_raw(dev)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _gemm(fn_name, in_dtype, A, B, C, alpha, beta, stream, bt=False):
