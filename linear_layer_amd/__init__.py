@@ -459,6 +459,27 @@ def _linear(fn_name, X, W, bias, act, Y, stream, wt=False, ws=None):
     return Y
 
 
+_call_module = None
+
+
+def _short_calls():
+    """The module that takes tensors apart for the short calls below. Its functions
+    return a status, or None where an argument is not what the call takes; what is
+    wrong with it, if anything is, the Python code after the call finds."""
+    global _call_module
+    if _call_module is None:
+        load()
+        _torch()
+        try:
+            from . import _call as module
+        except ImportError as e:
+            raise ImportError("linear_layer_amd/_call.so is missing or does not load: build it with "
+                              "`python -m linear_layer_amd._build`") from e
+        module.setup(*_raw_getters())
+        _call_module = module
+    return _call_module
+
+
 # ---- microscaled 4-bit floating point ---------------------------------------
 
 def mx4_shapes(rows: int, K: int):
@@ -498,6 +519,11 @@ def mx4_quantize(X, codes, scales, trans: bool = False, stream=None):
     """Quantise X (float32, float16 or bfloat16; M x K) into uint8 codes and scales,
     along its rows, or with ``trans`` along its columns into the packed transposed
     matrix (K rows of M values). Returns (codes, scales)."""
+    if stream is None:
+        st = _short_calls().mx4_quantize(X, codes, scales, trans)
+        if st is not None:
+            _check(st, "mx4_quantize")
+            return codes, scales
     t = _type_of(X, "X")
     px, M, K, ldx = _mat(X, X.dtype, "X")
     rows, pq, ldq, ps, lds = _packed(codes, scales, M if trans else K, "X")
@@ -510,6 +536,11 @@ def mx4_quantize(X, codes, scales, trans: bool = False, stream=None):
 
 def mx4_dequantize(codes, scales, Y, stream=None):
     """Y (float32, float16 or bfloat16; M x K) = the values codes and scales stand for."""
+    if stream is None:
+        st = _short_calls().mx4_dequantize(codes, scales, Y)
+        if st is not None:
+            _check(st, "mx4_dequantize")
+            return Y
     t = _type_of(Y, "Y")
     py, M, K, ldy = _mat(Y, Y.dtype, "Y")
     rows, pq, ldq, ps, lds = _packed(codes, scales, K, "Y")
@@ -523,6 +554,11 @@ def mx4_dequantize(codes, scales, Y, stream=None):
 def gemm_mx4f32_nt(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, K: int | None = None, stream=None):
     """C = alpha*A*B^T + beta*C with A (M x K) and B (N x K) as uint8 codes and scales;
     K is twice the codes' width unless given (an odd K has to be)."""
+    if stream is None:
+        st = _short_calls().gemm_mx4f32_nt(A, SA, B, SB, C, alpha, beta, K)
+        if st is not None:
+            _check(st, "gemm_mx4f32_nt")
+            return C
     torch = _torch()
     if K is None:
         K = 2 * A.shape[1] if getattr(A, "ndim", 0) == 2 else 0
@@ -538,6 +574,12 @@ def gemm_mx4f32_nt(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, K: in
 
 
 def _gemm_16mx4(fn_name, in_dtype, A, B, SB, C, alpha, beta, stream):
+    if stream is None:
+        st = getattr(_short_calls(), fn_name)(A, B, SB, C, alpha, beta)
+        if st is not None:
+            _check(st, fn_name)
+            return C
+    in_dtype = getattr(_torch(), in_dtype)
     torch = _torch()
     pa, M, K, lda = _mat(A, in_dtype, "A")
     N, pb, ldb, psb, ldsb = _packed(B, SB, K, "B")
@@ -551,12 +593,12 @@ def _gemm_16mx4(fn_name, in_dtype, A, B, SB, C, alpha, beta, stream):
 
 def gemm_f16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     """C = alpha*A*B^T + beta*C with fp16 A and B (N x K) as uint8 codes and scales."""
-    return _gemm_16mx4("gemm_f16mx4f32_nt", _torch().float16, A, B, SB, C, alpha, beta, stream)
+    return _gemm_16mx4("gemm_f16mx4f32_nt", "float16", A, B, SB, C, alpha, beta, stream)
 
 
 def gemm_bf16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     """C = alpha*A*B^T + beta*C with bf16 A and B (N x K) as uint8 codes and scales."""
-    return _gemm_16mx4("gemm_bf16mx4f32_nt", _torch().bfloat16, A, B, SB, C, alpha, beta, stream)
+    return _gemm_16mx4("gemm_bf16mx4f32_nt", "bfloat16", A, B, SB, C, alpha, beta, stream)
 
 
 # ---- residual norms ------------------------------------------------------------
@@ -587,6 +629,11 @@ def rmsnorm_residual(Y, w_post, gate, alpha, X, w_pre, XO, H, eps: float = 1e-5,
     """XO = X + alpha*gate*rms(Y)*w_post and H = rms(XO)*w_pre over the rows, rms(v) =
     v / sqrt(mean(v^2) + eps). Y is fp32, X, XO and H of one type; Y, the vectors and
     one of XO and H may be None. XO may be X. Returns (XO, H)."""
+    if stream is None:
+        st = _short_calls().rmsnorm_residual(Y, w_post, gate, alpha, X, w_pre, XO, H, eps)
+        if st is not None:
+            _check(st, "rmsnorm_residual")
+            return XO, H
     torch = _torch()
     t = _type_of(X, "X")
     px, M, N, ldx = _mat(X, X.dtype, "X")
@@ -613,6 +660,12 @@ def rmsnorm_residual_grad(DXO, DH, Y, w_post, gate, alpha, X, w_pre, DY, DX, dga
     and H; DY, DX, dgate, dw_post and dw_pre are written (each may be None). workspace:
     a contiguous device tensor of rmsnorm_grad_workspace_size(M, N) bytes or more.
     Returns (DY, DX, dgate, dw_post, dw_pre)."""
+    if stream is None:
+        st = _short_calls().rmsnorm_residual_grad(DXO, DH, Y, w_post, gate, alpha, X, w_pre, DY, DX, dgate, dw_post, dw_pre,
+                                           workspace, eps)
+        if st is not None:
+            _check(st, "rmsnorm_residual_grad")
+            return DY, DX, dgate, dw_post, dw_pre
     torch = _torch()
     t = _type_of(X, "X")
     px, M, N, ldx = _mat(X, X.dtype, "X")

@@ -1,4 +1,5 @@
-"""Build liblinear_layer.so (the C-ABI library) for gfx950 with hipcc, in-tree.
+"""Build liblinear_layer.so (the C-ABI library) for gfx950 with hipcc, and the Python
+module _call.so on top of it with the host compiler, in-tree.
 
 Usage: ``python -m linear_layer_amd._build``. Cross-compiles without a GPU.
 """
@@ -14,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "liblinear_layer.so")
+CALL = os.path.join(PKG, "_call.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "gemm_f32.hip", "gemm_f32_nt.hip", "gemm_f16.hip", "elementwise.hip",
@@ -38,6 +40,24 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_call() -> None:
+    """The module that takes tensors apart for the short calls (csrc/call.cpp)."""
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = CALL + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           os.path.join(CSRC, "call.cpp"), "-o", tmp, "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
+           "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-L", PKG, "-l:liblinear_layer.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath," + os.path.join(torch, "lib")]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"building _call.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALL)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     jobs = min(len(SOURCES), os.cpu_count() or 4, 16)
@@ -49,8 +69,10 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_call()
     if verbose:
         print("built", LIB)
+        print("built", CALL)
     return LIB
 
 
