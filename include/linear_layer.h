@@ -381,7 +381,7 @@ int rmsnorm_residual_grad(int M, int N, int type, const void *DXO, int lddxo, co
                           float *dgate, float *dw_post, float *dw_pre,
                           void *workspace, int64_t workspace_bytes, void *stream);
 /* Bytes of workspace rmsnorm_residual_grad needs (at most 8 * 512 * N for N up
- * to 16384); -1 for a negative size. */
+ * to 8192); -1 for a negative size. */
 int64_t ll_rmsnorm_grad_workspace_size(int M, int N);
 
 /* A static, human-readable string for a status code (never NULL). */

@@ -41,6 +41,48 @@ __device__ __forceinline__ typename Elem<TYPE>::type from_f32(float v)
         return __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// Eight values of a row from `src` on as they stand in memory, the first n of them
+// inside it (n >= 8: all) and the others 0; all 0 where src is null. Whole groups
+// take 16-byte loads at any alignment.
+template <int TYPE, int P>
+__device__ __forceinline__ void raw_row(const typename Elem<TYPE>::type *src, int64_t n, u32x4 (&v)[P])
+{
+    using T = typename Elem<TYPE>::type;
+    constexpr int PER = 16 / (int)sizeof(T);
+    static_assert(P * PER == 8, "eight values");
+    if (src != nullptr && n >= 8) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+            v[i] = load16<u32x4>(src + i * PER);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        v[i] = u32x4{0u, 0u, 0u, 0u};
+    if (src == nullptr)
+        return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j < n) {
+            uint32_t w = 0;
+            __builtin_memcpy(&w, src + j, sizeof(T));
+            v[j / PER][j % PER * (int)sizeof(T) / 4] |= w << (8 * (j * (int)sizeof(T) % 4));
+        }
+}
+
+template <int TYPE, int P>
+__device__ __forceinline__ void raw_values(const u32x4 (&raw)[P], float (&v)[8])
+{
+    constexpr int PER = 8 / P;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if constexpr (TYPE == LL_TYPE_F32)
+            v[j] = __uint_as_float(raw[j / PER][j % PER]);
+        else
+            v[j] = to_f32<TYPE>((uint16_t)(raw[0][j / 2] >> (16 * (j & 1))));
+    }
+}
+
 // E values of a row from `src` on, the first n of them inside it (n >= E: all);
 // the others are 0. Whole groups take 16-byte loads at any alignment.
 template <int TYPE, int E>

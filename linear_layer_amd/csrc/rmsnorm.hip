@@ -73,7 +73,9 @@ __device__ __forceinline__ void load_vec(const float *v, int64_t c, int64_t n, f
 // A thread holds C groups of 8 neighbouring values, 8 * NT columns apart.
 // LONG: rows longer than 8 * NT * C, walked in several passes over memory,
 // each sum in passes of its own.
-template <int TYPE, int NT, int C, bool LONG>
+// EARLY: the vectors are read with the row, not where they are used: with few rows
+// nothing else hides their latency (4 x 4096 binary16 4.9 -> 4.0 us).
+template <int TYPE, int NT, int C, bool LONG, bool EARLY>
 __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
 {
     using T = typename Elem<TYPE>::type;
@@ -96,8 +98,19 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
             }
         };
         float ry = 0.0f;
+        float ew[EARLY ? C : 1][8], eg[EARLY ? C : 1][8], ep[EARLY ? C : 1][8];
+        static_assert(!EARLY || !LONG, "one pass");
         if (!LONG)
             load(0);
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+                load_vec<8>(p.w_post, col, N, 1.0f, ew[c]);
+                load_vec<8>(p.gate, col, N, 1.0f, eg[c]);
+                load_vec<8>(p.w_pre, col, N, 1.0f, ep[c]);
+            }
+        }
         if (y != nullptr) {
             float s[1] = {0.0f};
             for (int pass = 0; pass < passes; ++pass) {
@@ -121,8 +134,14 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
                     continue;
                 if (y != nullptr) {
                     float w[8], g[8];
-                    load_vec<8>(p.w_post, col, N, 1.0f, w);
-                    load_vec<8>(p.gate, col, N, 1.0f, g);
+                    if constexpr (EARLY) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            w[j] = ew[c][j], g[j] = eg[c][j];
+                    } else {
+                        load_vec<8>(p.w_post, col, N, 1.0f, w);
+                        load_vec<8>(p.gate, col, N, 1.0f, g);
+                    }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         xv[c][j] = __builtin_fmaf(p.alpha * g[j], yv[c][j] * ry * w[j], xv[c][j]);
@@ -158,7 +177,13 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
                 if (col >= N)
                     continue;
                 float w[8];
-                load_vec<8>(p.w_pre, col, N, 1.0f, w);
+                if constexpr (EARLY) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = ep[c][j];
+                } else {
+                    load_vec<8>(p.w_pre, col, N, 1.0f, w);
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     xv[c][j] = xv[c][j] * rx * w[j];
@@ -173,20 +198,26 @@ static hipError_t norm_t(const NormParams &p, hipStream_t s)
 {
     const int64_t most = 1 << 20;
     const dim3 grid((unsigned)(p.M < most ? p.M : most));
-#define LL_NORM(NT, C, LONG) \
-    hipLaunchKernelGGL((rmsnorm_residual_kernel<TYPE, NT, C, LONG>), grid, dim3(NT), 0, s, p)
+#define LL_NORM(NT, C, LONG, EARLY) \
+    hipLaunchKernelGGL((rmsnorm_residual_kernel<TYPE, NT, C, LONG, EARLY>), grid, dim3(NT), 0, s, p)
+    // few rows: a thread to 8 columns and every load at once
+    const bool few = p.M <= 512;
     if (p.N <= 512)
-        LL_NORM(64, 1, false);
+        LL_NORM(64, 1, false, true);
     else if (p.N <= 2048)
-        LL_NORM(256, 1, false);
+        LL_NORM(256, 1, false, true);
+    else if (p.N <= 4096 && few)
+        LL_NORM(512, 1, false, true);
     else if (p.N <= 4096)
-        LL_NORM(256, 2, false);
+        LL_NORM(256, 2, false, false);
+    else if (p.N <= 8192 && few)
+        LL_NORM(1024, 1, false, true);
     else if (p.N <= 8192)
-        LL_NORM(512, 2, false);
+        LL_NORM(512, 2, false, false);
     else if (p.N <= 16384)
-        LL_NORM(1024, 2, false);
+        LL_NORM(1024, 2, false, false);
     else
-        LL_NORM(1024, 1, true);
+        LL_NORM(1024, 1, true, false);
 #undef LL_NORM
     return hipGetLastError();
 }
@@ -206,17 +237,22 @@ hipError_t launch_rmsnorm_residual(int type, const NormParams &p, hipStream_t s)
 // columns' shares of S and of dw_pre's sum; it writes them once, as row
 // blockIdx.x of `part` ([grid][2][N] floats), and a second launch adds the
 // rows in order. No atomics: the result does not depend on the run.
-
-template <int TYPE, int NT, int C>
-__global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradParams p)
+//
+// TEAMS: rows so short that one wave holds one are taken by TEAMS waves of a
+// workgroup, a row each, and their shares added in wave order at the end
+// (8192 x 512 bfloat16 39 -> 20 us).
+template <int TYPE, int NT, int C, int TEAMS>
+__global__ void __launch_bounds__(NT * TEAMS) rmsnorm_grad_kernel(NormGradParams p)
 {
     using T = typename Elem<TYPE>::type;
+    static_assert(TEAMS == 1 || (NT == 64 && C == 1), "a team is a wave: its sums need no barrier");
     __shared__ float lds[2 * (NT / 64)];
-    const int N = p.N;
+    const int N = p.N, tid = threadIdx.x % NT;
+    const int64_t stride = (int64_t)gridDim.x * TEAMS, first = (int64_t)blockIdx.x * TEAMS + threadIdx.x / NT;
     float sS[C][8], sP[C][8], t[C][8], wp[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+        const int64_t col = 8 * ((int64_t)c * NT + tid);
         float g[8];
         load_vec<8>(p.w_post, col, N, 1.0f, t[c]);
         load_vec<8>(p.gate, col, N, 1.0f, g);
@@ -227,30 +263,38 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradParams p)
             t[c][j] *= p.alpha * g[j];
         }
     }
-    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    // The next row is on its way while this one is worked on, since the sums have
+    // to wait for one another and the loads for nothing but memory (16-bit
+    // 8191 x 4096 128 -> 108 us, 4.9 TB/s; a large copy reaches 5.1 to 5.5).
+    constexpr int RAW = 8 / (16 / (int)sizeof(T));   // 16-byte pieces of 8 values
+    u32x4 ry4[C][2], rx4[C][RAW], rd4[C][RAW], rk4[C][RAW];
+    auto fetch = [&](int64_t m) __attribute__((always_inline)) {
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int64_t col = 8 * ((int64_t)c * NT + tid);
+            raw_row<LL_TYPE_F32>(p.Y != nullptr ? p.Y + m * p.ldy + col : nullptr, N - col, ry4[c]);
+            raw_row<TYPE>(static_cast<const T *>(p.X) + m * p.ldx + col, N - col, rx4[c]);
+            raw_row<TYPE>(p.DXO != nullptr ? static_cast<const T *>(p.DXO) + m * p.lddxo + col : nullptr, N - col, rd4[c]);
+            raw_row<TYPE>(p.DH != nullptr ? static_cast<const T *>(p.DH) + m * p.lddh + col : nullptr, N - col, rk4[c]);
+        }
+    };
+    if (first < p.M)
+        fetch(first);
+    for (int64_t m = first; m < p.M; m += stride) {
         float yv[C][8], xv[C][8], dv[C][8], kv[C][8];
         float s[1] = {0.0f};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
-            if (p.Y != nullptr)
-                load_row<LL_TYPE_F32, 8>(p.Y + m * p.ldy + col, N - col, yv[c]);
-            load_row<TYPE, 8>(static_cast<const T *>(p.X) + m * p.ldx + col, N - col, xv[c]);
-            if (p.DXO != nullptr)
-                load_row<TYPE, 8>(static_cast<const T *>(p.DXO) + m * p.lddxo + col, N - col, dv[c]);
-            if (p.DH != nullptr)
-                load_row<TYPE, 8>(static_cast<const T *>(p.DH) + m * p.lddh + col, N - col, kv[c]);
+            raw_values<LL_TYPE_F32>(ry4[c], yv[c]);
+            raw_values<TYPE>(rx4[c], xv[c]);
+            raw_values<TYPE>(rd4[c], dv[c]);
+            raw_values<TYPE>(rk4[c], kv[c]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (p.Y == nullptr)
-                    yv[c][j] = 0.0f;
-                if (p.DXO == nullptr)
-                    dv[c][j] = 0.0f;
-                if (p.DH == nullptr)
-                    kv[c][j] = 0.0f;
+            for (int j = 0; j < 8; ++j)
                 s[0] = __builtin_fmaf(yv[c][j], yv[c][j], s[0]);
-            }
         }
+        if (m + stride < p.M)
+            fetch(m + stride);
         block_sum<NT>(s, lds);
         const float ry = inv_rms(s[0], N, p.eps);
         float q[2] = {0.0f, 0.0f};   // sums of x'^2 and of dh * w_pre * x'
@@ -280,7 +324,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradParams p)
         const float mean_z = z[0] / (float)N;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+            const int64_t col = 8 * ((int64_t)c * NT + tid);
             if (col >= N)
                 continue;
             if (p.DX != nullptr)
@@ -292,9 +336,24 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_kernel(NormGradParams p)
                 store_row<LL_TYPE_F32, 8>(p.DY + m * p.lddy + col, N - col, dv[c]);
         }
     }
+    if constexpr (TEAMS > 1) {
+        __shared__ float shares[TEAMS][2][8 * NT + 8];
+        float(*mine)[8 * NT + 8] = shares[threadIdx.x / NT];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            mine[0][j * NT + tid] = sS[0][j], mine[1][j * NT + tid] = sP[0][j];
+        __syncthreads();
+        if (threadIdx.x >= NT)
+            return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int w = 1; w < TEAMS; ++w)
+                sS[0][j] += shares[w][0][j * NT + tid], sP[0][j] += shares[w][1][j * NT + tid];
+    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-        const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
+        const int64_t col = 8 * ((int64_t)c * NT + tid);
         if (col >= N)
             continue;
         float *row = p.part + (int64_t)blockIdx.x * 2 * N + col;
@@ -422,41 +481,56 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_cols_kernel(NormGradParams p
     store_row<LL_TYPE_F32, 8>(row + p.N, p.N - col, sP);
 }
 
-// The columns' sums over `rows` partial rows, then dgate, dw_post and dw_pre.
-// 64 columns to a workgroup; its 16 waves take every 16th row, and their sums
-// are added in wave order.
-__global__ void __launch_bounds__(1024) rmsnorm_grad_finish_kernel(NormGradParams p, int rows)
+// The columns' sums over `rows` partial rows, then dgate, dw_post and dw_pre. A
+// workgroup takes 16 columns; its threads, 4 quads of columns by 64, every 64th row,
+// 8 of them in flight, and their sums are added in a fixed order (16 MB of 512
+// partial rows of 4096: 8 us, with 32 columns to a workgroup 11).
+__global__ void __launch_bounds__(256) rmsnorm_grad_finish_kernel(NormGradParams p, int rows)
 {
-    __shared__ float sums[2][16][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t col = (int64_t)blockIdx.x * 64 + lane;
-    float a = 0.0f, b = 0.0f;
-    if (col < p.N)
-        for (int r = wave; r < rows; r += 16) {
-            a += p.part[(int64_t)r * 2 * p.N + col];
-            b += p.part[(int64_t)r * 2 * p.N + p.N + col];
-        }
-    sums[0][wave][lane] = a;
-    sums[1][wave][lane] = b;
-    __syncthreads();
-    if (wave != 0 || col >= p.N)
-        return;
-    a = b = 0.0f;
+    __shared__ float sums[64][2][16 + 1];
+    const int quad = threadIdx.x & 3, r0 = threadIdx.x >> 2;
+    const int64_t col = (int64_t)blockIdx.x * 16 + 4 * quad, left = p.N - col;
+    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (left > 0) {
+        for (int r = r0; r < rows; r += 512) {
+            float u[8][4], v[8][4];
 #pragma unroll
-    for (int w = 0; w < 16; ++w) {
-        a += sums[0][w][lane];
-        b += sums[1][w][lane];
+            for (int i = 0; i < 8; ++i) {
+                const float *row = p.part + (int64_t)(r + 64 * i) * 2 * p.N + col;
+                const int64_t n = r + 64 * i < rows ? left : 0;
+                load_row<LL_TYPE_F32, 4>(row, n, u[i]);
+                load_row<LL_TYPE_F32, 4>(row + p.N, n, v[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a[j] += u[i][j], b[j] += v[i][j];
+        }
     }
-    if (p.DGATE != nullptr)
-        p.DGATE[col] = p.alpha * (p.w_post != nullptr ? p.w_post[col] : 1.0f) * a;
-    if (p.DWPOST != nullptr)
-        p.DWPOST[col] = p.alpha * (p.gate != nullptr ? p.gate[col] : 1.0f) * a;
-    if (p.DWPRE != nullptr)
-        p.DWPRE[col] = b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sums[r0][0][4 * quad + j] = a[j], sums[r0][1][4 * quad + j] = b[j];
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
+    const int which = threadIdx.x >> 4;
+    if (which > 1 || c >= p.N)
+        return;
+    float t = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 64; ++r)
+        t += sums[r][which][threadIdx.x & 15];
+    if (which == 0 && p.DGATE != nullptr)
+        p.DGATE[c] = p.alpha * (p.w_post != nullptr ? p.w_post[c] : 1.0f) * t;
+    if (which == 0 && p.DWPOST != nullptr)
+        p.DWPOST[c] = p.alpha * (p.gate != nullptr ? p.gate[c] : 1.0f) * t;
+    if (which == 1 && p.DWPRE != nullptr)
+        p.DWPRE[c] = t;
 }
 
-// Rows the registers of 1024 threads hold.
-constexpr int kGradRegCols = 16384;
+// Rows that the registers of a workgroup hold, this one and the next (with 16384 in
+// 1024 threads they spill: 4096 x 16384 bfloat16 502 us against 462 in two launches).
+constexpr int kGradRegCols = 8192;
 // Workgroups (rows of partial sums) of a gradient: two for each CU.
 constexpr int kGradGroups = 512;
 
@@ -477,19 +551,18 @@ static hipError_t norm_grad_t(NormGradParams p, void *ws, hipStream_t s)
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + grad_stats_bytes(p.M, p.N));
     const int groups = grad_groups(p.M);
     const dim3 grid((unsigned)groups);
-#define LL_GRAD(NT, C) hipLaunchKernelGGL((rmsnorm_grad_kernel<TYPE, NT, C>), grid, dim3(NT), 0, s, p)
+#define LL_GRAD(NT, C, TEAMS) \
+    hipLaunchKernelGGL((rmsnorm_grad_kernel<TYPE, NT, C, TEAMS>), grid, dim3(NT * TEAMS), 0, s, p)
     if (p.M <= 0)
         ;   // no rows: the finishing launch writes zeros
     else if (p.N <= 512)
-        LL_GRAD(64, 1);
+        LL_GRAD(64, 1, 4);
     else if (p.N <= 2048)
-        LL_GRAD(256, 1);
+        LL_GRAD(256, 1, 1);
     else if (p.N <= 4096)
-        LL_GRAD(256, 2);
-    else if (p.N <= 8192)
-        LL_GRAD(1024, 1);
+        LL_GRAD(256, 2, 1);
     else if (p.N <= kGradRegCols)
-        LL_GRAD(1024, 2);
+        LL_GRAD(512, 2, 1);
     else {
         RowStats *stats = static_cast<RowStats *>(ws);
         const int slab = 1 << 20;   // rows of a launch: work items fit 32 bits
@@ -510,7 +583,7 @@ static hipError_t norm_grad_t(NormGradParams p, void *ws, hipStream_t s)
     }
 #undef LL_GRAD
     if (p.DGATE != nullptr || p.DWPOST != nullptr || p.DWPRE != nullptr)
-        hipLaunchKernelGGL(rmsnorm_grad_finish_kernel, dim3((unsigned)(((int64_t)p.N + 63) / 64)), dim3(1024), 0, s,
+        hipLaunchKernelGGL(rmsnorm_grad_finish_kernel, dim3((unsigned)(((int64_t)p.N + 15) / 16)), dim3(256), 0, s,
                            p, groups);
     return hipGetLastError();
 }
