@@ -250,6 +250,189 @@ static hipError_t launch_stream(MxParams p, hipStream_t s)
     return hipGetLastError();
 }
 
+// LDS of the row kernel: bytes of a plane of A (a piece of 8 values of every block
+// of a row, whole turns of 64 blocks; 64 bytes past a multiple of 256, so that the
+// pieces of a block lie on different banks), and in all.
+__host__ __device__ constexpr int rows_plane(int nblk) { return (nblk + 63) / 64 * 1024 + 64; }
+constexpr int rows_planes(int a) { return a == MXA_MX4 ? 1 : a == MXA_F16 ? 8 : 4; }
+constexpr int64_t rows_lds(int a, int64_t K)
+{
+    const int64_t nblk = (K + kMxBlock - 1) / kMxBlock;
+    return rows_planes(a) * ((nblk + 63) / 64 * 1024 + 64) + (a == MXA_MX4 ? (nblk + 63) / 64 * 64 : 0);
+}
+
+// ---------------------------------------------------------------------------
+// Row kernel, for a decode step's one row of A: HBM bounds it, and
+// memory serves whole rows better than the streaming kernel's 64 bytes of 16 (B
+// 28672 x 8192 in 4 bits both 24.5 us, 5.1 TB/s, against 32.4; with bfloat16 A 24.7
+// against 41.0; B 11008 x 4096 6.6 and 7.4 us against 9.2 and 10.9). A wave takes R rows of B, 64 blocks of
+// one at a time: lane l block l, a load of 1 KiB. The matrix instruction then has for
+// its 16 rows of B 16 sets of four blocks of the same row, and for its 16 rows of A
+// the same sets of A's: the sum of its result's diagonal is their inner
+// product. What it computes beside the diagonal is not used; it still takes 16
+// cycles (64 with 16-bit A, 128 with binary16) for a KiB of codes, more than four
+// times HBM's rate.
+// A lies in LDS as the instruction takes it: codes, or [piece of 8 values][block], so
+// that neighbouring lanes read neighbouring 16 bytes. binary16 is split into two
+// bfloat16 parts there (see split8), exact whatever the scales.
+// KW waves of a workgroup share rows, and NW such groups take rows of their own.
+// (With two rows of A it was no faster than the streaming kernel, with four slower.)
+template <int A, int R, int KW, int NW>
+__global__ void __launch_bounds__(64 * KW * NW) gemm_mx4_rows_kernel(MxParams p)
+{
+    constexpr bool MX = A == MXA_MX4;
+    constexpr int NT = 64 * KW * NW, PL = rows_planes(A);
+    extern __shared__ __attribute__((aligned(16))) uint8_t as[];
+    __shared__ float sums[KW > 1 ? KW * NW : 1][R];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = p.K, nblk = (K - 1) / kMxBlock + 1, padded = (nblk + 63) & ~63;
+    const int plane = rows_plane(nblk);
+    uint8_t *const scales = as + PL * plane;   // MX: `padded` bytes
+    const int64_t n0 = ((int64_t)block_index(blockIdx.x, gridDim.x) * NW + wave / KW) * R;
+
+    const uint8_t *brow[R], *sbrow[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const int64_t n = n0 + i < p.N ? n0 + i : p.N - 1;
+        brow[i] = p.B + n * p.ldb;
+        sbrow[i] = p.SB + n * p.ldsb;
+    }
+    // blocks past the row: codes 0 under scale 1
+    struct Unit {
+        u32x4 q[R];
+        uint32_t s[R];
+    };
+    auto fetch = [&](Unit &u, int blk) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            u.q[i] = u32x4{0u, 0u, 0u, 0u};
+            u.s[i] = 127u;
+        }
+        if (blk < K / kMxBlock) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                u.q[i] = load16<u32x4>(brow[i] + (int64_t)blk * 16);
+        } else if (blk < nblk) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                u.q[i] = load_block<true>(brow[i], blk, K);
+        }
+        if (blk < nblk) {
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                u.s[i] = sbrow[i][blk];
+        }
+    };
+    constexpr int STEP = 64 * KW;   // blocks of a turn
+    const int first = wave % KW * 64;
+    Unit u0, u1;
+    fetch(u0, first + lane);
+    fetch(u1, first + STEP + lane);
+
+    // A into LDS; 0 past its row
+    if constexpr (MX) {
+        for (int b = tid; b < padded; b += NT) {
+            *reinterpret_cast<u32x4 *>(as + b * 16) = load_block<true>(p.A, b, K);
+            scales[b] = b < nblk ? p.SA[b] : (uint8_t)127;
+        }
+    } else {
+        for (int c = tid; c < 4 * padded; c += NT) {
+            const u32x4 v = load_halves<true>(p.A, (int64_t)c * 8, K);
+            uint8_t *at = as + (c & 3) * plane + (c >> 2) * 16;
+            if constexpr (A == MXA_F16) {
+                u32x4 hi, lo;
+                split8(v, hi, lo);
+                *reinterpret_cast<u32x4 *>(at) = hi;
+                *reinterpret_cast<u32x4 *>(at + 4 * plane) = lo;
+            } else {
+                *reinterpret_cast<u32x4 *>(at) = v;
+            }
+        }
+    }
+    __syncthreads();
+
+    f32x4 acc[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+        acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](const Unit &u, int blk) __attribute__((always_inline)) {
+        if constexpr (MX) {
+            const u32x4 a = *reinterpret_cast<const u32x4 *>(as + blk * 16);
+            const int sa = scales[blk];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                acc[i] = mma_mx4<0, 0>(a, u.q[i], acc[i], sa, (int)u.s[i]);
+        } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                u32x4 a[PL / 4];
+#pragma unroll
+                for (int h = 0; h < PL / 4; ++h)
+                    a[h] = *reinterpret_cast<const u32x4 *>(as + (4 * h + t) * plane + blk * 16);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const u32x4 b = decode8<true>(u.q[i][t], __uint_as_float(u.s[i] << 23));
+#pragma unroll
+                    for (int h = PL / 4 - 1; h >= 0; --h)
+                        acc[i] = mma_bf16(a[h], b, acc[i]);
+                }
+            }
+        }
+    };
+    for (int base = first; base < nblk;) {
+        multiply(u0, base + lane);
+        if (base + 2 * STEP < nblk)
+            fetch(u0, base + 2 * STEP + lane);
+        base += STEP;
+        if (base >= nblk)
+            break;
+        multiply(u1, base + lane);
+        if (base + 2 * STEP < nblk)
+            fetch(u1, base + 2 * STEP + lane);
+        base += STEP;
+    }
+
+    // the diagonal: lane l has column l % 16 and rows 4 * (l / 16) .. +3
+    const int r16 = lane & 15;
+    const bool mine = (r16 >> 2) == lane >> 4;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        const f32x4 d = acc[i];
+        const float e = (r16 & 2) ? ((r16 & 1) ? d[3] : d[2]) : ((r16 & 1) ? d[1] : d[0]);
+        float v = dpp_row_sum16(mine ? e : 0.0f);
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        if constexpr (KW > 1) {
+            if (lane == 0)
+                sums[wave][i] = v;
+        } else if (lane == i && n0 + i < p.N) {
+            p.C[n0 + i] = finish(p, v, p.C + n0 + i);
+        }
+    }
+    if constexpr (KW > 1) {
+        __syncthreads();
+        if (wave % KW == 0 && lane < R && n0 + lane < p.N) {
+            float v = sums[wave][lane];
+#pragma unroll
+            for (int k = 1; k < KW; ++k)
+                v += sums[wave + k][lane];
+            p.C[n0 + lane] = finish(p, v, p.C + n0 + lane);
+        }
+    }
+}
+
+template <int A, int R, int KW, int NW>
+static hipError_t launch_rows(const MxParams &p, hipStream_t s)
+{
+    const int64_t groups = ((int64_t)p.N + R * NW - 1) / (R * NW);
+    if (groups > max_grid_x(64 * KW * NW))
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((gemm_mx4_rows_kernel<A, R, KW, NW>), dim3((unsigned)groups), dim3(64 * KW * NW),
+                       (unsigned)rows_lds(A, p.K), s, p);
+    return hipGetLastError();
+}
+
 // Which tile: 256 x 256, one to a CU, or 128 x 128, two to a CU, in rounds. A round
 // of the small one takes 0.57 of the large one's time (0.5 with one tile to a CU),
 // a large last round done in halves 0.62. Measured at K 4096 with both operands in
@@ -273,6 +456,10 @@ static hipError_t launch_a(const MxParams &p, int cus, hipStream_t s)
 {
     if (p.K < 32)
         return launch_stream<A, 1, 1, 1, 4, false>(p, s);
+    // one row of A (its LDS copy within 60 KiB): two waves to a row of B where the
+    // rows are long and few (4096 x 11008 6.9 against 7.4 us, 512 x 11008 4.4 against 5.7)
+    if (p.M == 1 && p.K >= 512 && rows_lds(A, p.K) <= 61440)
+        return p.K > 2 * (int64_t)p.N ? launch_rows<A, 2, 2, 4>(p, s) : launch_rows<A, 2, 1, 8>(p, s);
     if (p.M <= 16)
         return launch_stream<A, 1, 1, A == MXA_MX4 ? 2 : 1, 8>(p, s);
     // copies take rows of whole 16-byte pieces and 32-bit offsets within a tile

@@ -366,3 +366,34 @@ def test_product_nan_scales_in_large_products(which):
     want[:, cols] = True
     want[rows, :] = True
     assert torch.equal(~torch.isfinite(C).cpu(), want)
+
+
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("N,K", [(1, 512), (7, 2048), (33, 2049), (300, 4127), (17, 11008), (5, 12001), (3, 40000), (2, 70000)])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (3, 1)])
+def test_product_of_one_row(N, K, pad, shift, which):
+    """One row of A: whole turns of 64 blocks and what is left of them, a last block
+    cut short, rows of B shared by two waves, A too long for a workgroup's memory."""
+    check(which, 1, N, K, 1.0, 0.5 if shift else 0.0, pad, shift, seed=15)
+
+
+@pytest.mark.parametrize("which", WHICH)
+def test_one_row_with_far_scales_and_non_finite_values(which):
+    """Every scale byte; an infinity and a NaN of A reach every column, a NaN block of
+    B its own column and no other."""
+    N, K = 40, 64 * 32 * 3 + 40
+    check(which, 1, N, K, lo=0, hi=60, seed=16)
+    check(which, 1, N, K, lo=200, hi=230, seed=17)
+    r = rng(18)
+    c, s = packed_case(r, N, K)
+    s[3, 70], s[4, s.shape[1] - 1] = 255, 255
+    args, av = a_operand(which, r, 1, K, 0, 0)
+    C = torch.zeros((1, N), device=DEV)
+    product(which, args, torch.as_tensor(c).to(DEV), torch.as_tensor(s).to(DEV), C, 1.0, 0.0, K)
+    want = torch.zeros(N, dtype=torch.bool)
+    want[3], want[4] = True, True
+    assert torch.equal(torch.isnan(C[0]).cpu(), want)
+    if which != "mx4":
+        args[0][0, 65] = float("inf")
+        product(which, args, torch.as_tensor(c).to(DEV), torch.as_tensor(s).to(DEV), C, 1.0, 0.0, K)
+        assert not bool(torch.isfinite(C).any())
