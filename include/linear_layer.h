@@ -321,10 +321,9 @@ int mx4_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
  * Other arguments, rules and errors as gemm_f32: with beta == 0 C is not
  * read, K == 0 or alpha == 0 gives C = beta*C and reads neither operand, C
  * must not overlap an input. One launch, nothing allocated; the summation
- * order is fixed by the shape, so equal calls give equal results.
- * Rows (of A, of B) 16 bytes aligned, with K a multiple of 32, take the
- * direct-to-LDS tile kernels when the product is large; other operands are
- * streamed through registers at any alignment.
+ * order is fixed by the shape and the alignment, so equal calls give equal
+ * results. Rows (of A, of B) 16 bytes aligned take direct copies into LDS when
+ * the product is large; any other alignment is taken too.
  */
 int gemm_mx4f32_nt(int M, int N, int K, float alpha,
                    const uint8_t *A, int lda, const uint8_t *SA, int ldsa,
@@ -336,6 +335,36 @@ int gemm_f16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int l
 int gemm_bf16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int lda,
                        const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
                        float beta, float *C, int ldc, void *stream);
+
+/*
+ * The same products with a workspace. Where a product has few output tiles and a
+ * long K (some ten to some hundred rows of A), K is shared out over workgroups,
+ * whose sums go through the workspace and are added in order by a second launch;
+ * others ignore it.
+ *
+ *   workspace   NULL (the plain call), or at least ll_mx4_workspace_size(M, N, K,
+ *               a) bytes, 16-byte aligned, overlapping nothing; its contents need
+ *               no preparation. Calls that share one must not overlap in time.
+ * ll_mx4_workspace_size: bytes that help this shape on the current device, 0 if
+ * none do; -1 for a negative size or an unknown `a` (LL_A_*, the form of A).
+ */
+#define LL_A_MX4 0
+#define LL_A_F16 1
+#define LL_A_BF16 2
+int64_t ll_mx4_workspace_size(int M, int N, int K, int a);
+int gemm_mx4f32_nt_ws(int M, int N, int K, float alpha,
+                      const uint8_t *A, int lda, const uint8_t *SA, int ldsa,
+                      const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
+                      float beta, float *C, int ldc,
+                      void *workspace, int64_t workspace_bytes, void *stream);
+int gemm_f16mx4f32_nt_ws(int M, int N, int K, float alpha, const uint16_t *A, int lda,
+                         const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
+                         float beta, float *C, int ldc,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+int gemm_bf16mx4f32_nt_ws(int M, int N, int K, float alpha, const uint16_t *A, int lda,
+                          const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
+                          float beta, float *C, int ldc,
+                          void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * rmsnorm_residual — the residual step between two blocks of a network, the

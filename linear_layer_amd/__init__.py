@@ -29,6 +29,8 @@ Entry points (same names as the C ABI in ``include/linear_layer.h``):
 * ``gemm_mx4f32_nt(A, SA, B, SB, C, alpha=1.0, beta=0.0, K=None)`` — C = alpha*A*B^T
   + beta*C, both operands in that format; ``gemm_f16mx4f32_nt`` and
   ``gemm_bf16mx4f32_nt(A, B, SB, C, alpha=1.0, beta=0.0)`` — the same with 16-bit A.
+  On the current stream, a product whose K is worth sharing out over workgroups takes
+  its workspace from torch's allocator; with ``stream`` given it runs without one.
 * ``rmsnorm_residual(Y, w_post, gate, alpha, X, w_pre, XO, H, eps=1e-5)`` — the residual
   step between two blocks: XO = X + alpha*gate*rms(Y)*w_post, H = rms(XO)*w_pre;
   ``rmsnorm_residual_grad`` — its gradient (``rmsnorm_grad_workspace_size`` bytes of
@@ -81,6 +83,7 @@ EXPORTED = ("gemm_f32", "gemm_f16f32", "gemm_bf16f32", "linear_bias_act", "ll_st
             "linear_bias_act_ws", "ll_linear_workspace_size", "linear_bias_act_noalloc",
             "ll_set_noalloc_limit",
             "mx4_quantize", "mx4_dequantize", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
+            "gemm_mx4f32_nt_ws", "gemm_f16mx4f32_nt_ws", "gemm_bf16mx4f32_nt_ws", "ll_mx4_workspace_size",
             "rmsnorm_residual", "rmsnorm_residual_grad", "ll_rmsnorm_grad_workspace_size")
 
 
@@ -132,6 +135,11 @@ def load():
     lib.gemm_mx4f32_nt.argtypes = [i32, i32, i32, f32, vp, i32, vp, i32, vp, i32, vp, i32, f32, vp, i32, vp]
     lib.gemm_f16mx4f32_nt.argtypes = [i32, i32, i32, f32, vp, i32, vp, i32, vp, i32, f32, vp, i32, vp]
     lib.gemm_bf16mx4f32_nt.argtypes = lib.gemm_f16mx4f32_nt.argtypes
+    lib.gemm_mx4f32_nt_ws.argtypes = lib.gemm_mx4f32_nt.argtypes[:-1] + [vp, i64, vp]
+    lib.gemm_f16mx4f32_nt_ws.argtypes = lib.gemm_f16mx4f32_nt.argtypes[:-1] + [vp, i64, vp]
+    lib.gemm_bf16mx4f32_nt_ws.argtypes = lib.gemm_f16mx4f32_nt_ws.argtypes
+    lib.ll_mx4_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.ll_mx4_workspace_size.restype = i64
     lib.rmsnorm_residual.argtypes = [i32, i32, i32, vp, i32, vp, vp, f32, vp, i32, vp, f32, vp, i32, vp, i32, vp]
     lib.rmsnorm_residual_grad.argtypes = [i32, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, f32, vp, i32, vp, f32,
                                           vp, i32, vp, i32, vp, vp, vp, vp, i64, vp]
@@ -139,7 +147,7 @@ def load():
     lib.ll_rmsnorm_grad_workspace_size.argtypes = [i32, i32]
     lib.ll_rmsnorm_grad_workspace_size.restype = i64
     for f in (lib.mx4_quantize, lib.mx4_dequantize, lib.gemm_mx4f32_nt, lib.gemm_f16mx4f32_nt,
-              lib.gemm_bf16mx4f32_nt):
+              lib.gemm_bf16mx4f32_nt, lib.gemm_mx4f32_nt_ws, lib.gemm_f16mx4f32_nt_ws, lib.gemm_bf16mx4f32_nt_ws):
         f.restype = i32
     lib.ll_status_string.argtypes = [i32]
     lib.ll_status_string.restype = ctypes.c_char_p

@@ -49,9 +49,10 @@ int quantize_args(int rows, int cols, int type, const void *X, int ldx, int x_ro
 }
 
 int gemm_mx4(int M, int N, int K, float alpha, int a, const void *A, int lda, const void *SA, int ldsa,
-             const void *B, int ldb, const void *SB, int ldsb, float beta, float *C, int ldc, void *stream)
+             const void *B, int ldb, const void *SB, int ldsb, float beta, float *C, int ldc, void *workspace,
+             int64_t workspace_bytes, void *stream)
 {
-    if (M < 0 || N < 0 || K < 0 || ldc < max1(N))
+    if (M < 0 || N < 0 || K < 0 || ldc < max1(N) || workspace_bytes < 0)
         return LL_ERR_INVALID_VALUE;
     const Packed qa{A, SA, M, K, lda, ldsa}, qb{B, SB, N, K, ldb, ldsb};
     if (!qb.lds_ok() || (a == MXA_MX4 ? !qa.lds_ok() : lda < max1(K)))
@@ -69,6 +70,9 @@ int gemm_mx4(int M, int N, int K, float alpha, int a, const void *A, int lda, co
                              a == MXA_MX4 ? qa.code_range() : Range{A, span(M, K, lda, 2)},
                              a == MXA_MX4 ? qa.scale_range() : Range{nullptr, 0}};
         if (in[2].bytes < 0 || any_overlap(&c, 1, in, 4))
+            return LL_ERR_INVALID_VALUE;
+        const Range ws{workspace, workspace != nullptr ? workspace_bytes : 0};
+        if (workspace != nullptr && (!aligned(workspace, 16) || any_overlap(&ws, 1, in, 4) || overlap(ws, c)))
             return LL_ERR_INVALID_VALUE;
     }
     const Device dev = current_device();
@@ -94,6 +98,12 @@ int gemm_mx4(int M, int N, int K, float alpha, int a, const void *A, int lda, co
     p.K = K;
     p.alpha = alpha;
     p.beta = beta;
+    const int64_t need = workspace != nullptr ? mx4_workspace(M, N, K, a, dev.cus) : 0;
+    if (need > 0) {
+        if (workspace_bytes < need)
+            return LL_ERR_INVALID_VALUE;
+        p.ws = static_cast<float *>(workspace);
+    }
     const hipError_t e = launch_gemm_mx4(p, a, dev.cus, s);
     return e == hipErrorInvalidValue ? LL_ERR_INVALID_VALUE : status(e);
 }
@@ -136,19 +146,52 @@ int gemm_mx4f32_nt(int M, int N, int K, float alpha, const uint8_t *A, int lda, 
                    const uint8_t *B, int ldb, const uint8_t *SB, int ldsb, float beta, float *C, int ldc,
                    void *stream)
 {
-    return gemm_mx4(M, N, K, alpha, MXA_MX4, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, ldc, stream);
+    return gemm_mx4(M, N, K, alpha, MXA_MX4, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, ldc, nullptr, 0, stream);
 }
 
 int gemm_f16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int lda, const uint8_t *B, int ldb,
                       const uint8_t *SB, int ldsb, float beta, float *C, int ldc, void *stream)
 {
-    return gemm_mx4(M, N, K, alpha, MXA_F16, A, lda, nullptr, 0, B, ldb, SB, ldsb, beta, C, ldc, stream);
+    return gemm_mx4(M, N, K, alpha, MXA_F16, A, lda, nullptr, 0, B, ldb, SB, ldsb, beta, C, ldc, nullptr, 0, stream);
 }
 
 int gemm_bf16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int lda, const uint8_t *B, int ldb,
                        const uint8_t *SB, int ldsb, float beta, float *C, int ldc, void *stream)
 {
-    return gemm_mx4(M, N, K, alpha, MXA_BF16, A, lda, nullptr, 0, B, ldb, SB, ldsb, beta, C, ldc, stream);
+    return gemm_mx4(M, N, K, alpha, MXA_BF16, A, lda, nullptr, 0, B, ldb, SB, ldsb, beta, C, ldc, nullptr, 0, stream);
+}
+
+int64_t ll_mx4_workspace_size(int M, int N, int K, int a)
+{
+    if (M < 0 || N < 0 || K < 0 || (a != LL_A_MX4 && a != LL_A_F16 && a != LL_A_BF16))
+        return -1;
+    const Device dev = current_device();
+    return mx4_workspace(M, N, K, a == LL_A_MX4 ? MXA_MX4 : a == LL_A_F16 ? MXA_F16 : MXA_BF16,
+                         dev.status == LL_OK ? dev.cus : 256);
+}
+
+int gemm_mx4f32_nt_ws(int M, int N, int K, float alpha, const uint8_t *A, int lda, const uint8_t *SA, int ldsa,
+                      const uint8_t *B, int ldb, const uint8_t *SB, int ldsb, float beta, float *C, int ldc,
+                      void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return gemm_mx4(M, N, K, alpha, MXA_MX4, A, lda, SA, ldsa, B, ldb, SB, ldsb, beta, C, ldc, workspace, workspace_bytes,
+                    stream);
+}
+
+int gemm_f16mx4f32_nt_ws(int M, int N, int K, float alpha, const uint16_t *A, int lda, const uint8_t *B, int ldb,
+                         const uint8_t *SB, int ldsb, float beta, float *C, int ldc, void *workspace,
+                         int64_t workspace_bytes, void *stream)
+{
+    return gemm_mx4(M, N, K, alpha, MXA_F16, A, lda, nullptr, 0, B, ldb, SB, ldsb, beta, C, ldc, workspace, workspace_bytes,
+                    stream);
+}
+
+int gemm_bf16mx4f32_nt_ws(int M, int N, int K, float alpha, const uint16_t *A, int lda, const uint8_t *B, int ldb,
+                          const uint8_t *SB, int ldsb, float beta, float *C, int ldc, void *workspace,
+                          int64_t workspace_bytes, void *stream)
+{
+    return gemm_mx4(M, N, K, alpha, MXA_BF16, A, lda, nullptr, 0, B, ldb, SB, ldsb, beta, C, ldc, workspace, workspace_bytes,
+                    stream);
 }
 
 }  // extern "C"

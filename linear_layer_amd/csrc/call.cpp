@@ -7,6 +7,7 @@
 // then finds and reports what is wrong.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "linear_layer.h"
@@ -134,6 +135,14 @@ float *vec(Args &a, PyObject *o, int64_t n)
 int64_t code_bytes(int64_t K) { return (K + 1) / 2; }
 int64_t scale_bytes(int64_t K) { return (K + 31) / 32; }
 
+// The workspace a product gains from, if any: memory of torch's allocator, in the
+// order of the current stream, so that it may be given back at once.
+at::Tensor scratch(const Args &a, PyObject *like, const Mat &A, const Mat &B, int64_t K, int form)
+{
+    const int64_t bytes = a.ok && A.rows > 0 && B.rows > 0 ? ll_mx4_workspace_size(A.rows, B.rows, (int)K, form) : 0;
+    return bytes > 0 ? at::empty({bytes}, THPVariable_Unpack(like).options().dtype(at::kByte)) : at::Tensor();
+}
+
 template <class F>
 PyObject *enqueue(const Args &a, F call)
 {
@@ -222,10 +231,12 @@ PyObject *gemm_mx4(PyObject *const *x)
     const Mat SB(a, x[3], at::kByte, B.rows, scale_bytes(K)), C(a, x[4], at::kFloat, A.rows, B.rows);
     const float alpha = (float)a.number(x[5]), beta = (float)a.number(x[6]);
     void *stream = a.stream();
+    const at::Tensor w = scratch(a, x[4], A, B, K, LL_A_MX4);
     return enqueue(a, [&] {
-        return gemm_mx4f32_nt(A.rows, B.rows, (int)K, alpha, static_cast<uint8_t *>(A.p), A.ld,
+        return gemm_mx4f32_nt_ws(A.rows, B.rows, (int)K, alpha, static_cast<uint8_t *>(A.p), A.ld,
                               static_cast<uint8_t *>(SA.p), SA.ld, static_cast<uint8_t *>(B.p), B.ld,
-                              static_cast<uint8_t *>(SB.p), SB.ld, beta, static_cast<float *>(C.p), C.ld, stream);
+                              static_cast<uint8_t *>(SB.p), SB.ld, beta, static_cast<float *>(C.p), C.ld,
+                                 w.defined() ? w.data_ptr() : nullptr, w.defined() ? w.numel() : 0, stream);
     });
 }
 
@@ -238,10 +249,12 @@ PyObject *gemm_16mx4(PyObject *const *x)
     const Mat SB(a, x[2], at::kByte, B.rows, scale_bytes(A.cols)), C(a, x[3], at::kFloat, A.rows, B.rows);
     const float alpha = (float)a.number(x[4]), beta = (float)a.number(x[5]);
     void *stream = a.stream();
+    const at::Tensor w = scratch(a, x[3], A, B, A.cols, BF16 ? LL_A_BF16 : LL_A_F16);
     return enqueue(a, [&] {
-        return (BF16 ? gemm_bf16mx4f32_nt : gemm_f16mx4f32_nt)(
+        return (BF16 ? gemm_bf16mx4f32_nt_ws : gemm_f16mx4f32_nt_ws)(
             A.rows, B.rows, A.cols, alpha, static_cast<uint16_t *>(A.p), A.ld, static_cast<uint8_t *>(B.p), B.ld,
-            static_cast<uint8_t *>(SB.p), SB.ld, beta, static_cast<float *>(C.p), C.ld, stream);
+            static_cast<uint8_t *>(SB.p), SB.ld, beta, static_cast<float *>(C.p), C.ld,
+            w.defined() ? w.data_ptr() : nullptr, w.defined() ? w.numel() : 0, stream);
     });
 }
 

@@ -47,12 +47,15 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r16 = lane & 15;
-    const int id = block_index(blockIdx.x, gridDim.x);
-    const int tm = id % p.tiles_m, tn = id / p.tiles_m;
+    const int tiles = p.tiles_m * p.tiles_n, id = block_index(blockIdx.x, gridDim.x);
+    const int split = id / tiles, tile = id - split * tiles;
+    const int tm = tile % p.tiles_m, tn = tile / p.tiles_m;
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
     const int K = p.K;
     const int nblk = (K - 1) / kMxBlock + 1;
-    const int nunit = (nblk + 4 * J - 1) / (4 * J);
+    const int all = (nblk + 4 * J - 1) / (4 * J);
+    // this workgroup's units: all of them, or the split-th of p.splits shares
+    const int begin = (int)((int64_t)all * split / p.splits), nunit = (int)((int64_t)all * (split + 1) / p.splits);
 
     const uint8_t *arow[FM], *sarow[FM], *brow[FN], *sbrow[FN];
 #pragma unroll
@@ -184,9 +187,9 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
     };
 
     // whole units, two in flight
-    const int whole = K / (128 * J);
+    const int whole = min(K / (128 * J), nunit);
     Unit u0, u1;
-    int unit = wave, left = nunit;   // units from `left` on are still to do
+    int unit = begin + wave, left = nunit;   // units from `left` on are still to do
     if (unit < whole)
         fetch(u0, unit);
     while (unit < whole) {
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
         }
     }
     // the one that K ends in, and for binary16 A what its wave left
-    if (left == nunit && whole < nunit && whole % W == wave)
+    if (left == nunit && whole < nunit && (whole - begin) % W == wave)
         left = whole;
     for (; left < nunit; left += W) {
         fetch_ragged(u0, left);
@@ -233,8 +236,31 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
 #pragma unroll
         for (int w = 1; w < W; ++w)
             v += part[w][i];
-        float *dst = p.C + m * p.ldc + n;
-        *dst = finish(p, v, dst);
+        if (p.splits > 1) {
+            p.ws[((int64_t)split * p.M + m) * p.N + n] = v;
+        } else {
+            float *dst = p.C + m * p.ldc + n;
+            *dst = finish(p, v, dst);
+        }
+    }
+}
+
+// C from the shares' sums, added in their order: four columns to a thread.
+__global__ void __launch_bounds__(256) gemm_mx4_join_kernel(MxParams p, int quads, int64_t items)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        const int64_t m = i / quads, n = (i - m * quads) * 4;
+        const float *src = p.ws + m * p.N + n;
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            float v[4];
+            load_row<LL_TYPE_F32, 4>(src + (int64_t)s * p.M * p.N, p.N - n, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum[j] += v[j];
+        }
+        finish4(p, sum, p.C + m * p.ldc + n, 0, p.N - n);
     }
 }
 
@@ -243,10 +269,16 @@ static hipError_t launch_stream(MxParams p, hipStream_t s)
 {
     p.tiles_m = cdiv(p.M, 16 * FM);
     p.tiles_n = cdiv(p.N, 16 * FN);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n;
+    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
     if (tiles > max_grid_x(64 * W))
         return hipErrorInvalidValue;
     hipLaunchKernelGGL((gemm_mx4_stream_kernel<A, FM, FN, J, W, LONG>), dim3((unsigned)tiles), dim3(64 * W), 0, s, p);
+    if (p.splits > 1) {
+        const int quads = cdiv(p.N, 4);
+        const int64_t items = (int64_t)p.M * quads, groups = (items + 255) / 256;
+        hipLaunchKernelGGL(gemm_mx4_join_kernel, dim3((unsigned)(groups < 1 << 20 ? groups : 1 << 20)), dim3(256), 0, s, p,
+                           quads, items);
+    }
     return hipGetLastError();
 }
 
@@ -433,43 +465,114 @@ static hipError_t launch_rows(const MxParams &p, hipStream_t s)
     return hipGetLastError();
 }
 
-// Which tile: 256 x 256, one to a CU, or 128 x 128, two to a CU, in rounds. A round
-// of the small one takes 0.57 of the large one's time (0.5 with one tile to a CU),
-// a large last round done in halves 0.62. Measured at K 4096 with both operands in
-// 4 bits: 4096^2 (one full round) 47 against 54 us, 2047 x 4096 30.1 against 28.9,
-// 1024 x 4096 23.6 against 20.8, 1024 x 11008 39 against 43, 2047 x 11008 68
-// against 70; with bfloat16 A 61.8/65.0, 52.9/46.9, 92/97 and 155/174.
-static int choose_tile(const MxParams &p, bool dma, int cus)
+// ---------------------------------------------------------------------------
+// The plan of a product: which kernel, and for the streaming kernel in how many
+// shares of K (one without a workspace).
+
+enum Kernel : int { ROWS, ROWS_SHARED, TINY, TILE_256, TILE_128, STREAM };   // from STREAM on: kStream's
+struct Stream {
+    int fm, fn;
+    bool mx, h16;   // built for A in MX4, in 16 bits
+};
+constexpr Stream kStream[] = {{1, 1, true, true}, {2, 2, true, true}, {4, 4, true, false}, {1, 4, false, true},
+                              {2, 4, false, true}, {3, 4, false, true}};
+constexpr int kStreams = sizeof kStream / sizeof kStream[0];
+
+struct Plan {
+    int kernel, splits;
+};
+
+// Estimated times in us, from measurements on MI355X. The streaming kernel's
+// follows the bytes that a CU's workgroups read (16-bit A: 64 x 4096 x 4096 270 KB in
+// 14.4 us, 256 x 4096 x 4096 802 in 35.5, 128 x 11008 x 4096 1203 in 53; 4-bit A, in
+// shorter loads: 48 x 11008 x 4096 278 KB in 17.3), the tiles' the stages of a round: 128 x 128 alone on a CU
+// 15.7 us at K 4096 in 4 bits and 43 with 16-bit A, two to a CU 28.9 and 65; 256 x 256
+// 47 and 114, in halves 20.3 and 49.
+static Plan plan(int64_t M, int64_t N, int64_t K, int a, bool copies, bool workspace, int cus)
 {
-    if (!dma || p.M < 256 || p.N < 256)
-        return MX_TILE_128;
-    const int64_t large = (int64_t)cdiv(p.M, 256) * cdiv(p.N, 256), small = (int64_t)cdiv(p.M, 128) * cdiv(p.N, 128);
-    auto rounds = [](int64_t tiles, int slots, int few, double cost_few, double cost) {
-        const int64_t last = tiles % slots;
-        return (double)(tiles / slots) * cost + (last == 0 ? 0.0 : last <= few ? cost_few : cost);
+    if (K < 32)
+        return {TINY, 1};
+    // one row of A (its LDS copy within 60 KiB): two waves to a row of B where the
+    // rows are long and few (4096 x 11008 6.9 against 7.4 us, 512 x 11008 4.4 against 5.7)
+    if (M == 1 && K >= 512 && rows_lds(a, K) <= 61440)
+        return {K > 2 * N ? ROWS_SHARED : ROWS, 1};
+    const bool mx = a == MXA_MX4;
+    auto tiles = [&](int64_t bm, int64_t bn) { return (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn); };
+    auto rounds = [](double n, double slots) { return (double)(int64_t)((n + slots - 1) / slots); };
+    Plan best = {STREAM, 1};
+    double least = 1e30;
+    auto offer = [&](double us, int kernel, int splits) {
+        if (us < least) {
+            least = us;
+            best = {kernel, splits};
+        }
     };
-    return rounds(large, cus, cus / 2, 0.62, 1.0) <= rounds(small, 2 * cus, cus, 0.5, 0.57) ? MX_TILE_256 : MX_TILE_128;
+    const double arow = (double)(mx ? K / 2 + K / 32 : 2 * K), brow = (double)(K / 2 + K / 32);
+    for (int i = 0; i < kStreams; ++i) {
+        const Stream &c = kStream[i];
+        if (!(mx ? c.mx : c.h16))
+            continue;
+        const double n = tiles(16 * c.fm, 16 * c.fn);
+        const double bytes = (16 * c.fm < M ? 16 * c.fm : M) * arow + (16 * c.fn < N ? 16 * c.fn : N) * brow;
+        for (int s = 1; s <= (workspace ? 16 : 1); ++s) {
+            // a share has at least 8 blocks of four for its eight waves; the sums are
+            // written and read again, and added by a second launch
+            if (s > 1 && (K < 1024 * (int64_t)s || (double)M * (double)N * 4 * s > 6.4e7))
+                break;
+            offer(3.0 + rounds(n * s, cus) * bytes / s / (mx ? 20e3 : 26e3) + (s > 1 ? 4.5 + (double)M * (double)N * 8 * s / 3e6 : 0.0),
+                  STREAM + i, s);
+        }
+    }
+    if (M >= 128 && N >= 128 && K >= 512) {
+        const double t = tiles(128, 128), k = (double)K / 4096, full = (double)(int64_t)(t / (2 * cus)), last = t - full * 2 * cus;
+        offer(3.0 + k * (full * (mx ? 26.0 : 62.0) + (last > cus ? (mx ? 26.0 : 62.0) : last > 0 ? (mx ? 13.0 : 40.0) : 0.0)), TILE_128, 1);
+    }
+    if (copies && M >= 256 && N >= 256 && K >= 512) {
+        const double t = tiles(256, 256), k = (double)K / 4096, full = (double)(int64_t)(t / cus), last = t - full * cus;
+        offer(4.0 + k * (full * (mx ? 43.0 : 108.0) + (last > cus / 2 ? (mx ? 43.0 : 108.0) : last > 0 ? (mx ? 17.0 : 46.0) : 0.0)), TILE_256, 1);
+    }
+    return best;
+}
+
+int64_t mx4_workspace(int M, int N, int K, int a, int cus)
+{
+    if (M <= 0 || N <= 0 || K <= 0)
+        return 0;
+    int splits = 1;
+    for (int copies = 0; copies < 2; ++copies) {
+        const int n = plan(M, N, K, a, copies != 0, true, cus).splits;
+        splits = n > splits ? n : splits;
+    }
+    return splits > 1 ? (int64_t)splits * M * N * 4 : 0;
 }
 
 template <int A>
-static hipError_t launch_a(const MxParams &p, int cus, hipStream_t s)
+static hipError_t launch_a(MxParams p, int cus, hipStream_t s)
 {
-    if (p.K < 32)
-        return launch_stream<A, 1, 1, 1, 4, false>(p, s);
-    // one row of A (its LDS copy within 60 KiB): two waves to a row of B where the
-    // rows are long and few (4096 x 11008 6.9 against 7.4 us, 512 x 11008 4.4 against 5.7)
-    if (p.M == 1 && p.K >= 512 && rows_lds(A, p.K) <= 61440)
-        return p.K > 2 * (int64_t)p.N ? launch_rows<A, 2, 2, 4>(p, s) : launch_rows<A, 2, 1, 8>(p, s);
-    if (p.M <= 16)
-        return launch_stream<A, 1, 1, A == MXA_MX4 ? 2 : 1, 8>(p, s);
     // copies take rows of whole 16-byte pieces and 32-bit offsets within a tile
-    const bool dma = ((uintptr_t)p.A | (uintptr_t)p.B | (uintptr_t)p.lda | (uintptr_t)p.ldb) % 16 == 0 &&
-                     p.lda < 1 << 24 && p.ldb < 1 << 24 && p.ldsa < 1 << 24 && p.ldsb < 1 << 24;
-    if (p.M >= 128 && p.N >= 128 && p.K >= 512)
-        return launch_gemm_mx4_tile(p, A, choose_tile(p, dma, cus), dma, cus, s);
-    if (p.M <= 64)
-        return launch_stream<A, 2, 2, 1, 8>(p, s);
-    return launch_stream<A, 4, 4, 1, 4>(p, s);
+    const bool copies = ((uintptr_t)p.A | (uintptr_t)p.B | (uintptr_t)p.lda | (uintptr_t)p.ldb) % 16 == 0 &&
+                        p.lda < 1 << 24 && p.ldb < 1 << 24 && p.ldsa < 1 << 24 && p.ldsb < 1 << 24;
+    const Plan q = plan(p.M, p.N, p.K, A, copies, p.ws != nullptr, cus);
+    p.splits = q.splits;
+    constexpr bool MX = A == MXA_MX4;
+    switch (q.kernel) {
+    case ROWS: return launch_rows<A, 2, 1, 8>(p, s);
+    case ROWS_SHARED: return launch_rows<A, 2, 2, 4>(p, s);
+    case TINY: return launch_stream<A, 1, 1, 1, 4, false>(p, s);
+    case TILE_256: return launch_gemm_mx4_tile(p, A, MX_TILE_256, copies, cus, s);
+    case TILE_128: return launch_gemm_mx4_tile(p, A, MX_TILE_128, copies, cus, s);
+    case STREAM: return launch_stream<A, 1, 1, MX ? 2 : 1, 8>(p, s);
+    case STREAM + 1: return launch_stream<A, 2, 2, 1, 8>(p, s);
+    }
+    if constexpr (MX) {
+        return launch_stream<A, 4, 4, 1, 8>(p, s);
+    } else {
+        switch (q.kernel) {
+        case STREAM + 3: return launch_stream<A, 1, 4, 1, 8>(p, s);
+        case STREAM + 4: return launch_stream<A, 2, 4, 1, 8>(p, s);
+        default: return launch_stream<A, 3, 4, 1, 8>(p, s);
+        }
+    }
 }
 
 hipError_t launch_gemm_mx4(MxParams p, int a, int cus, hipStream_t s)

@@ -28,12 +28,16 @@ struct MxParams {
     int tiles_m, tiles_n;
     int group_m;             // tile rows per group in the tiles' order
     int halved;              // tiles at its end done in two halves
+    float *ws;               // room for the shares' sums, or null: K is not shared out
+    int splits;              // shares of K
 };
 
 // Tiles of 256 x 256 or 128 x 128 (M and N at least that, K at least 512); `copies`:
 // rows of 16-byte pieces, copied straight into LDS.
 enum MxTile : int { MX_TILE_256 = 0, MX_TILE_128 = 1 };
 hipError_t launch_gemm_mx4_tile(MxParams p, int a, int tile, bool copies, int cus, hipStream_t s);
+// Bytes of workspace that make a product faster (0: none does).
+int64_t mx4_workspace(int M, int N, int K, int a, int cus);
 hipError_t launch_gemm_mx4(MxParams p, int a, int cus, hipStream_t s);
 
 // The residual step between two blocks (rmsnorm.hip); null pointers leave parts out.

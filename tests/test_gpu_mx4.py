@@ -397,3 +397,74 @@ def test_one_row_with_far_scales_and_non_finite_values(which):
         args[0][0, 65] = float("inf")
         product(which, args, torch.as_tensor(c).to(DEV), torch.as_tensor(s).to(DEV), C, 1.0, 0.0, K)
         assert not bool(torch.isfinite(C).any())
+
+
+SHARED = [(33, 300, 11008), (20, 300, 9001), (8, 70, 8192), (64, 1000, 4100), (5, 16, 30000), (100, 90, 6000)]
+
+
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("M,N,K", SHARED)
+@pytest.mark.parametrize("alpha,beta,pad,shift", [(1.0, 0.0, 0, 0), (1.5, 0.5, 3, 1)])
+def test_product_shared_out_over_k(M, N, K, alpha, beta, pad, shift, which):
+    """Few tiles and a long K: shares of K through a workspace where the plan finds
+    them faster, as the call on the current stream takes one."""
+    check(which, M, N, K, alpha, beta, pad, shift, seed=19)
+
+
+@pytest.mark.parametrize("which", WHICH)
+def test_workspace_of_the_c_call(which):
+    """The call with a workspace: one too small is refused, a larger one taken, nothing
+    past it written, and the result is the call's on the current stream bit for bit."""
+    M, N, K = 33, 300, 11008
+    r = rng(20)
+    args, _ = a_operand(which, r, M, K, 0, 0)
+    c, s = (torch.as_tensor(v).to(DEV) for v in packed_case(r, N, K))
+    C, D = torch.zeros((M, N), device=DEV), torch.zeros((M, N), device=DEV)
+    product(which, args, c, s, C, 1.0, 0.0, K)
+    lib = ll.load()
+    need = lib.ll_mx4_workspace_size(M, N, K, {"mx4": 0, "f16": 1, "bf16": 2}[which])
+    work = torch.full((need + 256,), 255, dtype=torch.uint8, device=DEV)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(out, p, n):
+        b = (c.data_ptr(), c.stride(0), s.data_ptr(), s.stride(0), 0.0, out.data_ptr(), N, p, n, stream)
+        if which == "mx4":
+            a, sa = args
+            return lib.gemm_mx4f32_nt_ws(M, N, K, 1.0, a.data_ptr(), a.stride(0), sa.data_ptr(), sa.stride(0), *b)
+        f = lib.gemm_f16mx4f32_nt_ws if which == "f16" else lib.gemm_bf16mx4f32_nt_ws
+        return f(M, N, K, 1.0, args[0].data_ptr(), args[0].stride(0), *b)
+
+    assert call(D, work.data_ptr(), need - 1) == ll.ERR_INVALID_VALUE
+    assert call(D, work.data_ptr() + 4, need) == ll.ERR_INVALID_VALUE
+    assert call(D, c.data_ptr(), need) == ll.ERR_INVALID_VALUE
+    assert call(D, work.data_ptr(), need + 128) == ll.OK
+    assert torch.equal(C, D) and bool((work[need:] == 255).all())
+    E = torch.zeros((M, N), device=DEV)
+    assert call(E, None, 0) == ll.OK      # without one: another order of the same sums
+    assert torch.allclose(E, D, rtol=1e-3, atol=1e-3 * float(D.abs().max()))
+
+
+def test_shared_products_replay_from_a_graph():
+    """A product with a workspace and a norm's input after it, captured and replayed
+    with new inputs between the program's own calls."""
+    M, N, K = 33, 256, 11008
+    r = rng(21)
+    A = torch.zeros((M, K), dtype=torch.bfloat16, device=DEV)
+    c, s = (torch.as_tensor(v).to(DEV) for v in packed_case(r, N, K))
+    C = torch.empty((M, N), device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ll.gemm_bf16mx4f32_nt(A, c, s, C)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        ll.gemm_bf16mx4f32_nt(A, c, s, C)
+    for _ in range(4):
+        A.copy_(torch.randn((M, K), device=DEV))
+        want = torch.empty_like(C)
+        ll.gemm_bf16mx4f32_nt(A, c, s, want)
+        C.fill_(-1.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(C, want)

@@ -136,3 +136,22 @@ def test_reference_pins():
     # a value of the grid comes back as itself
     g = np.concatenate([GRID, -GRID, GRID, -GRID])[None, :]
     assert np.array_equal(values(*quantize(g), 32), g)
+
+
+def test_workspace_size_and_refusals():
+    lib = ll.load()
+    size = lib.ll_mx4_workspace_size
+    assert size(-1, 8, 64, 0) == -1 and size(4, -1, 64, 0) == -1 and size(4, 8, -1, 0) == -1
+    assert size(4, 8, 64, 3) == -1 and size(4, 8, 64, -1) == -1
+    assert size(0, 8, 64, 0) == 0 and size(1, 11008, 4096, 2) == 0 and size(8192, 8192, 8192, 0) == 0
+    assert size(33, 4096, 11008, 1) > 0 and size(33, 4096, 11008, 1) % (33 * 4096 * 4) == 0
+    for a in (0, 1, 2):
+        for M in (1, 3, 17, 100, 1000):
+            for N in (16, 500, 11008):
+                for K in (1, 31, 100, 5000, 100000):
+                    assert 0 <= size(M, N, K, a) <= 64e6
+    q, s = 32, 2
+    call = lambda ws, n: lib.gemm_mx4f32_nt_ws(4, 8, 64, 1.0, PX, q, PS, s, PB, q, PT, s, 0.0, PO, 8, ws, n, None)  # noqa: E731
+    assert call(PX, 256) == E and call(PO, 256) == E and call(PC + 8, 256) == E and call(PC, -1) == E
+    if no_device():
+        assert call(PC, 256) in FINE and call(None, 0) in FINE
