@@ -71,7 +71,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 # The in-package library, or another build of it named by LINEAR_LAYER_LIBRARY
 # (the CPU sanitizer test loads an AddressSanitizer build of the host code
 # that way). Either way the file must exist: there is no fallback.
-_LIB_PATH = os.environ.get("LINEAR_LAYER_LIBRARY") or os.path.join(_HERE, "liblinear_layer.so")
+_DEFAULT_LIB_PATH = os.path.join(_HERE, "liblinear_layer.so")
+_LIB_PATH = os.environ.get("LINEAR_LAYER_LIBRARY") or _DEFAULT_LIB_PATH
 _lib = None
 
 # Every symbol the C header declares.
@@ -470,6 +471,13 @@ def _linear(fn_name, X, W, bias, act, Y, stream, wt=False, ws=None):
 _call_module = None
 
 
+class _NoShortCalls:
+    """Every call takes the Python code: another build of the library is in use."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _short_calls():
     """The module that takes tensors apart for the short calls below. Its functions
     return a status, or None where an argument is not what the call takes; what is
@@ -478,6 +486,9 @@ def _short_calls():
     if _call_module is None:
         load()
         _torch()
+        if os.path.realpath(_LIB_PATH) != os.path.realpath(_DEFAULT_LIB_PATH):
+            _call_module = _NoShortCalls()   # (the module is linked with the library beside it)
+            return _call_module
         try:
             from . import _call as module
         except ImportError as e:

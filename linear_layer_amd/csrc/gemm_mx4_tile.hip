@@ -1,5 +1,27 @@
-// Tile kernel of the products with a 4-bit microscaled operand (see gemm_mx4.hip
-// for the operands' layout in the matrix instructions).
+// Tile kernel of the products with a 4-bit microscaled operand (the operands'
+// layout in the matrix instructions: gemm_mx4.hip).
+//
+// A workgroup computes a BM x BN tile of C, eight waves (256 x 256, one to a CU) or
+// four (128 x 128, two to a CU), a wave's share in 16 x 16 blocks. Codes and 16-bit
+// values go from memory straight into a ring of LDS stages (global_load_lds, rows of
+// 128 bytes where the operand allows, 16-byte pieces XOR-swizzled so that 16 lanes
+// read 16 different bank groups); operands that are not 16-byte aligned go through
+// registers into the same stages. A stage is two steps of the matrix instruction
+// (256 values of K in 4 bits, 64 with 16-bit A); a step's operands are read while the
+// step before multiplies, and 16-bit A finds B decoded in registers.
+//
+// Scales are single bytes, 32 values apart: loaded stage by stage they cost as many
+// requests as the codes. They come in panels of 16 a row instead, turned around in
+// registers so that one LDS read gives a lane the scales of all its rows, which the
+// instruction picks by byte.
+//
+// What bounds it: with both operands in 4 bits the rate at which L2 fills the CUs
+// (64 KiB a stage of 256 x 256 in 1.87 us, 34 bytes a ns and CU; the matrix cores are
+// busy 37 % of the time, a third stage, 128 x 256 tiles in three stages or twice as
+// many workgroups were no faster) and C's 4 bytes a value, which leave in whole rows
+// of 256 bytes through LDS: 8192^3 336 us, 3.3 PFLOP/s, of which 225 are the stages;
+// writing C in the instruction's 64-byte pieces took 30 us more. With bfloat16 A the
+// matrix cores' power limit: 8192^3 790 us, 1.39 PFLOP/s, 2047 x 11008 x 4096 157 us.
 #include "linear_layer.h"
 #include "gemm_mx4.hpp"
 
@@ -348,7 +370,8 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
                 store_panel((kt + 1) * NB);
         }
         __syncthreads();
-        read_ops(next, kt + 1, std::integral_constant<int, 0>{}, ops[0]);   // (after the last stage: unused)
+        if (REFILL || kt + 1 < nk)
+            read_ops(next, kt + 1, std::integral_constant<int, 0>{}, ops[0]);
         if ((kt + 2) % PS == 0 && (REFILL || kt + 2 < nk))
             load_panel((kt + 2) * NB);
         if constexpr (REFILL && !DMA)
