@@ -409,8 +409,8 @@ int rmsnorm_residual_grad(int M, int N, int type, const void *DXO, int lddxo, co
                           float *DY, int lddy, void *DX, int lddx,
                           float *dgate, float *dw_post, float *dw_pre,
                           void *workspace, int64_t workspace_bytes, void *stream);
-/* Bytes of workspace rmsnorm_residual_grad needs (at most 8 * 512 * N for N up
- * to 8192); -1 for a negative size. */
+/* Bytes of workspace rmsnorm_residual_grad needs (at most 8 * 1024 * N for N
+ * up to 8192); -1 for a negative size. */
 int64_t ll_rmsnorm_grad_workspace_size(int M, int N);
 
 /* A static, human-readable string for a status code (never NULL). */

@@ -14,7 +14,7 @@
 //
 // Both are bound by HBM: a row is read once into registers and its sums go
 // through one workgroup. Rows too long for the registers are read again. 8192 x 4096
-// bfloat16 forward 70 us, 4.8 TB/s; 8191 x 4096 gradient 117 us, 4.6 TB/s, of which 8
+// bfloat16 forward 70 us, 4.8 TB/s; 8191 x 4096 gradient 114 us, 4.7 TB/s, of which 8
 // add the partial sums over rows.
 #include "linear_layer.h"
 #include "lowp.hpp"
@@ -22,11 +22,25 @@
 
 namespace ll {
 
-// The sums of V values over a workgroup of NT threads, in every thread. The
-// order is fixed: lanes by halving distance, then waves in turn. `lds` is used
-// again by the next call: two barriers.
-template <int NT, int V>
-__device__ __forceinline__ void block_sum(float (&v)[V], float *lds)
+// LDS of a workgroup's sums: a place for each of up to 16 waves, of `N` sums in turn.
+template <int N>
+struct Sums {
+    float at[N][16];
+    // Once, by every thread of a workgroup of more than one wave.
+    __device__ __forceinline__ void clear()
+    {
+        if (threadIdx.x < 16 * N)
+            (&at[0][0])[threadIdx.x] = 0.0f;
+        __syncthreads();
+    }
+};
+
+// The sums of V values over a workgroup, in every thread, by way of places SLOT ..
+// SLOT + V - 1; where WAVE over the calling wave alone. The order is fixed: lanes by
+// halving distance, then waves likewise. One barrier: a slot is used again only after
+// a sum through another one.
+template <bool WAVE, int SLOT, int V, int N>
+__device__ __forceinline__ void block_sum(float (&v)[V], Sums<N> &lds)
 {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -34,23 +48,21 @@ __device__ __forceinline__ void block_sum(float (&v)[V], float *lds)
         for (int d = 32; d >= 1; d >>= 1)
             v[i] += __shfl_xor(v[i], d);
     }
-    if constexpr (NT > 64) {
-        constexpr int NW = NT / 64;
-        const int wave = threadIdx.x >> 6;
+    if constexpr (!WAVE) {
+        static_assert(SLOT + V <= N, "places");
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
             for (int i = 0; i < V; ++i)
-                lds[i * NW + wave] = v[i];
+                lds.at[SLOT + i][threadIdx.x >> 6] = v[i];
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            v[i] = 0.0f;
+            v[i] = lds.at[SLOT + i][threadIdx.x & 15];
 #pragma unroll
-            for (int w = 0; w < NW; ++w)
-                v[i] += lds[i * NW + w];
+            for (int d = 8; d >= 1; d >>= 1)
+                v[i] += __shfl_xor(v[i], d);
         }
-        __syncthreads();
     }
 }
 
@@ -59,31 +71,35 @@ __device__ __forceinline__ float inv_rms(float sum, int n, float eps)
     return 1.0f / sqrtf(sum / (float)n + eps);
 }
 
-// E values of a column vector from c on; `one` where there is no vector.
-template <int E>
-__device__ __forceinline__ void load_vec(const float *v, int64_t c, int64_t n, float one, float (&o)[E])
+// Eight values of a column vector from c on; `one` where there is no vector.
+__device__ __forceinline__ void load_vec(const float *v, int64_t c, int64_t n, float one, float (&o)[8])
 {
     if (v == nullptr) {
 #pragma unroll
-        for (int j = 0; j < E; ++j)
+        for (int j = 0; j < 8; ++j)
             o[j] = one;
     } else {
-        load_row<LL_TYPE_F32, E>(v + c, n - c, o);
+        load_row<LL_TYPE_F32, 8>(v + c, n - c, o);
     }
 }
 
-// A thread holds C groups of 8 neighbouring values, 8 * NT columns apart.
-// LONG: rows longer than 8 * NT * C, walked in several passes over memory,
+// A thread holds C groups of 8 neighbouring values, 8 columns times the workgroup's
+// width (whole waves, as many as the row needs) apart. LONG: rows longer than 8 * NT * C, walked in several passes over memory,
 // each sum in passes of its own.
+// MAX 64: a row to a wave, four waves to a workgroup, no barrier.
 // EARLY: the vectors are read with the row, not where they are used: with few rows
 // nothing else hides their latency (4 x 4096 binary16 4.9 -> 4.0 us).
-template <int TYPE, int NT, int C, bool LONG, bool EARLY>
-__global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
+template <int TYPE, int MAX, int C, bool LONG, bool EARLY>
+__global__ void __launch_bounds__(MAX == 64 ? 256 : MAX) rmsnorm_residual_kernel(NormParams p)
 {
     using T = typename Elem<TYPE>::type;
-    __shared__ float lds[2 * (NT / 64)];
-    const int N = p.N;
-    for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
+    constexpr bool WAVE = MAX == 64;
+    __shared__ Sums<2> lds;
+    const int N = p.N, NT = WAVE ? 64 : (int)blockDim.x, tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t rows = WAVE ? 4 : 1;
+    if constexpr (!WAVE)
+        lds.clear();
+    for (int64_t m = blockIdx.x * rows + (WAVE ? threadIdx.x >> 6 : 0); m < p.M; m += gridDim.x * rows) {
         const float *y = p.Y != nullptr ? p.Y + m * p.ldy : nullptr;
         const T *x = static_cast<const T *>(p.X) + m * p.ldx;
         T *xo = p.XO != nullptr ? static_cast<T *>(p.XO) + m * p.ldxo : nullptr;
@@ -93,7 +109,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
         auto load = [&](int pass) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + threadIdx.x);
+                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + tid);
                 load_row<TYPE, 8>(x + col, N - col, xv[c]);
                 if (y != nullptr)
                     load_row<LL_TYPE_F32, 8>(y + col, N - col, yv[c]);
@@ -107,10 +123,10 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
         if constexpr (EARLY) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int64_t col = 8 * ((int64_t)c * NT + threadIdx.x);
-                load_vec<8>(p.w_post, col, N, 1.0f, ew[c]);
-                load_vec<8>(p.gate, col, N, 1.0f, eg[c]);
-                load_vec<8>(p.w_pre, col, N, 1.0f, ep[c]);
+                const int64_t col = 8 * ((int64_t)c * NT + tid);
+                load_vec(p.w_post, col, N, 1.0f, ew[c]);
+                load_vec(p.gate, col, N, 1.0f, eg[c]);
+                load_vec(p.w_pre, col, N, 1.0f, ep[c]);
             }
         }
         if (y != nullptr) {
@@ -124,14 +140,14 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
                     for (int j = 0; j < 8; ++j)
                         s[0] = __builtin_fmaf(yv[c][j], yv[c][j], s[0]);
             }
-            block_sum<NT>(s, lds);
+            block_sum<WAVE, 0>(s, lds);
             ry = inv_rms(s[0], N, p.eps);
         }
         // x' in xv; written where asked for
         auto residual = [&](int pass, bool store) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + threadIdx.x);
+                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + tid);
                 if (col >= N)
                     continue;
                 if (y != nullptr) {
@@ -141,8 +157,8 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
                         for (int j = 0; j < 8; ++j)
                             w[j] = ew[c][j], g[j] = eg[c][j];
                     } else {
-                        load_vec<8>(p.w_post, col, N, 1.0f, w);
-                        load_vec<8>(p.gate, col, N, 1.0f, g);
+                        load_vec(p.w_post, col, N, 1.0f, w);
+                        load_vec(p.gate, col, N, 1.0f, g);
                     }
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -166,7 +182,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
         }
         if (h == nullptr)
             continue;
-        block_sum<NT>(s, lds);
+        block_sum<WAVE, 1>(s, lds);
         const float rx = inv_rms(s[0], N, p.eps);
         for (int pass = 0; pass < passes; ++pass) {
             if (LONG) {
@@ -175,7 +191,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + threadIdx.x);
+                const int64_t col = (int64_t)pass * span + 8 * ((int64_t)c * NT + tid);
                 if (col >= N)
                     continue;
                 float w[8];
@@ -184,7 +200,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_residual_kernel(NormParams p)
                     for (int j = 0; j < 8; ++j)
                         w[j] = ep[c][j];
                 } else {
-                    load_vec<8>(p.w_pre, col, N, 1.0f, w);
+                    load_vec(p.w_pre, col, N, 1.0f, w);
                 }
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
@@ -199,27 +215,27 @@ template <int TYPE>
 static hipError_t norm_t(const NormParams &p, hipStream_t s)
 {
     const int64_t most = 1 << 20;
-    const dim3 grid((unsigned)(p.M < most ? p.M : most));
-#define LL_NORM(NT, C, LONG, EARLY) \
-    hipLaunchKernelGGL((rmsnorm_residual_kernel<TYPE, NT, C, LONG, EARLY>), grid, dim3(NT), 0, s, p)
-    // few rows: a thread to 8 columns and every load at once
-    const bool few = p.M <= 512;
+    const int64_t groups = p.N <= 1024 ? ((int64_t)p.M + 3) / 4 : p.M;
+    const dim3 grid((unsigned)(groups < most ? groups : most));
+#define LL_NORM(MAX, C, LONG, EARLY, NT) \
+    hipLaunchKernelGGL((rmsnorm_residual_kernel<TYPE, MAX, C, LONG, EARLY>), grid, dim3(NT), 0, s, p)
+    // a thread to 8 columns, or 16 where there are rows to hide its latency; few
+    // rows read everything at once (6061 x 4892 binary16 93 us, in a fixed 512 threads 102)
+    const int one = cdiv(cdiv(p.N, 8), 64) * 64, two = cdiv(cdiv(p.N, 16), 64) * 64;
     if (p.N <= 512)
-        LL_NORM(64, 1, false, true);
+        LL_NORM(64, 1, false, true, 256);
+    else if (p.N <= 1024)
+        LL_NORM(64, 2, false, true, 256);
     else if (p.N <= 2048)
-        LL_NORM(256, 1, false, true);
-    else if (p.N <= 4096 && few)
-        LL_NORM(512, 1, false, true);
-    else if (p.N <= 4096)
-        LL_NORM(256, 2, false, false);
-    else if (p.N <= 8192 && few)
-        LL_NORM(1024, 1, false, true);
+        LL_NORM(256, 1, false, true, one);
+    else if (p.N <= 8192 && p.M <= 512)
+        LL_NORM(1024, 1, false, true, one);
     else if (p.N <= 8192)
-        LL_NORM(512, 2, false, false);
+        LL_NORM(512, 2, false, false, two);
     else if (p.N <= 16384)
-        LL_NORM(1024, 2, false, false);
+        LL_NORM(1024, 2, false, false, two);
     else
-        LL_NORM(1024, 1, true, false);
+        LL_NORM(1024, 1, true, false, 1024);
 #undef LL_NORM
     return hipGetLastError();
 }
@@ -243,22 +259,25 @@ hipError_t launch_rmsnorm_residual(int type, const NormParams &p, hipStream_t s)
 // TEAMS: rows so short that one wave holds one are taken by TEAMS waves of a
 // workgroup, a row each, and their shares added in wave order at the end
 // (8192 x 512 bfloat16 39 -> 20 us).
-template <int TYPE, int NT, int C, int TEAMS>
-__global__ void __launch_bounds__(NT * TEAMS) rmsnorm_grad_kernel(NormGradParams p)
+template <int TYPE, int MAX, int C, int TEAMS>
+__global__ void __launch_bounds__(MAX * TEAMS) rmsnorm_grad_kernel(NormGradParams p)
 {
     using T = typename Elem<TYPE>::type;
-    static_assert(TEAMS == 1 || (NT == 64 && C == 1), "a team is a wave: its sums need no barrier");
-    __shared__ float lds[2 * (NT / 64)];
-    const int N = p.N, tid = threadIdx.x % NT;
-    const int64_t stride = (int64_t)gridDim.x * TEAMS, first = (int64_t)blockIdx.x * TEAMS + threadIdx.x / NT;
+    static_assert(TEAMS == 1 || (MAX == 64 && C == 1), "a team is a wave: its sums need no barrier");
+    constexpr bool WAVE = MAX == 64;
+    __shared__ Sums<4> lds;
+    if constexpr (!WAVE)
+        lds.clear();
+    const int N = p.N, NT = WAVE ? 64 : (int)blockDim.x, tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+    const int64_t stride = (int64_t)gridDim.x * TEAMS, first = (int64_t)blockIdx.x * TEAMS + (WAVE ? threadIdx.x >> 6 : 0);
     float sS[C][8], sP[C][8], t[C][8], wp[C][8];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t col = 8 * ((int64_t)c * NT + tid);
         float g[8];
-        load_vec<8>(p.w_post, col, N, 1.0f, t[c]);
-        load_vec<8>(p.gate, col, N, 1.0f, g);
-        load_vec<8>(p.w_pre, col, N, 1.0f, wp[c]);
+        load_vec(p.w_post, col, N, 1.0f, t[c]);
+        load_vec(p.gate, col, N, 1.0f, g);
+        load_vec(p.w_pre, col, N, 1.0f, wp[c]);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             sS[c][j] = sP[c][j] = 0.0f;
@@ -274,10 +293,10 @@ __global__ void __launch_bounds__(NT * TEAMS) rmsnorm_grad_kernel(NormGradParams
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int64_t col = 8 * ((int64_t)c * NT + tid);
-            raw_row<LL_TYPE_F32>(p.Y != nullptr ? p.Y + m * p.ldy + col : nullptr, N - col, ry4[c]);
-            raw_row<TYPE>(static_cast<const T *>(p.X) + m * p.ldx + col, N - col, rx4[c]);
-            raw_row<TYPE>(p.DXO != nullptr ? static_cast<const T *>(p.DXO) + m * p.lddxo + col : nullptr, N - col, rd4[c]);
-            raw_row<TYPE>(p.DH != nullptr ? static_cast<const T *>(p.DH) + m * p.lddh + col : nullptr, N - col, rk4[c]);
+            raw_row<LL_TYPE_F32>(p.Y != nullptr ? p.Y + m * p.ldy + col : nullptr, N - col, N >= 8, ry4[c]);
+            raw_row<TYPE>(static_cast<const T *>(p.X) + m * p.ldx + col, N - col, N >= 8, rx4[c]);
+            raw_row<TYPE>(p.DXO != nullptr ? static_cast<const T *>(p.DXO) + m * p.lddxo + col : nullptr, N - col, N >= 8, rd4[c]);
+            raw_row<TYPE>(p.DH != nullptr ? static_cast<const T *>(p.DH) + m * p.lddh + col : nullptr, N - col, N >= 8, rk4[c]);
         }
     };
     if (first < p.M)
@@ -287,17 +306,17 @@ __global__ void __launch_bounds__(NT * TEAMS) rmsnorm_grad_kernel(NormGradParams
         float s[1] = {0.0f};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            raw_values<LL_TYPE_F32>(ry4[c], yv[c]);
-            raw_values<TYPE>(rx4[c], xv[c]);
-            raw_values<TYPE>(rd4[c], dv[c]);
-            raw_values<TYPE>(rk4[c], kv[c]);
+            raw_values<LL_TYPE_F32>(ry4[c], N - 8 * ((int64_t)c * NT + tid), N >= 8, yv[c]);
+            raw_values<TYPE>(rx4[c], N - 8 * ((int64_t)c * NT + tid), N >= 8, xv[c]);
+            raw_values<TYPE>(rd4[c], N - 8 * ((int64_t)c * NT + tid), N >= 8, dv[c]);
+            raw_values<TYPE>(rk4[c], N - 8 * ((int64_t)c * NT + tid), N >= 8, kv[c]);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 s[0] = __builtin_fmaf(yv[c][j], yv[c][j], s[0]);
         }
         if (m + stride < p.M)
             fetch(m + stride);
-        block_sum<NT>(s, lds);
+        block_sum<WAVE, 0>(s, lds);
         const float ry = inv_rms(s[0], N, p.eps);
         float q[2] = {0.0f, 0.0f};   // sums of x'^2 and of dh * w_pre * x'
 #pragma unroll
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(NT * TEAMS) rmsnorm_grad_kernel(NormGradParams
                 q[0] = __builtin_fmaf(xv[c][j], xv[c][j], q[0]);
                 q[1] = __builtin_fmaf(kv[c][j] * wp[c][j], xv[c][j], q[1]);
             }
-        block_sum<NT>(q, lds);
+        block_sum<WAVE, 1>(q, lds);
         const float rx = inv_rms(q[0], N, p.eps), mean_kn = q[1] * rx / (float)N;
         float z[1] = {0.0f};
 #pragma unroll
@@ -322,7 +341,7 @@ __global__ void __launch_bounds__(NT * TEAMS) rmsnorm_grad_kernel(NormGradParams
                 sS[c][j] = __builtin_fmaf(dv[c][j], yv[c][j], sS[c][j]);
                 z[0] = __builtin_fmaf(dv[c][j] * t[c][j], yv[c][j], z[0]);
             }
-        block_sum<NT>(z, lds);
+        block_sum<WAVE, 3>(z, lds);
         const float mean_z = z[0] / (float)N;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
@@ -339,19 +358,19 @@ __global__ void __launch_bounds__(NT * TEAMS) rmsnorm_grad_kernel(NormGradParams
         }
     }
     if constexpr (TEAMS > 1) {
-        __shared__ float shares[TEAMS][2][8 * NT + 8];
-        float(*mine)[8 * NT + 8] = shares[threadIdx.x / NT];
+        __shared__ float shares[TEAMS][2][8 * MAX + 8];
+        float(*mine)[8 * MAX + 8] = shares[threadIdx.x / MAX];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            mine[0][j * NT + tid] = sS[0][j], mine[1][j * NT + tid] = sP[0][j];
+            mine[0][j * MAX + tid] = sS[0][j], mine[1][j * MAX + tid] = sP[0][j];
         __syncthreads();
-        if (threadIdx.x >= NT)
+        if (threadIdx.x >= MAX)
             return;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
             for (int w = 1; w < TEAMS; ++w)
-                sS[0][j] += shares[w][0][j * NT + tid], sP[0][j] += shares[w][1][j * NT + tid];
+                sS[0][j] += shares[w][0][j * MAX + tid], sP[0][j] += shares[w][1][j * MAX + tid];
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -379,9 +398,9 @@ struct GradCols {
     __device__ __forceinline__ void vectors(const NormGradParams &p, int64_t col)
     {
         float g[8];
-        load_vec<8>(p.w_post, col, p.N, 1.0f, t);
-        load_vec<8>(p.gate, col, p.N, 1.0f, g);
-        load_vec<8>(p.w_pre, col, p.N, 1.0f, wp);
+        load_vec(p.w_post, col, p.N, 1.0f, t);
+        load_vec(p.gate, col, p.N, 1.0f, g);
+        load_vec(p.w_pre, col, p.N, 1.0f, wp);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             t[j] *= p.alpha * g[j];
@@ -405,7 +424,8 @@ struct GradCols {
 template <int TYPE, int NT>
 __global__ void __launch_bounds__(NT) rmsnorm_grad_stats_kernel(NormGradParams p, RowStats *stats)
 {
-    __shared__ float lds[2 * (NT / 64)];
+    __shared__ Sums<4> lds;
+    lds.clear();
     const int64_t m = blockIdx.x;
     GradCols<TYPE> v;
     RowStats r;
@@ -416,7 +436,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_stats_kernel(NormGradParams p
         for (int j = 0; j < 8; ++j)
             s[0] = __builtin_fmaf(v.y[j], v.y[j], s[0]);
     }
-    block_sum<NT>(s, lds);
+    block_sum<false, 0>(s, lds);
     r.ry = inv_rms(s[0], p.N, p.eps);
     for (int64_t col = 8 * (int64_t)threadIdx.x; col < p.N; col += 8 * NT) {
         v.row(p, m, col);
@@ -428,7 +448,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_stats_kernel(NormGradParams p
             q[1] = __builtin_fmaf(v.k[j] * v.wp[j], x, q[1]);
         }
     }
-    block_sum<NT>(q, lds);
+    block_sum<false, 1>(q, lds);
     r.rx = inv_rms(q[0], p.N, p.eps);
     r.mean_kn = q[1] * r.rx / (float)p.N;
     for (int64_t col = 8 * (int64_t)threadIdx.x; col < p.N; col += 8 * NT) {
@@ -441,7 +461,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_stats_kernel(NormGradParams p
             z[0] = __builtin_fmaf(total * v.t[j], u, z[0]);
         }
     }
-    block_sum<NT>(z, lds);
+    block_sum<false, 3>(z, lds);
     r.mean_z = z[0] / (float)p.N;
     if (threadIdx.x == 0)
         stats[m] = r;
@@ -533,10 +553,13 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_finish_kernel(NormGradParams
 // Rows that the registers of a workgroup hold, this one and the next (with 16384 in
 // 1024 threads they spill: 4096 x 16384 bfloat16 502 us against 462 in two launches).
 constexpr int kGradRegCols = 8192;
-// Workgroups (rows of partial sums) of a gradient: two for each CU.
-constexpr int kGradGroups = 512;
-
-static int grad_groups(int M) { return M < kGradGroups ? M : kGradGroups; }
+// Workgroups (rows of partial sums) of a gradient: two for each CU, four of short
+// rows (8192 x 600 FP32 39 us, with two 52).
+static int grad_groups(int M, int N)
+{
+    const int most = N <= 2048 ? 1024 : 512;
+    return M < most ? M : most;
+}
 static int64_t grad_stats_bytes(int M, int N)
 {
     return N > kGradRegCols ? ((int64_t)M * (int64_t)sizeof(RowStats) + 255) / 256 * 256 : 0;
@@ -544,27 +567,28 @@ static int64_t grad_stats_bytes(int M, int N)
 
 int64_t rmsnorm_grad_workspace(int M, int N)
 {
-    return M <= 0 || N <= 0 ? 0 : grad_stats_bytes(M, N) + (int64_t)grad_groups(M) * 2 * N * 4;
+    return M <= 0 || N <= 0 ? 0 : grad_stats_bytes(M, N) + (int64_t)grad_groups(M, N) * 2 * N * 4;
 }
 
 template <int TYPE>
 static hipError_t norm_grad_t(NormGradParams p, void *ws, hipStream_t s)
 {
     p.part = reinterpret_cast<float *>(static_cast<char *>(ws) + grad_stats_bytes(p.M, p.N));
-    const int groups = grad_groups(p.M);
+    const int groups = grad_groups(p.M, p.N);
     const dim3 grid((unsigned)groups);
-#define LL_GRAD(NT, C, TEAMS) \
-    hipLaunchKernelGGL((rmsnorm_grad_kernel<TYPE, NT, C, TEAMS>), grid, dim3(NT * TEAMS), 0, s, p)
+#define LL_GRAD(MAX, C, TEAMS, NT) \
+    hipLaunchKernelGGL((rmsnorm_grad_kernel<TYPE, MAX, C, TEAMS>), grid, dim3(NT), 0, s, p)
+    const int one = cdiv(cdiv(p.N, 8), 64) * 64, two = cdiv(cdiv(p.N, 16), 64) * 64;
     if (p.M <= 0)
         ;   // no rows: the finishing launch writes zeros
     else if (p.N <= 512)
-        LL_GRAD(64, 1, 4);
+        LL_GRAD(64, 1, 4, 256);
     else if (p.N <= 2048)
-        LL_GRAD(256, 1, 1);
-    else if (p.N <= 4096)
-        LL_GRAD(256, 2, 1);
+        LL_GRAD(256, 1, 1, one);
+    else if (p.N <= 3584)
+        LL_GRAD(512, 1, 1, one);
     else if (p.N <= kGradRegCols)
-        LL_GRAD(512, 2, 1);
+        LL_GRAD(512, 2, 1, two);
     else {
         RowStats *stats = static_cast<RowStats *>(ws);
         const int slab = 1 << 20;   // rows of a launch: work items fit 32 bits
