@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
 {
     constexpr bool MX = A == MXA_MX4;
     constexpr int BM = 16 * FM, BN = 16 * FN;
-    __shared__ float part[W][BM * BN];
+    __shared__ __attribute__((aligned(16))) float part[W][BM * BN];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r16 = lane & 15;
@@ -233,20 +233,31 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
             for (int r = 0; r < 4; ++r)
                 part[wave][(16 * m + 4 * g + r) * BN + 16 * n + r16] = acc[m][n][r];
     __syncthreads();
-#pragma unroll
-    for (int i = tid; i < BM * BN; i += 64 * W) {
-        const int64_t m = m0 + i / BN, n = n0 + i % BN;
+    constexpr int QUADS = BN / 4;
+    for (int i = tid; i < BM * QUADS; i += 64 * W) {
+        const int64_t m = m0 + i / QUADS, n = n0 + i % QUADS * 4;
         if (m >= p.M || n >= p.N)
             continue;
-        float v = part[0][i];
+        f32x4 v = *reinterpret_cast<const f32x4 *>(&part[0][4 * i]);
 #pragma unroll
-        for (int w = 1; w < W; ++w)
-            v += part[w][i];
+        for (int w = 1; w < W; ++w) {
+            const f32x4 u = *reinterpret_cast<const f32x4 *>(&part[w][4 * i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                v[j] += u[j];
+        }
         if (p.splits > 1) {
-            p.ws[((int64_t)split * p.M + m) * p.N + n] = v;
+            float *dst = p.ws + ((int64_t)split * p.M + m) * p.N + n;
+            if (n + 4 <= p.N) {
+                __builtin_memcpy(dst, &v, 16);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                    if (n + j < p.N)
+                        dst[j] = v[j];
+            }
         } else {
-            float *dst = p.C + m * p.ldc + n;
-            *dst = finish(p, v, dst);
+            finish4(p, v, p.C + m * p.ldc + n, 0, p.N - n);
         }
     }
 }
@@ -475,7 +486,7 @@ static hipError_t launch_rows(const MxParams &p, hipStream_t s)
 // The plan of a product: which kernel, and for the streaming kernel in how many
 // shares of K (one without a workspace).
 
-enum Kernel : int { ROWS, ROWS_SHARED, TINY, TILE_256, TILE_128, STREAM };   // from STREAM on: kStream's
+enum Kernel : int { ROWS, ROWS_SHARED, TINY, SHORT, TILE_256, TILE_128, STREAM };   // from STREAM on: kStream's
 struct Stream {
     int fm, fn;
     bool mx, h16;   // built for A in MX4, in 16 bits
@@ -491,7 +502,8 @@ struct Plan {
 // Estimated times in us, from measurements on MI355X. The streaming kernel's
 // follows the bytes that a CU's workgroups read (16-bit A: 64 x 4096 x 4096 270 KB in
 // 14.4 us, 256 x 4096 x 4096 802 in 35.5, 128 x 11008 x 4096 1203 in 53; 4-bit A, in
-// shorter loads: 48 x 11008 x 4096 278 KB in 17.3), the tiles' the stages of a round: 128 x 128 alone on a CU
+// shorter loads: 48 x 11008 x 4096 278 KB in 17.3), or the turns of its eight waves
+// (8 x 1000 x 8000 in 4 bits 12.2, in shares 8.2), the tiles' the stages of a round: 128 x 128 alone on a CU
 // 15.7 us at K 4096 in 4 bits and 43 with 16-bit A, two to a CU 28.9 and 65; 256 x 256
 // 47 and 114, in halves 20.3 and 49.
 static Plan plan(int64_t M, int64_t N, int64_t K, int a, bool copies, bool workspace, int cus)
@@ -505,6 +517,11 @@ static Plan plan(int64_t M, int64_t N, int64_t K, int a, bool copies, bool works
     const bool mx = a == MXA_MX4;
     auto tiles = [&](int64_t bm, int64_t bn) { return (double)((M + bm - 1) / bm) * (double)((N + bn - 1) / bn); };
     auto rounds = [](double n, double slots) { return (double)(int64_t)((n + slots - 1) / slots); };
+    // K of one or two turns: one wave to a tile, since the others of a workgroup would
+    // find nothing to do (5366 x 10986 x 128 in 4 bits 88 against 188 us, 1000 x 11008
+    // x 32 20 against 59)
+    if (K <= 256 && tiles(mx ? 64 : 32, 64) >= 2 * cus)
+        return {SHORT, 1};
     Plan best = {STREAM, 1};
     double least = 1e30;
     auto offer = [&](double us, int kernel, int splits) {
@@ -525,7 +542,10 @@ static Plan plan(int64_t M, int64_t N, int64_t K, int a, bool copies, bool works
             // written and read again, and added by a second launch
             if (s > 1 && (K < 1024 * (int64_t)s || (double)M * (double)N * 4 * s > 6.4e7))
                 break;
-            offer(3.0 + rounds(n * s, cus) * bytes / s / (mx ? 20e3 : 26e3) + (s > 1 ? 4.5 + (double)M * (double)N * 8 * s / 3e6 : 0.0),
+            // (two workgroups of a CU wait for their turns together)
+            const double fill = rounds(n * s, cus) * bytes / s / (mx ? 20e3 : 26e3);
+            const double wait = 1.15 * K / 1024 / s * (n * s > 2 * cus ? n * s / (2 * cus) : 1.0);
+            offer(3.0 + (fill > wait ? fill : wait) + (s > 1 ? 4.5 + (double)M * (double)N * 8 * s / 3e6 : 0.0),
                   STREAM + i, s);
         }
     }
@@ -565,6 +585,7 @@ static hipError_t launch_a(MxParams p, int cus, hipStream_t s)
     case ROWS: return launch_rows<A, 2, 1, 8>(p, s);
     case ROWS_SHARED: return launch_rows<A, 2, 2, 4>(p, s);
     case TINY: return launch_stream<A, 1, 1, 1, 4, false>(p, s);
+    case SHORT: return launch_stream<A, MX ? 4 : 2, 4, 1, 1>(p, s);
     case TILE_256: return launch_gemm_mx4_tile(p, A, MX_TILE_256, copies, cus, s);
     case TILE_128: return launch_gemm_mx4_tile(p, A, MX_TILE_128, copies, cus, s);
     case STREAM: return launch_stream<A, 1, 1, MX ? 2 : 1, 8>(p, s);

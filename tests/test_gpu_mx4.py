@@ -468,3 +468,11 @@ def test_shared_products_replay_from_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(C, want)
+
+
+@pytest.mark.parametrize("which", WHICH)
+@pytest.mark.parametrize("M,N,K", [(1300, 1700, 32), (2100, 1100, 128), (1501, 1603, 201), (1300, 1700, 256)])
+@pytest.mark.parametrize("alpha,beta,pad,shift", [(1.0, 0.0, 0, 0), (-1.5, 0.5, 3, 1)])
+def test_product_with_a_short_k(M, N, K, alpha, beta, pad, shift, which):
+    """Large outputs of a K of one or two turns: one wave to a tile."""
+    check(which, M, N, K, alpha, beta, pad, shift, seed=22)
