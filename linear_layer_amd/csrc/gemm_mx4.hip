@@ -503,7 +503,7 @@ struct Plan {
 // follows the bytes that a CU's workgroups read (16-bit A: 64 x 4096 x 4096 270 KB in
 // 14.4 us, 256 x 4096 x 4096 802 in 35.5, 128 x 11008 x 4096 1203 in 53; 4-bit A, in
 // shorter loads: 48 x 11008 x 4096 278 KB in 17.3), or the turns of its eight waves
-// (8 x 1000 x 8000 in 4 bits 12.2, in shares 8.2), the tiles' the stages of a round: 128 x 128 alone on a CU
+// (8 x 1000 x 8000 in 4 bits 12.2, in shares 9.8), the tiles' the stages of a round: 128 x 128 alone on a CU
 // 15.7 us at K 4096 in 4 bits and 43 with 16-bit A, two to a CU 28.9 and 65; 256 x 256
 // 47 and 114, in halves 20.3 and 49.
 static Plan plan(int64_t M, int64_t N, int64_t K, int a, bool copies, bool workspace, int cus)
