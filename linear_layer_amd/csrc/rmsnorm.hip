@@ -100,6 +100,11 @@ __global__ void __launch_bounds__(MAX == 64 ? 256 : MAX) rmsnorm_residual_kernel
     if constexpr (!WAVE)
         lds.clear();
     for (int64_t m = blockIdx.x * rows + (WAVE ? threadIdx.x >> 6 : 0); m < p.M; m += gridDim.x * rows) {
+        // without y or h a row has one sum: its slot is free for the next row once
+        // every wave has read it (of a workgroup that has a next row, past 2^20 rows)
+        if constexpr (!WAVE)
+            if (m != blockIdx.x && (p.Y == nullptr || p.H == nullptr))
+                __syncthreads();
         const float *y = p.Y != nullptr ? p.Y + m * p.ldy : nullptr;
         const T *x = static_cast<const T *>(p.X) + m * p.ldx;
         T *xo = p.XO != nullptr ? static_cast<T *>(p.XO) + m * p.ldxo : nullptr;
