@@ -1,5 +1,5 @@
-"""The residual norms past the ordinary: more rows than workgroups. Against the formulas
-in float64 on the GPU (torch), row slab by row slab.
+"""The residual norms past the ordinary: more rows than workgroups, no y and no eps.
+Against the formulas in float64 on the GPU (torch), slab by slab.
 
 Tolerances as in test_gpu_norm: 64 half-steps of FP32 (2^-24) of a result's size, the sum
 of its terms' magnitudes, and half a step of the output's type, finfo.eps / 2, of its
@@ -90,3 +90,29 @@ def test_more_rows_than_workgroups_with_both():
         size = xd.abs() + step.abs()
         close(xo[m:m + (1 << 17)], out, size, 64, f"x', rows from {m}")
         close(h[m:m + (1 << 17)], out * r(out, 1e-5) * w.double(), size * r(out, 1e-5) * w.double().abs(), 64, f"h, rows from {m}")
+
+
+@pytest.mark.parametrize("M,N", [(3, 100), (40, 600), (5, 4096), (2, 9001)])
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("eps", [0.0, 1e-5])
+def test_gradient_without_y_takes_nothing_from_its_norm(M, N, dtype, eps):
+    """x' = x: neither the norm of an absent y (1 / 0 where eps is 0) nor w_post, gate
+    and alpha, whatever they hold, have a part in dx and dw_pre. A chain of two results
+    each 64 half-steps off: 128; a sum over M rows M more."""
+    g = gen(4)
+    x, dxo, dh = (torch.randn((M, N), generator=g, device=DEV).to(dtype) for _ in range(3))
+    w = 1 + 0.2 * torch.randn((N,), generator=g, device=DEV)
+    xd, kd = x.double(), dh.double() * w.double()
+    rx = r(xd, eps)
+    n = xd * rx
+    total = dxo.double() + rx * (kd - n * (kd * n).mean(1, keepdim=True))
+    size = dxo.double().abs() + rx * (kd.abs() + n.abs() * (kd * n).abs().mean(1, keepdim=True))
+    sums, sum_size = (dh.double() * n).sum(0), (dh.double() * n).abs().sum(0)
+    work = torch.empty((ll.rmsnorm_grad_workspace_size(M, N),), dtype=torch.uint8, device=DEV)
+    far = torch.full((N,), float("nan"), device=DEV)
+    far[::2] = float("inf")
+    for w_post, gate, alpha in ((None, None, 1.0), (far, None, 1.0), (None, far, 0.7), (None, None, float("inf"))):
+        dx, dw = torch.full_like(x, -7.0), torch.full((N,), -7.0, device=DEV)
+        ll.rmsnorm_residual_grad(dxo, dh, None, w_post, gate, alpha, x, w, None, dx, None, None, dw, work, eps=eps)
+        close(dx, total, size, 128, "dx")
+        close(dw, sums, sum_size, 128 + M, "dw_pre")
