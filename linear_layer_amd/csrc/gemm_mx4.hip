@@ -17,7 +17,8 @@
 // included, which the matrix units keep). In binary16 it is exact for scale
 // bytes 104 .. 140 only (2^-23 .. 2^13); past those the wave splits A's values
 // into two bfloat16 parts instead (11 bits of fraction into 8 and 3) and
-// multiplies twice, which is exact for every scale.
+// multiplies twice, which is exact too. The two largest scales pass bfloat16's
+// range as well: see far_dot.
 #include "linear_layer.h"
 #include "gemm_mx4.hpp"
 
@@ -234,6 +235,15 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
                 part[wave][(16 * m + 4 * g + r) * BN + 16 * n + r16] = acc[m][n][r];
     __syncthreads();
     constexpr int QUADS = BN / 4;
+    if constexpr (!MX && W == 1)   // a lone wave looks at all its sums at once (5000 x 5000 x 128 in bfloat16 32.4 us, in the loop 33.6)
+        if (__builtin_expect(__any(!all_finite(acc)), 0))
+#pragma unroll 1
+            for (int i = tid; i < BM * QUADS; i += 64) {
+                const int64_t m = m0 + i / QUADS, n = n0 + i % QUADS * 4;
+                float *at = &part[0][4 * i];
+                if (m < p.M)
+                    settle4<A>(p, *reinterpret_cast<f32x4 *>(at), at, m, n, begin * 4 * J, min(nunit * 4 * J, nblk));
+            }
     for (int i = tid; i < BM * QUADS; i += 64 * W) {
         const int64_t m = m0 + i / QUADS, n = n0 + i % QUADS * 4;
         if (m >= p.M || n >= p.N)
@@ -246,6 +256,9 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
             for (int j = 0; j < 4; ++j)
                 v[j] += u[j];
         }
+        if constexpr (!MX && W > 1)
+            if (__builtin_expect(!finite4(v), 0))
+                v = settle4<A>(p, v, &part[0][4 * i], m, n, begin * 4 * J, min(nunit * 4 * J, nblk));
         if (p.splits > 1) {
             float *dst = p.ws + ((int64_t)split * p.M + m) * p.N + n;
             if (n + 4 <= p.N) {
@@ -445,6 +458,7 @@ __global__ void __launch_bounds__(64 * KW * NW) gemm_mx4_rows_kernel(MxParams p)
     // the diagonal: lane l has column l % 16 and rows 4 * (l / 16) .. +3
     const int r16 = lane & 15;
     const bool mine = (r16 >> 2) == lane >> 4;
+    float sum = 0.0f;   // lane i: of row i
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         const f32x4 d = acc[i];
@@ -452,22 +466,24 @@ __global__ void __launch_bounds__(64 * KW * NW) gemm_mx4_rows_kernel(MxParams p)
         float v = dpp_row_sum16(mine ? e : 0.0f);
         v += __shfl_xor(v, 16);
         v += __shfl_xor(v, 32);
-        if constexpr (KW > 1) {
-            if (lane == 0)
-                sums[wave][i] = v;
-        } else if (lane == i && n0 + i < p.N) {
-            p.C[n0 + i] = finish(p, v, p.C + n0 + i);
-        }
+        sum = lane == i ? v : sum;
     }
     if constexpr (KW > 1) {
+        if (lane < R)
+            sums[wave][lane] = sum;
         __syncthreads();
-        if (wave % KW == 0 && lane < R && n0 + lane < p.N) {
-            float v = sums[wave][lane];
+        if (wave % KW != 0)
+            return;
+    }
+    const int64_t n = n0 + lane;
+    if (lane < R && n < p.N) {
 #pragma unroll
-            for (int k = 1; k < KW; ++k)
-                v += sums[wave + k][lane];
-            p.C[n0 + lane] = finish(p, v, p.C + n0 + lane);
-        }
+        for (int k = 1; k < KW; ++k)
+            sum += sums[wave + k][lane];
+        if constexpr (!MX)
+            if (__builtin_expect(!finite(sum), 0))
+                sum = far_dot<A>(sum, p.A, p.B + n * p.ldb, p.SB + n * p.ldsb, 0, nblk, K);
+        p.C[n] = finish(p, sum, p.C + n);
     }
 }
 

@@ -88,6 +88,68 @@ __device__ __forceinline__ void turn4(u32x4 &v)
 // Whether a scale byte keeps the decoded values exact in binary16.
 __device__ __forceinline__ bool f16_scale_ok(uint32_t s) { return s - 104u <= 36u; }
 
+// Scale bytes 253 and 254: values reach 6 * 2^127, past bfloat16 and FP32, and
+// decode8 makes them infinite. They are rare, so nothing looks for them before a sum
+// has come out infinite or NaN, as any such value makes it: then its inner product
+// over the blocks [b0, b1) is taken again, value by value, those blocks decoded 2^-4
+// lower and their products (exact, and 2^-13 at least) times 2^4. Returns the sum as
+// it was where its row of B has no such scale. (Looked for in the loops they cost
+// the bfloat16 products 2 to 7 %.)
+__device__ __forceinline__ bool far_scale(uint32_t s) { return s - 253u < 2u; }
+
+__device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
+
+template <int A>
+__device__ __forceinline__ float far_dot(float sum, const uint8_t *a, const uint8_t *b, const uint8_t *sb, int b0, int b1,
+                                         int K)
+{
+    bool far = false;
+#pragma unroll 1
+    for (int blk = b0; blk < b1; ++blk)
+        far |= far_scale(sb[blk]);
+    if (!far)
+        return sum;
+    sum = 0.0f;
+#pragma unroll 1
+    for (int64_t k = (int64_t)b0 * kMxBlock; k < K && k < (int64_t)b1 * kMxBlock; ++k) {
+        const uint32_t s = sb[k / kMxBlock], code = b[k / 2] >> (4 * (k & 1)) & 15u;
+        const uint16_t h = reinterpret_cast<const uint16_t *>(a)[k];
+        const float x = A == MXA_F16 ? to_f32<LL_TYPE_F16>(h) : to_f32<LL_TYPE_BF16>(h);
+        const float y = __uint_as_float(decode8<true>(code, __uint_as_float((far_scale(s) ? s - 4u : s) << 23))[0] << 16);
+        sum = __builtin_fmaf(x * y, far_scale(s) ? 16.0f : 1.0f, sum);
+    }
+    return sum;
+}
+
+// Four neighbouring sums of row m and columns n .. n+3 (those inside N), in LDS that
+// the calling lane alone uses, and all four after far_dot had those that are not finite.
+template <int A>
+__device__ __forceinline__ f32x4 settle4(const MxParams &p, const f32x4 &v, float *at, int64_t m, int64_t n, int b0, int b1)
+{
+    *reinterpret_cast<f32x4 *>(at) = v;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j)
+        if (n + j < p.N && !finite(at[j]))
+            at[j] = far_dot<A>(at[j], p.A + m * p.lda, p.B + (n + j) * p.ldb, p.SB + (n + j) * p.ldsb, b0, b1, p.K);
+    return *reinterpret_cast<f32x4 *>(at);
+}
+// Whether sums are finite, by one comparison of theirs (false too where they overflow
+// together, which costs a look at each).
+__device__ __forceinline__ bool finite4(const f32x4 &v) { return finite(v[0] + v[1] + v[2] + v[3]); }
+template <int M, int N>
+__device__ __forceinline__ bool all_finite(const f32x4 (&v)[M][N])
+{
+    f32x4 t = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                t[r] += v[m][n][r];
+    return finite4(t);
+}
+
 // One value through the epilogue.
 __device__ __forceinline__ float finish(const MxParams &p, float v, const float *dst)
 {

@@ -452,7 +452,20 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
     static_assert(NW * 32 * LDC * 4 <= sizeof(Lds), "the waves' rows fit the stages");
     float *mine = reinterpret_cast<float *>(&lds) + wave * (32 * LDC);
     const int64_t n = nb + wn * WTN + 4 * r16;
-    const bool plain = p.beta == 0.0f && ma == m0 && nb == n0 && mleft == BM && nleft == BN;
+    // bfloat16 A: whether a sum of this wave is not finite and which of its rows of B, a
+    // lane each, have a far scale
+    uint64_t far = 0;
+    if constexpr (A == MXA_BF16) {
+        if (__builtin_expect(__any(!all_finite(acc)), 0)) {
+            const uint8_t *row = sbbase + min(wn * WTN + lane, nleft - 1) * p.ldsb;
+            bool any = false;
+#pragma unroll 1
+            for (int blk = 0; blk < nblk; ++blk)
+                any |= far_scale(row[blk]);
+            far = __ballot(any);
+        }
+    }
+    const bool plain = p.beta == 0.0f && ma == m0 && nb == n0 && mleft == BM && nleft == BN && far == 0;
 #pragma unroll
     for (int i = 0; i < FM; i += 2) {
 #pragma unroll
@@ -461,7 +474,7 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
             for (int j = 0; j < FN; ++j)
                 *reinterpret_cast<f32x4 *>(&mine[(16 * h + r16) * LDC + 16 * j + 4 * g]) = acc[i + h][j];
         float *dst = p.C + (ma + wm * WTM + 16 * i + g) * p.ldc + n;
-        const float *from = &mine[g * LDC + 4 * r16];
+        float *from = &mine[g * LDC + 4 * r16];
         if (plain) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -475,8 +488,13 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
 #pragma unroll 1
             for (int q = 0; q < 8; ++q) {
                 const int64_t m = ma + wm * WTM + 16 * i + 4 * q + g;
-                if (m >= m0 && m < p.M)
-                    finish4(p, *reinterpret_cast<const f32x4 *>(from + 4 * q * LDC), dst + 4 * q * p.ldc, n0 - n, p.N - n);
+                if (m >= m0 && m < p.M) {
+                    f32x4 v = *reinterpret_cast<const f32x4 *>(from + 4 * q * LDC);
+                    if constexpr (A == MXA_BF16)
+                        if ((far >> (4 * r16) & 15) != 0 && !finite4(v))
+                            v = settle4<A>(p, v, from + 4 * q * LDC, m, n, 0, nblk);
+                    finish4(p, v, dst + 4 * q * p.ldc, n0 - n, p.N - n);
+                }
             }
         }
     }
@@ -487,9 +505,9 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
 // values in two parts. A wave takes its rows 32 at a time (few registers, so that
 // the path above keeps them), operands straight from memory.
 template <int BM, int BN, int WGM, int WGN>
-__device__ __forceinline__ void mx4_tile_wide(const MxParams &p, int64_t m0, int64_t n0)
+__device__ __forceinline__ void mx4_tile_wide(const MxParams &p, int64_t m0, int64_t n0, uint8_t *raw)
 {
-    constexpr int FM = 2, FN = BN / WGN / 16;
+    constexpr int FM = 2, FN = BN / WGN / 16, NT = 64 * WGM * WGN;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, r16 = lane & 15;
     const int64_t n = n0 + wave % WGN * (BN / WGN);
@@ -524,16 +542,22 @@ __device__ __forceinline__ void mx4_tile_wide(const MxParams &p, int64_t m0, int
                 }
             }
         }
+        // through LDS, a thread's own, so that the sums can be told apart by a loop
+        f32x4 *mine = reinterpret_cast<f32x4 *>(raw) + threadIdx.x;
 #pragma unroll
-        for (int a = 0; a < FM; ++a) {
-            const int64_t row = m + 16 * a + r16;
+        for (int a = 0; a < FM; ++a)
+#pragma unroll
+            for (int b = 0; b < FN; ++b)
+                mine[(a * FN + b) * NT] = acc[a][b];
+#pragma unroll 1
+        for (int j = 0; j < FM * FN; ++j) {
+            const int64_t row = m + 16 * (j / FN) + r16, col = n + 16 * (j % FN) + 4 * g;
+            f32x4 v = mine[j * NT];
             if (row >= p.M)
                 continue;
-#pragma unroll
-            for (int b = 0; b < FN; ++b) {
-                const int64_t col = n + 16 * b + 4 * g;
-                finish4(p, acc[a][b], p.C + row * p.ldc + col, 0, p.N - col);
-            }
+            if (!finite4(v))
+                v = settle4<MXA_F16>(p, v, reinterpret_cast<float *>(mine + j * NT), row, col, 0, nblk);
+            finish4(p, v, p.C + row * p.ldc + col, 0, p.N - col);
         }
     }
 }
@@ -543,8 +567,10 @@ __device__ __forceinline__ void mx4_tile_any(const MxParams &p, int64_t m0, int6
 {
     const bool done = mx4_tile<A, BM, BN, 2, NBUF, WGM, WGN, DMA>(p, m0, n0, raw);
     if constexpr (A == MXA_F16)
-        if (!done)
-            mx4_tile_wide<BM, BN, WGM, WGN>(p, m0, n0);
+        if (!done) {
+            static_assert(2 * (BN / WGN / 16) * 64 * WGM * WGN * 16 <= tile_lds<A>(BM, BN, 2, NBUF), "the waves' sums fit the stages");
+            mx4_tile_wide<BM, BN, WGM, WGN>(p, m0, n0, raw);
+        }
 }
 
 // One workgroup a tile, in an order that keeps an XCD's tiles together. The last
