@@ -189,16 +189,18 @@ static hipError_t quantize_t(const void *X, int64_t ldx, bool trans, uint8_t *co
     using T = typename Elem<TYPE>::type;
     const T *x = static_cast<const T *>(X);
     if (trans) {
-        const int tiles_k = cdiv(K, kTransCols);
-        const int per = 0x3fffffff / tiles_k / 512;   // tile rows of a launch (work items fit 32 bits)
-        const int64_t tall = (int64_t)kTransBlocks * kMxBlock;
-        const int tiles_m = (int)(((int64_t)M + tall - 1) / tall), slab = per < 1 ? 1 : per;
-        for (int t = 0; t < tiles_m; t += slab) {
-            const int n = tiles_m - t < slab ? tiles_m - t : slab;
-            const int64_t m0 = t * tall;
-            hipLaunchKernelGGL(mx4_quantize_trans_kernel<TYPE>, dim3((unsigned)(n * tiles_k)),
-                               dim3(64 * kTransBlocks), 0, s, x + m0 * ldx, ldx, codes + m0 / 2, ldq,
-                               scales + m0 / kMxBlock, lds, (int)(M - m0), K, tiles_k);
+        // launches of at most 2^30 work items: slabs of columns, and of rows of tiles
+        constexpr int most = (1 << 30) / (64 * kTransBlocks), cols = most * kTransCols, tall = kTransBlocks * kMxBlock;
+        const int tiles_m = cdiv(M, tall);
+        for (int64_t k0 = 0; k0 < K; k0 += cols) {
+            const int k = (int)(K - k0 < cols ? K - k0 : cols), tiles_k = cdiv(k, kTransCols), slab = most / tiles_k;
+            for (int t = 0; t < tiles_m; t += slab) {
+                const int n = tiles_m - t < slab ? tiles_m - t : slab;
+                const int64_t m0 = (int64_t)t * tall;
+                hipLaunchKernelGGL(mx4_quantize_trans_kernel<TYPE>, dim3((unsigned)(n * tiles_k)),
+                                   dim3(64 * kTransBlocks), 0, s, x + m0 * ldx + k0, ldx, codes + k0 * ldq + m0 / 2, ldq,
+                                   scales + k0 * lds + m0 / kMxBlock, lds, (int)(M - m0), k, tiles_k);
+            }
         }
     } else {
         const int slab = slab_rows(M, K);
