@@ -365,6 +365,12 @@ int gemm_bf16mx4f32_nt_ws(int M, int N, int K, float alpha, const uint16_t *A, i
                           const uint8_t *B, int ldb, const uint8_t *SB, int ldsb,
                           float beta, float *C, int ldc,
                           void *workspace, int64_t workspace_bytes, void *stream);
+/* Name of the kernel such a product takes on a device with num_cus compute units
+ * (num_cus <= 0: 256), with rows of A and B on 16 bytes (`aligned`) and with a
+ * workspace or not: "rows", "rows_shared", "tiny", "short", "tile_256x256",
+ * "tile_128x128" or "stream_" and a tile's size; "" for a product without work or a
+ * bad argument. Static string. */
+const char *ll_mx4_chosen_kernel(int M, int N, int K, int a, int aligned, int workspace, int num_cus);
 
 /*
  * rmsnorm_residual — the residual step between two blocks of a network, the

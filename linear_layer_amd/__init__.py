@@ -31,6 +31,7 @@ Entry points (same names as the C ABI in ``include/linear_layer.h``):
   ``gemm_bf16mx4f32_nt(A, B, SB, C, alpha=1.0, beta=0.0)`` — the same with 16-bit A.
   On the current stream, a product whose K is worth sharing out over workgroups takes
   its workspace from torch's allocator; with ``stream`` given it runs without one.
+  ``mx4_chosen_kernel`` names the kernel that such a product takes.
 * ``rmsnorm_residual(Y, w_post, gate, alpha, X, w_pre, XO, H, eps=1e-5)`` — the residual
   step between two blocks: XO = X + alpha*gate*rms(Y)*w_post, H = rms(XO)*w_pre;
   ``rmsnorm_residual_grad`` — its gradient (``rmsnorm_grad_workspace_size`` bytes of
@@ -52,7 +53,7 @@ __all__ = [
     "linear_bias_act_ws", "linear_workspace_size", "linear_bias_act_noalloc", "NOALLOC_SCRATCH_BYTES",
     "set_noalloc_limit",
     "mx4_quantize", "mx4_dequantize", "mx4_shapes", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
-    "rmsnorm_residual", "rmsnorm_residual_grad", "rmsnorm_grad_workspace_size",
+    "mx4_chosen_kernel", "A_MX4", "A_F16", "A_BF16", "rmsnorm_residual", "rmsnorm_residual_grad", "rmsnorm_grad_workspace_size",
     "TYPE_F32", "TYPE_F16", "TYPE_BF16",
     "library_path", "load", "set_tile", "num_tiles", "tile_name", "chosen_tile",
     "set_split_k", "chosen_split_k", "set_stream_k", "chosen_stream_k",
@@ -64,6 +65,7 @@ OK, ERR_INVALID_VALUE, ERR_NO_DEVICE, ERR_UNSUPPORTED_ARCH, ERR_LAUNCH = 0, 1, 2
 ACT_NONE, ACT_RELU = 0, 1
 DTYPE_F32, DTYPE_F16 = 0, 1
 TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2   # element types of mx4_quantize, mx4_dequantize and the residual norms
+A_MX4, A_F16, A_BF16 = 0, 1, 2   # the forms of A of the 4-bit products
 PLAN_RELU, PLAN_B_NK, PLAN_UNALIGNED = 0x100, 0x200, 0x400   # flags OR-ed into dtype for chosen_*
 NOALLOC_SCRATCH_BYTES = 65 << 20   # the static workspace of linear_bias_act_noalloc
 
@@ -85,6 +87,7 @@ EXPORTED = ("gemm_f32", "gemm_f16f32", "gemm_bf16f32", "linear_bias_act", "ll_st
             "ll_set_noalloc_limit",
             "mx4_quantize", "mx4_dequantize", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
             "gemm_mx4f32_nt_ws", "gemm_f16mx4f32_nt_ws", "gemm_bf16mx4f32_nt_ws", "ll_mx4_workspace_size",
+            "ll_mx4_chosen_kernel",
             "rmsnorm_residual", "rmsnorm_residual_grad", "ll_rmsnorm_grad_workspace_size")
 
 
@@ -141,6 +144,8 @@ def load():
     lib.gemm_bf16mx4f32_nt_ws.argtypes = lib.gemm_f16mx4f32_nt_ws.argtypes
     lib.ll_mx4_workspace_size.argtypes = [i32, i32, i32, i32]
     lib.ll_mx4_workspace_size.restype = i64
+    lib.ll_mx4_chosen_kernel.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.ll_mx4_chosen_kernel.restype = ctypes.c_char_p
     lib.rmsnorm_residual.argtypes = [i32, i32, i32, vp, i32, vp, vp, f32, vp, i32, vp, f32, vp, i32, vp, i32, vp]
     lib.rmsnorm_residual_grad.argtypes = [i32, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, f32, vp, i32, vp, f32,
                                           vp, i32, vp, i32, vp, vp, vp, vp, i64, vp]
@@ -618,6 +623,14 @@ def gemm_f16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream
 def gemm_bf16mx4f32_nt(A, B, SB, C, alpha: float = 1.0, beta: float = 0.0, stream=None):
     """C = alpha*A*B^T + beta*C with bf16 A and B (N x K) as uint8 codes and scales."""
     return _gemm_16mx4("gemm_bf16mx4f32_nt", "bfloat16", A, B, SB, C, alpha, beta, stream)
+
+
+def mx4_chosen_kernel(M: int, N: int, K: int, a: int, aligned: bool = True, workspace: bool = True,
+                      num_cus: int = 0) -> str:
+    """Name of the kernel that a product with A in the form ``a`` (A_*) takes, with rows
+    on 16 bytes or not; "" for one without work."""
+    return load().ll_mx4_chosen_kernel(int(M), int(N), int(K), int(a), int(bool(aligned)), int(bool(workspace)),
+                                       int(num_cus)).decode()
 
 
 # ---- residual norms ------------------------------------------------------------

@@ -31,6 +31,10 @@ struct Packed {
     }
 };
 
+// The form of A (LL_A_*) as the launchers name it.
+bool known_form(int a) { return a == LL_A_MX4 || a == LL_A_F16 || a == LL_A_BF16; }
+int form(int a) { return a == LL_A_MX4 ? MXA_MX4 : a == LL_A_F16 ? MXA_F16 : MXA_BF16; }
+
 int quantize_args(int rows, int cols, int type, const void *X, int ldx, int x_rows, int x_cols, const Packed &q,
                   bool writes_x)
 {
@@ -163,11 +167,15 @@ int gemm_bf16mx4f32_nt(int M, int N, int K, float alpha, const uint16_t *A, int 
 
 int64_t ll_mx4_workspace_size(int M, int N, int K, int a)
 {
-    if (M < 0 || N < 0 || K < 0 || (a != LL_A_MX4 && a != LL_A_F16 && a != LL_A_BF16))
+    if (M < 0 || N < 0 || K < 0 || !known_form(a))
         return -1;
     const Device dev = current_device();
-    return mx4_workspace(M, N, K, a == LL_A_MX4 ? MXA_MX4 : a == LL_A_F16 ? MXA_F16 : MXA_BF16,
-                         dev.status == LL_OK ? dev.cus : 256);
+    return mx4_workspace(M, N, K, form(a), dev.status == LL_OK ? dev.cus : 256);
+}
+
+const char *ll_mx4_chosen_kernel(int M, int N, int K, int a, int aligned, int workspace, int num_cus)
+{
+    return known_form(a) ? mx4_kernel_name(M, N, K, form(a), aligned != 0, workspace != 0, num_cus > 0 ? num_cus : 256) : "";
 }
 
 int gemm_mx4f32_nt_ws(int M, int N, int K, float alpha, const uint8_t *A, int lda, const uint8_t *SA, int ldsa,

@@ -588,6 +588,14 @@ int64_t mx4_workspace(int M, int N, int K, int a, int cus)
     return splits > 1 ? (int64_t)splits * M * N * 4 : 0;
 }
 
+const char *mx4_kernel_name(int M, int N, int K, int a, bool copies, bool workspace, int cus)
+{
+    static const char *const names[] = {"rows", "rows_shared", "tiny", "short", "tile_256x256", "tile_128x128",
+                                        "stream_16x16", "stream_32x32", "stream_64x64", "stream_16x64", "stream_32x64", "stream_48x64"};
+    static_assert(sizeof names / sizeof names[0] == STREAM + kStreams, "a name for each");
+    return M <= 0 || N <= 0 || K <= 0 ? "" : names[plan(M, N, K, a, copies, workspace, cus).kernel];
+}
+
 template <int A>
 static hipError_t launch_a(MxParams p, int cus, hipStream_t s)
 {

@@ -38,6 +38,8 @@ enum MxTile : int { MX_TILE_256 = 0, MX_TILE_128 = 1 };
 hipError_t launch_gemm_mx4_tile(MxParams p, int a, int tile, bool copies, int cus, hipStream_t s);
 // Bytes of workspace that make a product faster (0: none does).
 int64_t mx4_workspace(int M, int N, int K, int a, int cus);
+// The name of the kernel it takes.
+const char *mx4_kernel_name(int M, int N, int K, int a, bool copies, bool workspace, int cus);
 hipError_t launch_gemm_mx4(MxParams p, int a, int cus, hipStream_t s);
 
 // The residual step between two blocks (rmsnorm.hip); null pointers leave parts out.
