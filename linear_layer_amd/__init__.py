@@ -231,6 +231,7 @@ def chosen_stream_k(dtype: int, M: int, N: int, K: int, num_cus: int = 0, batch:
 # ---- tensor marshalling ---------------------------------------------------
 
 _torch_module = None
+_INT_MAX = 2 ** 31 - 1   # of the C calls' sizes and leading dimensions
 
 
 def _torch():
@@ -260,6 +261,8 @@ def _mat(t, dtype, name):
         ld = cols
     elif ld < cols:
         raise ValueError(f"{name}: row stride {ld} smaller than width {cols}")
+    if ld > _INT_MAX or rows > _INT_MAX:   # (ctypes would pass on the lower 32 bits)
+        raise ValueError(f"{name}: {rows} rows of {cols} values, {ld} apart: the calls take sizes up to {_INT_MAX}")
     return t.data_ptr(), rows, cols, ld if ld > 1 else 1
 
 
@@ -277,6 +280,8 @@ def _bmat(t, dtype, name):
         if not t.is_cuda:
             raise ValueError(f"{name} must be a device tensor")
         return 0, 0, t.shape[1], t.shape[2], max(t.shape[2], 1), 0
+    if nb > _INT_MAX:
+        raise ValueError(f"{name}: the calls take sizes up to {_INT_MAX}")
     ptr, rows, cols, ld = _mat(t[0], dtype, name)
     bstride = t.stride(0) if nb > 1 else 0
     if bstride < 0:
@@ -680,6 +685,8 @@ def rmsnorm_residual(Y, w_post, gate, alpha, X, w_pre, XO, H, eps: float = 1e-5,
 
 def rmsnorm_grad_workspace_size(M: int, N: int) -> int:
     """Bytes of workspace rmsnorm_residual_grad needs for M x N."""
+    if M > _INT_MAX or N > _INT_MAX:
+        raise ValueError(f"the calls take sizes up to {_INT_MAX}")
     n = load().ll_rmsnorm_grad_workspace_size(int(M), int(N))
     if n < 0:
         raise ValueError("negative size")
