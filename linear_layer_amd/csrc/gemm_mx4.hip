@@ -22,6 +22,7 @@
 #include "linear_layer.h"
 #include "gemm_mx4.hpp"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace ll {
@@ -294,19 +295,39 @@ __global__ void __launch_bounds__(256) gemm_mx4_join_kernel(MxParams p, int quad
     }
 }
 
-template <int A, int FM, int FN, int J, int W, bool LONG = true>
-static hipError_t launch_stream(MxParams p, hipStream_t s)
+// The part of a product from row m and column n on, `rows` x `cols` of it.
+static MxParams part_of(MxParams p, int64_t m, int64_t n, int64_t rows, int64_t cols)
 {
-    p.tiles_m = cdiv(p.M, 16 * FM);
-    p.tiles_n = cdiv(p.N, 16 * FN);
-    const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * p.splits;
-    if (tiles > max_grid_x(64 * W))
-        return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gemm_mx4_stream_kernel<A, FM, FN, J, W, LONG>), dim3((unsigned)tiles), dim3(64 * W), 0, s, p);
-    if (p.splits > 1) {
-        const int quads = cdiv(p.N, 4);
-        const int64_t items = (int64_t)p.M * quads, groups = (items + 255) / 256;
-        hipLaunchKernelGGL(gemm_mx4_join_kernel, dim3((unsigned)(groups < 1 << 20 ? groups : 1 << 20)), dim3(256), 0, s, p,
+    p.A += m * p.lda;
+    p.SA = p.SA != nullptr ? p.SA + m * p.ldsa : nullptr;
+    p.B += n * p.ldb;
+    p.SB += n * p.ldsb;
+    p.C += m * p.ldc + n;
+    p.M = (int)rows;
+    p.N = (int)cols;
+    return p;
+}
+
+template <int A, int FM, int FN, int J, int W, bool LONG = true>
+static hipError_t launch_stream(const MxParams &whole, hipStream_t s)
+{
+    // launches of as many tiles as their work items can be counted (a product with
+    // shares of K, whose workspace is laid out for all of it, has far fewer)
+    constexpr int64_t most = max_grid_x(64 * W), BM = 16 * FM, BN = 16 * FN;
+    const int64_t rows = std::min<int64_t>(whole.M, most * BM);
+    const int64_t cols = std::min<int64_t>(whole.N, most / ((rows + BM - 1) / BM) * BN);
+    for (int64_t m = 0; m < whole.M; m += rows)
+        for (int64_t n = 0; n < whole.N; n += cols) {
+            MxParams p = part_of(whole, m, n, std::min(rows, whole.M - m), std::min(cols, whole.N - n));
+            p.tiles_m = cdiv(p.M, BM);
+            p.tiles_n = cdiv(p.N, BN);
+            hipLaunchKernelGGL((gemm_mx4_stream_kernel<A, FM, FN, J, W, LONG>),
+                               dim3((unsigned)(p.tiles_m * p.tiles_n * p.splits)), dim3(64 * W), 0, s, p);
+        }
+    if (whole.splits > 1) {
+        const int quads = cdiv(whole.N, 4);
+        const int64_t items = (int64_t)whole.M * quads, groups = (items + 255) / 256;
+        hipLaunchKernelGGL(gemm_mx4_join_kernel, dim3((unsigned)(groups < 1 << 20 ? groups : 1 << 20)), dim3(256), 0, s, whole,
                            quads, items);
     }
     return hipGetLastError();
@@ -488,13 +509,14 @@ __global__ void __launch_bounds__(64 * KW * NW) gemm_mx4_rows_kernel(MxParams p)
 }
 
 template <int A, int R, int KW, int NW>
-static hipError_t launch_rows(const MxParams &p, hipStream_t s)
+static hipError_t launch_rows(const MxParams &whole, hipStream_t s)
 {
-    const int64_t groups = ((int64_t)p.N + R * NW - 1) / (R * NW);
-    if (groups > max_grid_x(64 * KW * NW))
-        return hipErrorInvalidValue;
-    hipLaunchKernelGGL((gemm_mx4_rows_kernel<A, R, KW, NW>), dim3((unsigned)groups), dim3(64 * KW * NW),
-                       (unsigned)rows_lds(A, p.K), s, p);
+    constexpr int64_t cols = max_grid_x(64 * KW * NW) * R * NW;   // of a launch
+    for (int64_t n = 0; n < whole.N; n += cols) {
+        const MxParams p = part_of(whole, 0, n, 1, std::min(cols, whole.N - n));
+        hipLaunchKernelGGL((gemm_mx4_rows_kernel<A, R, KW, NW>), dim3((unsigned)cdiv(p.N, R * NW)), dim3(64 * KW * NW),
+                           (unsigned)rows_lds(A, p.K), s, p);
+    }
     return hipGetLastError();
 }
 
