@@ -522,12 +522,13 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_cols_kernel(NormGradParams p
 // The columns' sums over `rows` partial rows, then dgate, dw_post and dw_pre. A
 // workgroup takes 16 columns; its threads, 4 quads of columns by 64, every 64th row,
 // 8 of them in flight, and their sums are added in a fixed order (16 MB of 512
-// partial rows of 4096: 8 us, with 32 columns to a workgroup 11).
-__global__ void __launch_bounds__(256) rmsnorm_grad_finish_kernel(NormGradParams p, int rows)
+// partial rows of 4096: 8 us, with 32 columns to a workgroup 11). The launch's
+// columns begin at `from`.
+__global__ void __launch_bounds__(256) rmsnorm_grad_finish_kernel(NormGradParams p, int rows, int64_t from)
 {
     __shared__ float sums[64][2][16 + 1];
     const int quad = threadIdx.x & 3, r0 = threadIdx.x >> 2;
-    const int64_t col = (int64_t)blockIdx.x * 16 + 4 * quad, left = p.N - col;
+    const int64_t col = from + (int64_t)blockIdx.x * 16 + 4 * quad, left = p.N - col;
     float a[4] = {0.0f, 0.0f, 0.0f, 0.0f}, b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (left > 0) {
         for (int r = r0; r < rows; r += 512) {
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(256) rmsnorm_grad_finish_kernel(NormGradParams
     for (int j = 0; j < 4; ++j)
         sums[r0][0][4 * quad + j] = a[j], sums[r0][1][4 * quad + j] = b[j];
     __syncthreads();
-    const int64_t c = (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
+    const int64_t c = from + (int64_t)blockIdx.x * 16 + (threadIdx.x & 15);
     const int which = threadIdx.x >> 4;
     if (which > 1 || c >= p.N)
         return;
@@ -624,9 +625,13 @@ static hipError_t norm_grad_t(NormGradParams p, void *ws, hipStream_t s)
                            stats);
     }
 #undef LL_GRAD
-    if (p.DGATE != nullptr || p.DWPOST != nullptr || p.DWPRE != nullptr)
-        hipLaunchKernelGGL(rmsnorm_grad_finish_kernel, dim3((unsigned)(((int64_t)p.N + 15) / 16)), dim3(256), 0, s,
-                           p, groups);
+    if (p.DGATE != nullptr || p.DWPOST != nullptr || p.DWPRE != nullptr) {
+        constexpr int64_t cols = (int64_t)1 << 27;   // of a launch: work items fit 32 bits
+        for (int64_t from = 0; from < p.N; from += cols) {
+            const int64_t n = p.N - from < cols ? p.N - from : cols;
+            hipLaunchKernelGGL(rmsnorm_grad_finish_kernel, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, s, p, groups, from);
+        }
+    }
     return hipGetLastError();
 }
 

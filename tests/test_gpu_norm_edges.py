@@ -116,3 +116,21 @@ def test_gradient_without_y_takes_nothing_from_its_norm(M, N, dtype, eps):
         ll.rmsnorm_residual_grad(dxo, dh, None, w_post, gate, alpha, x, w, None, dx, None, None, dw, work, eps=eps)
         close(dx, total, size, 128, "dx")
         close(dw, sums, sum_size, 128 + M, "dw_pre")
+
+
+def test_gradient_of_a_row_past_a_launch():
+    """More columns than the finishing launch has work items for. x is 1 and -1 and dh
+    whole numbers, so that the sums over the row are exact but for its last additions,
+    and the ordinary 128 half-steps hold."""
+    N = 2 ** 28 + 1000
+    g = gen(5)
+    x = (2 * torch.randint(0, 2, (1, 1009), generator=g, device=DEV) - 1).to(BF).repeat(1, N // 1009 + 1)[:, :N]
+    dh = torch.randint(-3, 4, (1, 997), generator=g, device=DEV).to(BF).repeat(1, N // 997 + 1)[:, :N]
+    dx, dw = torch.full((1, N), 7.0, dtype=BF, device=DEV), torch.full((N,), float("nan"), device=DEV)
+    work = torch.empty((ll.rmsnorm_grad_workspace_size(1, N),), dtype=torch.uint8, device=DEV)
+    ll.rmsnorm_residual_grad(None, dh, None, None, None, 1.0, x, None, None, dx, None, None, dw, work, eps=0.0)
+    mean = (dh.double() * x.double()).mean()
+    for c in range(0, N, 1 << 26):
+        xs, ds = x[:, c:c + (1 << 26)].double(), dh[:, c:c + (1 << 26)].double()
+        close(dx[:, c:c + (1 << 26)], ds - xs * mean, ds.abs() + xs.abs() * mean.abs(), 128, f"dx from {c}")
+        close(dw[c:c + (1 << 26)], (ds * xs)[0], (ds * xs)[0].abs(), 129, f"dw_pre from {c}")
