@@ -1,5 +1,5 @@
 """Build liblinear_layer.so (the C-ABI library) for gfx950 with hipcc, and the Python
-module _call.so on top of it with the host compiler, in-tree.
+module _call.so on top of it where torch is installed, in-tree.
 
 Usage: ``python -m linear_layer_amd._build``. Cross-compiles without a GPU.
 """
@@ -40,14 +40,19 @@ def _compile(src: str) -> str:
     return obj
 
 
-def _build_call() -> None:
-    """The module that takes tensors apart for the short calls (csrc/call.cpp)."""
+def _build_call() -> bool:
+    """The module that takes tensors apart for the short calls (csrc/call.cpp), with hipcc
+    as the host's compiler; False where there is no torch, which the C library and its
+    users do without."""
     import importlib.util
     import sysconfig
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        return False
+    torch = os.path.dirname(spec.origin)
     tmp = CALL + ".tmp%d" % os.getpid()
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           os.path.join(CSRC, "call.cpp"), "-o", tmp, "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
+    cmd = [HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           os.path.join(CSRC, "call.cpp"), "-x", "none", "-o", tmp, "-I", INCLUDE, "-isystem", os.path.join(torch, "include"),
            "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
            "-I", sysconfig.get_paths()["include"], "-L", PKG, "-l:liblinear_layer.so", "-Wl,-rpath,$ORIGIN",
            "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
@@ -56,6 +61,7 @@ def _build_call() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"building _call.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALL)
+    return True
 
 
 def build(verbose: bool = False) -> str:
@@ -69,10 +75,10 @@ def build(verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _build_call()
+    call = _build_call()
     if verbose:
         print("built", LIB)
-        print("built", CALL)
+        print("built " + CALL if call else "no torch: without " + CALL)
     return LIB
 
 
