@@ -100,7 +100,7 @@ int rmsnorm_residual_grad(int M, int N, int type, const void *DXO, int lddxo, co
     if (dev.status != LL_OK)
         return dev.status;
     const NormGradParams p{Y,   w_post, gate, w_pre, X,     DXO,  DH,   DY,   DX, dgate, dw_post, dw_pre, nullptr,
-                           ldy, ldx,    lddxo, lddh, lddy,  lddx, M,    N,    alpha, eps};
+                           ldy, ldx,    lddxo, lddh, lddy,  lddx, M,    N,    alpha, eps,  0.0f};
     return status(launch_rmsnorm_grad(type, p, workspace, static_cast<hipStream_t>(stream)));
 }
 

@@ -64,9 +64,10 @@ struct NormGradParams {
     int64_t ldy, ldx, lddxo, lddh, lddy, lddx;
     int M, N;
     float alpha, eps;
+    float eps_y;                           // eps of y's norm (set by the launcher)
 };
 // Bytes of the workspace launch_rmsnorm_grad uses.
 int64_t rmsnorm_grad_workspace(int M, int N);
-hipError_t launch_rmsnorm_grad(int type, const NormGradParams &p, void *ws, hipStream_t s);
+hipError_t launch_rmsnorm_grad(int type, NormGradParams p, void *ws, hipStream_t s);
 
 }  // namespace ll

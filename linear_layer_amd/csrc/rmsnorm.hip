@@ -255,18 +255,7 @@ hipError_t launch_rmsnorm_residual(int type, const NormParams &p, hipStream_t s)
 }
 
 // ---- gradient ---------------------------------------------------------------
-
-// t of a column, and r_y of a row whose y^2 sum to `sum`. Without y both are 0, and
-// so is all that they enter: x' = x, whatever eps (1 / 0), gate and w_post hold.
-__device__ __forceinline__ float grad_scale(const NormGradParams &p, float w_post, float gate)
-{
-    return p.Y != nullptr ? p.alpha * gate * w_post : 0.0f;
-}
-__device__ __forceinline__ float grad_ry(const NormGradParams &p, float sum)
-{
-    return p.Y != nullptr ? inv_rms(sum, p.N, p.eps) : 0.0f;
-}
-
+//
 // A workgroup walks rows blockIdx.x, blockIdx.x + grid, .. and keeps its
 // columns' shares of S and of dw_pre's sum; it writes them once, as row
 // blockIdx.x of `part` ([grid][2][N] floats), and a second launch adds the
@@ -297,7 +286,7 @@ __global__ void __launch_bounds__(MAX * TEAMS) rmsnorm_grad_kernel(NormGradParam
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             sS[c][j] = sP[c][j] = 0.0f;
-            t[c][j] = grad_scale(p, t[c][j], g[j]);
+            t[c][j] *= p.alpha * g[j];
         }
     }
     // The next row is on its way while this one is worked on, since the sums have
@@ -333,7 +322,7 @@ __global__ void __launch_bounds__(MAX * TEAMS) rmsnorm_grad_kernel(NormGradParam
         if (m + stride < p.M)
             fetch(m + stride);
         block_sum<WAVE, 0>(s, lds);
-        const float ry = grad_ry(p, s[0]);
+        const float ry = inv_rms(s[0], N, p.eps_y);
         float q[2] = {0.0f, 0.0f};   // sums of x'^2 and of dh * w_pre * x'
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -419,7 +408,7 @@ struct GradCols {
         load_vec(p.w_pre, col, p.N, 1.0f, wp);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-            t[j] = grad_scale(p, t[j], g[j]);
+            t[j] *= p.alpha * g[j];
     }
     __device__ __forceinline__ void row(const NormGradParams &p, int64_t m, int64_t col)
     {
@@ -453,7 +442,7 @@ __global__ void __launch_bounds__(NT) rmsnorm_grad_stats_kernel(NormGradParams p
             s[0] = __builtin_fmaf(v.y[j], v.y[j], s[0]);
     }
     block_sum<false, 0>(s, lds);
-    r.ry = grad_ry(p, s[0]);
+    r.ry = inv_rms(s[0], p.N, p.eps_y);
     for (int64_t col = 8 * (int64_t)threadIdx.x; col < p.N; col += 8 * NT) {
         v.row(p, m, col);
         v.vectors(p, col);
@@ -635,8 +624,14 @@ static hipError_t norm_grad_t(NormGradParams p, void *ws, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_rmsnorm_grad(int type, const NormGradParams &p, void *ws, hipStream_t s)
+hipError_t launch_rmsnorm_grad(int type, NormGradParams p, void *ws, hipStream_t s)
 {
+    p.eps_y = p.eps;
+    if (p.Y == nullptr) {   // x' = x: y is 0, so is t, and r_y a number, whatever eps, gate and w_post hold
+        p.w_post = p.gate = nullptr;
+        p.alpha = 0.0f;
+        p.eps_y = 1.0f;
+    }
     if (type == LL_TYPE_F32)
         return norm_grad_t<LL_TYPE_F32>(p, ws, s);
     if (type == LL_TYPE_F16)
