@@ -627,7 +627,8 @@ static hipError_t norm_grad_t(NormGradParams p, void *ws, hipStream_t s)
 hipError_t launch_rmsnorm_grad(int type, NormGradParams p, void *ws, hipStream_t s)
 {
     p.eps_y = p.eps;
-    if (p.Y == nullptr) {   // x' = x: y is 0, so is t, and r_y a number, whatever eps, gate and w_post hold
+    // x' = x, or no rows: y is 0, so is t, and r_y a number, whatever eps, gate and w_post hold
+    if (p.Y == nullptr || p.M <= 0) {
         p.w_post = p.gate = nullptr;
         p.alpha = 0.0f;
         p.eps_y = 1.0f;

@@ -134,3 +134,16 @@ def test_gradient_of_a_row_past_a_launch():
         xs, ds = x[:, c:c + (1 << 26)].double(), dh[:, c:c + (1 << 26)].double()
         close(dx[:, c:c + (1 << 26)], ds - xs * mean, ds.abs() + xs.abs() * mean.abs(), 128, f"dx from {c}")
         close(dw[c:c + (1 << 26)], (ds * xs)[0], (ds * xs)[0].abs(), 129, f"dw_pre from {c}")
+
+
+def test_gradient_without_rows_is_zero_whatever_the_vectors_hold():
+    """The C call, with pointers to matrices of no rows."""
+    N = 70
+    m, bad = torch.empty((1, N), device=DEV), torch.full((N,), float("inf"), device=DEV)
+    vec = [torch.full((N,), float("nan"), device=DEV) for _ in range(3)]
+    p, b = m.data_ptr(), bad.data_ptr()
+    st = ll.load().rmsnorm_residual_grad(0, N, ll.TYPE_F32, p, N, p, N, p, N, b, b, 0.5, p, N, b, 1e-5, p, N, p, N,
+                                         *(v.data_ptr() for v in vec), None, 0, torch.cuda.current_stream().cuda_stream)
+    assert st == ll.OK
+    for v in vec:
+        assert bool((v == 0).all())
