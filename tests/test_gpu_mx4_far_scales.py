@@ -101,3 +101,28 @@ def test_not_finite_beside_the_largest_scales(M, N, K, which):
             bv = values(codes, scales, K)[others]
             want, size = 1.5 * (av[1:] @ bv.T) + 0.5 * c0[1:, others], 1.5 * (np.abs(av[1:]) @ np.abs(bv).T) + 0.5 * np.abs(c0[1:, others])
         assert (np.abs(got[1:, others] - want) <= (K + 8) * (HALF_STEP * size + 2.0 ** -126)).all()
+
+
+@pytest.mark.parametrize("which", ["mx4", "f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 6184), (1, 30, 100), (5, 33, 1000), (33, 300, 11008), (70, 90, 31), (1300, 1700, 128),
+                                   (1000, 1500, 1577), (2100, 2200, 1600)])
+def test_quantised_nan_reaches_the_product(M, N, K, which):
+    """A block that held a NaN or an infinity has codes of 0 under the NaN scale: its row
+    is NaN in the product all the same, and no other, also against zeros of A."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(7)
+    w = torch.randn((N, K), generator=g, device=DEV)
+    w[3, K // 2], w[N - 1, K - 1] = float("nan"), float("-inf")
+
+    def pack(t):
+        (c, s) = ll.mx4_shapes(*t.shape)
+        return ll.mx4_quantize(t, *(torch.empty(v, dtype=torch.uint8, device=DEV) for v in (c, s)))
+
+    x = torch.randn((M, K), generator=g, device=DEV)
+    x[M // 2] = 0
+    a = pack(x) if which == "mx4" else (x.to(TYPES[which]),)
+    C = torch.zeros((M, N), device=DEV)
+    product(which, a, *pack(w), C, K)
+    want = torch.zeros((M, N), dtype=torch.bool, device=DEV)
+    want[:, [3, N - 1]] = True
+    assert torch.equal(torch.isnan(C), want) and bool(torch.isfinite(C[~want]).all())
