@@ -18,7 +18,7 @@
 // bytes 104 .. 140 only (2^-23 .. 2^13); past those the wave splits A's values
 // into two bfloat16 parts instead (11 bits of fraction into 8 and 3) and
 // multiplies twice, which is exact too. The two largest scales pass bfloat16's
-// range as well: see far_dot.
+// range as well: see far_scale.
 #include "linear_layer.h"
 #include "gemm_mx4.hpp"
 
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
                 const int64_t m = m0 + i / QUADS, n = n0 + i % QUADS * 4;
                 float *at = &part[0][4 * i];
                 if (m < p.M)
-                    settle4<A>(p, *reinterpret_cast<f32x4 *>(at), at, m, n, begin * 4 * J, min(nunit * 4 * J, nblk));
+                    settle4<A, LONG>(p, *reinterpret_cast<f32x4 *>(at), at, m, n, begin * 4 * J, min(nunit * 4 * J, nblk));
             }
     for (int i = tid; i < BM * QUADS; i += 64 * W) {
         const int64_t m = m0 + i / QUADS, n = n0 + i % QUADS * 4;
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(64 * W) gemm_mx4_stream_kernel(MxParams p)
         }
         if constexpr (!MX && W > 1)
             if (__builtin_expect(!finite4(v), 0))
-                v = settle4<A>(p, v, &part[0][4 * i], m, n, begin * 4 * J, min(nunit * 4 * J, nblk));
+                v = settle4<A, LONG>(p, v, &part[0][4 * i], m, n, begin * 4 * J, min(nunit * 4 * J, nblk));
         if (p.splits > 1) {
             float *dst = p.ws + ((int64_t)split * p.M + m) * p.N + n;
             if (n + 4 <= p.N) {
@@ -503,7 +503,7 @@ __global__ void __launch_bounds__(64 * KW * NW) gemm_mx4_rows_kernel(MxParams p)
             sum += sums[wave + k][lane];
         if constexpr (!MX)
             if (__builtin_expect(!finite(sum), 0))
-                sum = far_dot<A>(sum, p.A, p.B + n * p.ldb, p.SB + n * p.ldsb, 0, nblk, K);
+                sum = far_dot<A, true>(sum, p.A, p.B + n * p.ldb, p.SB + n * p.ldsb, 0, nblk, K);
         p.C[n] = finish(p, sum, p.C + n);
     }
 }

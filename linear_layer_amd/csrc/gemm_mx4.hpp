@@ -89,50 +89,17 @@ __device__ __forceinline__ void turn4(u32x4 &v)
 __device__ __forceinline__ bool f16_scale_ok(uint32_t s) { return s - 104u <= 36u; }
 
 // Scale bytes 253 and 254: values reach 6 * 2^127, past bfloat16 and FP32, and
-// decode8 makes them infinite. They are rare, so nothing looks for them before a sum
-// has come out infinite or NaN, as any such value makes it: then its inner product
-// over the blocks [b0, b1) is taken again, value by value, those blocks decoded 2^-4
-// lower and their products (exact, and 2^-13 at least) times 2^4. Returns the sum as
-// it was where its row of B has no such scale. (Looked for in the loops they cost
-// the bfloat16 products 2 to 7 %.)
+// decode8 makes them infinite. Such a block is decoded 2^-4 lower instead, and its
+// products (exact, and 2^-13 at least) enter their sum times 2^4. They are rare, so
+// nothing looks for them before a sum has come out infinite or NaN, as any such value
+// makes it (looked for in the loops they cost the bfloat16 products 2 to 7 %).
 __device__ __forceinline__ bool far_scale(uint32_t s) { return s - 253u < 2u; }
+// The scale to decode with, and what is left of it.
+__device__ __forceinline__ float near_part(uint32_t s) { return __uint_as_float((far_scale(s) ? s - 4u : s) << 23); }
+__device__ __forceinline__ float far_part(uint32_t s) { return far_scale(s) ? 16.0f : 1.0f; }
 
 __device__ __forceinline__ bool finite(float v) { return __builtin_fabsf(v) < __builtin_inff(); }
 
-template <int A>
-__device__ __forceinline__ float far_dot(float sum, const uint8_t *a, const uint8_t *b, const uint8_t *sb, int b0, int b1,
-                                         int K)
-{
-    bool far = false;
-#pragma unroll 1
-    for (int blk = b0; blk < b1; ++blk)
-        far |= far_scale(sb[blk]);
-    if (!far)
-        return sum;
-    sum = 0.0f;
-#pragma unroll 1
-    for (int64_t k = (int64_t)b0 * kMxBlock; k < K && k < (int64_t)b1 * kMxBlock; ++k) {
-        const uint32_t s = sb[k / kMxBlock], code = b[k / 2] >> (4 * (k & 1)) & 15u;
-        const uint16_t h = reinterpret_cast<const uint16_t *>(a)[k];
-        const float x = A == MXA_F16 ? to_f32<LL_TYPE_F16>(h) : to_f32<LL_TYPE_BF16>(h);
-        const float y = __uint_as_float(decode8<true>(code, __uint_as_float((far_scale(s) ? s - 4u : s) << 23))[0] << 16);
-        sum = __builtin_fmaf(x * y, far_scale(s) ? 16.0f : 1.0f, sum);
-    }
-    return sum;
-}
-
-// Four neighbouring sums of row m and columns n .. n+3 (those inside N), in LDS that
-// the calling lane alone uses, and all four after far_dot had those that are not finite.
-template <int A>
-__device__ __forceinline__ f32x4 settle4(const MxParams &p, const f32x4 &v, float *at, int64_t m, int64_t n, int b0, int b1)
-{
-    *reinterpret_cast<f32x4 *>(at) = v;
-#pragma unroll 1
-    for (int j = 0; j < 4; ++j)
-        if (n + j < p.N && !finite(at[j]))
-            at[j] = far_dot<A>(at[j], p.A + m * p.lda, p.B + (n + j) * p.ldb, p.SB + (n + j) * p.ldsb, b0, b1, p.K);
-    return *reinterpret_cast<f32x4 *>(at);
-}
 // Whether sums are finite, by one comparison of theirs (false too where they overflow
 // together, which costs a look at each).
 __device__ __forceinline__ bool finite4(const f32x4 &v) { return finite(v[0] + v[1] + v[2] + v[3]); }
@@ -246,6 +213,63 @@ __device__ __forceinline__ u32x4 load_halves(const uint8_t *row, int64_t k, int 
         }
     }
     return v;
+}
+
+// A sum that is not finite, over the blocks [b0, b1) of a row of 16-bit A and a row of
+// B: taken again by vector FMAs if a block has a far scale and none is NaN.
+template <int A, bool LONG>
+__device__ __forceinline__ float far_dot(float sum, const uint8_t *a, const uint8_t *b, const uint8_t *sb, int b0, int b1,
+                                         int K)
+{
+    bool far = false, nan = false;
+#pragma unroll 1
+    for (int blk = b0; blk < b1; ++blk) {
+        const uint32_t s = sb[blk];
+        far |= far_scale(s);
+        nan |= s == 255u;
+    }
+    if (!far || nan)
+        return sum;
+    sum = 0.0f;
+    auto half = [&](const uint16_t h) __attribute__((always_inline)) { return A == MXA_F16 ? to_f32<LL_TYPE_F16>(h) : to_f32<LL_TYPE_BF16>(h); };
+    if constexpr (LONG) {
+#pragma unroll 1
+        for (int blk = b0; blk < b1; ++blk) {
+            const u32x4 q = load_block<true>(b, blk, K);
+            const uint32_t s = sb[blk];
+            float part = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const u32x4 x = load_halves<true>(a, (int64_t)blk * kMxBlock + 8 * t, K), y = decode8<true>(q[t], near_part(s));
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    part = __builtin_fmaf(half((uint16_t)(x[j / 2] >> (16 * (j & 1)))),
+                                          to_f32<LL_TYPE_BF16>((uint16_t)(y[j / 2] >> (16 * (j & 1)))), part);
+            }
+            sum = __builtin_fmaf(part, far_part(s), sum);
+        }
+    } else {   // K < 32: one block, value by value
+#pragma unroll 1
+        for (int k = 0; k < K; ++k) {
+            const uint32_t y = decode8<true>(b[k / 2] >> (4 * (k & 1)) & 15u, near_part(sb[0]))[0];
+            sum = __builtin_fmaf(half(reinterpret_cast<const uint16_t *>(a)[k]), to_f32<LL_TYPE_BF16>((uint16_t)y), sum);
+        }
+        sum *= far_part(sb[0]);
+    }
+    return sum;
+}
+
+// Four neighbouring sums of row m and columns n .. n+3 (those inside N), in LDS that
+// the calling lane alone uses, and all four after far_dot had those that are not finite.
+template <int A, bool LONG>
+__device__ __forceinline__ f32x4 settle4(const MxParams &p, const f32x4 &v, float *at, int64_t m, int64_t n, int b0, int b1)
+{
+    *reinterpret_cast<f32x4 *>(at) = v;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j)
+        if (n + j < p.N && !finite(at[j]))
+            at[j] = far_dot<A, LONG>(at[j], p.A + m * p.lda, p.B + (n + j) * p.ldb, p.SB + (n + j) * p.ldsb, b0, b1, p.K);
+    return *reinterpret_cast<f32x4 *>(at);
 }
 
 }  // namespace ll

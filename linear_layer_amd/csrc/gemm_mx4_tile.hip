@@ -63,8 +63,8 @@ constexpr int tile_lds(int BM, int BN, int steps, int nbuf)
 }
 
 // The BM x BN block of C from row m0 and column n0 on, by WGM x WGN waves. For
-// binary16 A it returns false, with nothing stored, where a scale is
-// past what binary16 can take.
+// 16-bit A it returns false, with nothing stored, where a scale is past what A's
+// type can take (of bfloat16: the far ones).
 template <int A, int BM, int BN, int STEPS, int NBUF, int WGM, int WGN, bool DMA>
 __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t n0, uint8_t *raw)
 {
@@ -439,7 +439,20 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
                 wide |= !f16_scale_ok(o.sb[f / 4] >> (8 * (f % 4)) & 0xffu);
         multiply(o, [](auto) {});
     }
-    if (A == MXA_F16 && __syncthreads_or(wide))
+    if constexpr (A == MXA_BF16) {
+        static_assert(WTN == 64, "a lane to each of the wave's rows of B");
+        if (__builtin_expect(__any(!all_finite(acc)), 0)) {
+            const uint8_t *row = sbbase + min(wn * WTN + lane, nleft - 1) * p.ldsb;
+            bool nan = false;   // (a row with a NaN block is NaN in any case)
+#pragma unroll 1
+            for (int blk = 0; blk < nblk; ++blk) {
+                wide |= far_scale(row[blk]);
+                nan |= row[blk] == 255;
+            }
+            wide &= !nan;
+        }
+    }
+    if (!MX && __syncthreads_or(wide))
         return false;
 
     // ---- epilogue: lane l has row l % 16 and columns 4 * (l / 16) .. +3 of a
@@ -452,20 +465,7 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
     static_assert(NW * 32 * LDC * 4 <= sizeof(Lds), "the waves' rows fit the stages");
     float *mine = reinterpret_cast<float *>(&lds) + wave * (32 * LDC);
     const int64_t n = nb + wn * WTN + 4 * r16;
-    // bfloat16 A: whether a sum of this wave is not finite and which of its rows of B, a
-    // lane each, have a far scale
-    uint64_t far = 0;
-    if constexpr (A == MXA_BF16) {
-        if (__builtin_expect(__any(!all_finite(acc)), 0)) {
-            const uint8_t *row = sbbase + min(wn * WTN + lane, nleft - 1) * p.ldsb;
-            bool any = false;
-#pragma unroll 1
-            for (int blk = 0; blk < nblk; ++blk)
-                any |= far_scale(row[blk]);
-            far = __ballot(any);
-        }
-    }
-    const bool plain = p.beta == 0.0f && ma == m0 && nb == n0 && mleft == BM && nleft == BN && far == 0;
+    const bool plain = p.beta == 0.0f && ma == m0 && nb == n0 && mleft == BM && nleft == BN;
 #pragma unroll
     for (int i = 0; i < FM; i += 2) {
 #pragma unroll
@@ -474,7 +474,7 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
             for (int j = 0; j < FN; ++j)
                 *reinterpret_cast<f32x4 *>(&mine[(16 * h + r16) * LDC + 16 * j + 4 * g]) = acc[i + h][j];
         float *dst = p.C + (ma + wm * WTM + 16 * i + g) * p.ldc + n;
-        float *from = &mine[g * LDC + 4 * r16];
+        const float *from = &mine[g * LDC + 4 * r16];
         if (plain) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -488,26 +488,22 @@ __device__ __forceinline__ bool mx4_tile(const MxParams &p, int64_t m0, int64_t 
 #pragma unroll 1
             for (int q = 0; q < 8; ++q) {
                 const int64_t m = ma + wm * WTM + 16 * i + 4 * q + g;
-                if (m >= m0 && m < p.M) {
-                    f32x4 v = *reinterpret_cast<const f32x4 *>(from + 4 * q * LDC);
-                    if constexpr (A == MXA_BF16)
-                        if ((far >> (4 * r16) & 15) != 0 && !finite4(v))
-                            v = settle4<A>(p, v, from + 4 * q * LDC, m, n, 0, nblk);
-                    finish4(p, v, dst + 4 * q * p.ldc, n0 - n, p.N - n);
-                }
+                if (m >= m0 && m < p.M)
+                    finish4(p, *reinterpret_cast<const f32x4 *>(from + 4 * q * LDC), dst + 4 * q * p.ldc, n0 - n, p.N - n);
             }
         }
     }
     return true;
 }
 
-// binary16 A against scales past its range: through the bfloat16 instruction, A's
-// values in two parts. A wave takes its rows 32 at a time (few registers, so that
-// the path above keeps them), operands straight from memory.
-template <int BM, int BN, int WGM, int WGN>
-__device__ __forceinline__ void mx4_tile_wide(const MxParams &p, int64_t m0, int64_t n0, uint8_t *raw)
+// 16-bit A against scales past its range: through the bfloat16 instruction, binary16
+// values in two parts, and a block's products apart from the sum where a scale is far. A
+// wave takes its rows 32 at a time (few registers, so that the path above keeps them),
+// operands straight from memory.
+template <int A, int BM, int BN, int WGM, int WGN>
+__device__ __forceinline__ void mx4_tile_wide(const MxParams &p, int64_t m0, int64_t n0)
 {
-    constexpr int FM = 2, FN = BN / WGN / 16, NT = 64 * WGM * WGN;
+    constexpr int FM = 2, FN = BN / WGN / 16;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int g = lane >> 4, r16 = lane & 15;
     const int64_t n = n0 + wave % WGN * (BN / WGN);
@@ -527,37 +523,51 @@ __device__ __forceinline__ void mx4_tile_wide(const MxParams &p, int64_t m0, int
 #pragma unroll
             for (int a = 0; a < FM; ++a) {
                 const int64_t row = m + 16 * a + r16 < p.M ? m + 16 * a + r16 : p.M - 1;
-                split8(load_halves<true>(p.A + row * p.lda, (int64_t)blk * kMxBlock + 8 * g, p.K), hi[a], lo[a]);
+                hi[a] = load_halves<true>(p.A + row * p.lda, (int64_t)blk * kMxBlock + 8 * g, p.K);
+                if constexpr (A == MXA_F16)
+                    split8(hi[a], hi[a], lo[a]);
             }
+            auto product = [&](const u32x4 &d, int a, f32x4 c) __attribute__((always_inline)) {
+                if constexpr (A == MXA_F16)
+                    c = mma_bf16(d, lo[a], c);
+                return mma_bf16(d, hi[a], c);
+            };
 #pragma unroll
             for (int b = 0; b < FN; ++b) {
                 const int64_t row = n + 16 * b + r16 < p.N ? n + 16 * b + r16 : p.N - 1;
                 const u32x4 v = load_block<true>(p.B + row * p.ldb, blk, p.K);
                 const uint32_t q = g < 2 ? (g == 0 ? v[0] : v[1]) : (g == 2 ? v[2] : v[3]);
-                const u32x4 d = decode8<true>(q, __builtin_bit_cast(float, (uint32_t)p.SB[row * p.ldsb + blk] << 23));
+                const uint32_t s = p.SB[row * p.ldsb + blk];
+                const u32x4 d = decode8<true>(q, near_part(s));
+                if (__any(far_scale(s))) {
+                    float up[4];   // of this lane's four columns of C, rows 4 g .. +3 of B's 16
 #pragma unroll
-                for (int a = 0; a < FM; ++a) {
-                    acc[a][b] = mma_bf16(d, lo[a], acc[a][b]);
-                    acc[a][b] = mma_bf16(d, hi[a], acc[a][b]);
+                    for (int r = 0; r < 4; ++r)
+                        up[r] = __shfl(far_part(s), 4 * g + r);
+#pragma unroll
+                    for (int a = 0; a < FM; ++a) {
+                        const f32x4 c = product(d, a, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            acc[a][b][r] = __builtin_fmaf(c[r], up[r], acc[a][b][r]);
+                    }
+                } else {
+#pragma unroll
+                    for (int a = 0; a < FM; ++a)
+                        acc[a][b] = product(d, a, acc[a][b]);
                 }
             }
         }
-        // through LDS, a thread's own, so that the sums can be told apart by a loop
-        f32x4 *mine = reinterpret_cast<f32x4 *>(raw) + threadIdx.x;
 #pragma unroll
-        for (int a = 0; a < FM; ++a)
-#pragma unroll
-            for (int b = 0; b < FN; ++b)
-                mine[(a * FN + b) * NT] = acc[a][b];
-#pragma unroll 1
-        for (int j = 0; j < FM * FN; ++j) {
-            const int64_t row = m + 16 * (j / FN) + r16, col = n + 16 * (j % FN) + 4 * g;
-            f32x4 v = mine[j * NT];
+        for (int a = 0; a < FM; ++a) {
+            const int64_t row = m + 16 * a + r16;
             if (row >= p.M)
                 continue;
-            if (!finite4(v))
-                v = settle4<MXA_F16>(p, v, reinterpret_cast<float *>(mine + j * NT), row, col, 0, nblk);
-            finish4(p, v, p.C + row * p.ldc + col, 0, p.N - col);
+#pragma unroll
+            for (int b = 0; b < FN; ++b) {
+                const int64_t col = n + 16 * b + 4 * g;
+                finish4(p, acc[a][b], p.C + row * p.ldc + col, 0, p.N - col);
+            }
         }
     }
 }
@@ -566,11 +576,9 @@ template <int A, int BM, int BN, int NBUF, int WGM, int WGN, bool DMA>
 __device__ __forceinline__ void mx4_tile_any(const MxParams &p, int64_t m0, int64_t n0, uint8_t *raw)
 {
     const bool done = mx4_tile<A, BM, BN, 2, NBUF, WGM, WGN, DMA>(p, m0, n0, raw);
-    if constexpr (A == MXA_F16)
-        if (!done) {
-            static_assert(2 * (BN / WGN / 16) * 64 * WGM * WGN * 16 <= tile_lds<A>(BM, BN, 2, NBUF), "the waves' sums fit the stages");
-            mx4_tile_wide<BM, BN, WGM, WGN>(p, m0, n0, raw);
-        }
+    if constexpr (A != MXA_MX4)
+        if (!done)
+            mx4_tile_wide<A, BM, BN, WGM, WGN>(p, m0, n0);
 }
 
 // One workgroup a tile, in an order that keeps an XCD's tiles together. The last
