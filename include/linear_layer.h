@@ -314,13 +314,15 @@ int mx4_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
  * (N-by-K, the [out][in] layout of a weight) in MX4, FP32 sums and FP32 C.
  * gemm_f16mx4f32_nt, gemm_bf16mx4f32_nt — the same with A in binary16 or
  * bfloat16 (bit patterns; lda >= max(1, K) elements) and B in MX4: every
- * decoded value of B enters its products exactly, whatever its scale.
+ * decoded value of B enters its products exactly, whatever its scale (those past
+ * bfloat16's range too, more slowly).
  *
  *   SA, SB    the scales of A and B; ldsa, ldsb >= max(1, ceil(K/32)) bytes.
  *   lda, ldb  bytes between rows of codes, >= max(1, ceil(K/2)).
  * Other arguments, rules and errors as gemm_f32: with beta == 0 C is not
  * read, K == 0 or alpha == 0 gives C = beta*C and reads neither operand, C
- * must not overlap an input. One launch, nothing allocated; the summation
+ * must not overlap an input. One launch (several where one cannot count the work
+ * items: 2^27 rows of A or B and more), nothing allocated; the summation
  * order is fixed by the shape and the alignment, so equal calls give equal
  * results. Rows (of A, of B) 16 bytes aligned take direct copies into LDS when
  * the product is large; any other alignment is taken too.

@@ -40,7 +40,7 @@ namespace ll {
 // What bounds it is the rate at which a CU reads its rows of A and B from L2,
 // 20 to 34 bytes a ns: hence tiles that are as high as M, wide enough not to read
 // A too often, and as many workgroups as CUs (33 x 4096 x 11008 in binary16: 48 x 64
-// tiles in four shares 15.0 us and 4.6 to join, 32 x 32 tiles in one 28).
+// tiles in four shares 15.2 us and 3.9 to join, 32 x 32 tiles in one 28).
 //
 // Rows past M or N read the last row instead; their sums are not stored. binary16
 // A meets a scale past its range: the wave leaves the loop and does the rest of its
@@ -346,9 +346,11 @@ constexpr int64_t rows_lds(int a, int64_t K)
 
 // ---------------------------------------------------------------------------
 // Row kernel, for a decode step's one row of A: HBM bounds it, and
-// memory serves whole rows better than the streaming kernel's 64 bytes of 16 (B
-// 28672 x 8192 in 4 bits both 24.5 us, 5.1 TB/s, against 32.4; with bfloat16 A 24.7
-// against 41.0; B 11008 x 4096 6.6 and 7.4 us against 9.2 and 10.9). A wave takes R rows of B, 64 blocks of
+// memory serves whole rows better than the streaming kernel's 64 bytes of 16. With
+// weights that cycle through more than the cache: B 28672 x 8192 24.7 us under a 4-bit
+// row, 5.1 TB/s (streaming 32.4), 25.4 under a bfloat16 one (41.0), 29.7 under binary16,
+// in two parts; B 11008 x 4096, 24 MB, 6.5, 7.3 and 8.3 (streaming 9.2 and 10.9 for the
+// first two), and from the cache 3.8, 5.1 and 6.0. A wave takes R rows of B, 64 blocks of
 // one at a time: lane l block l, a load of 1 KiB. The matrix instruction then has for
 // its 16 rows of B 16 sets of four blocks of the same row, and for its 16 rows of A
 // the same sets of A's: the sum of its result's diagonal is their inner

@@ -15,13 +15,17 @@
 // registers so that one LDS read gives a lane the scales of all its rows, which the
 // instruction picks by byte.
 //
-// What bounds it: with both operands in 4 bits the rate at which L2 fills the CUs
-// (64 KiB a stage of 256 x 256 in 1.87 us, 34 bytes a ns and CU; the matrix cores are
-// busy 37 % of the time, a third stage, 128 x 256 tiles in three stages or twice as
-// many workgroups were no faster) and C's 4 bytes a value, which leave in whole rows
-// of 256 bytes through LDS: 8192^3 336 us, 3.3 PFLOP/s, of which 225 are the stages;
-// writing C in the instruction's 64-byte pieces took 30 us more. With bfloat16 A the
-// matrix cores' power limit: 8192^3 790 us, 1.39 PFLOP/s, 2047 x 11008 x 4096 157 us.
+// What bounds it: with both operands in 4 bits the rate at which L2 fills the CUs.
+// 8192 x 8192 x K takes 48 us and 32.8 for every 1024 of K (512: 64, 2048: 109, 8192: 311, 3.5
+// PFLOP/s; on inputs that change from pass to pass 336 to 341): 2.05 us a stage of 256 x 256,
+// 64 KiB, 32 bytes a ns and CU, with the matrix cores busy 40 % of the time; a third
+// stage, 128 x 256 tiles in three stages or twice as many workgroups were no faster. The
+// 48 us are C's 268 MB, which one workgroup a CU does not write behind another tile's
+// stages; they leave in whole rows of 256 bytes through LDS (in the instruction's 64-byte
+// pieces 30 us more). A workgroup that fetches its next tile meanwhile has not been
+// tried. LDS bank conflicts are 96 cycles a stage and 1024 an epilogue, 2.5 % of a tile's
+// time. With bfloat16 A the matrix cores' power limit: 8192^3 773 us, 1.42 PFLOP/s, 2047 x
+// 11008 x 4096 153 to 158 us.
 #include "linear_layer.h"
 #include "gemm_mx4.hpp"
 
