@@ -39,9 +39,12 @@ extern "C" {
 #define LL_ERR_UNSUPPORTED_ARCH 3/* the current device is not gfx950 (MI355X class) */
 #define LL_ERR_LAUNCH 4          /* the HIP runtime reported an error at launch */
 
-/* Activations for linear_bias_act. */
+/* Activations: of linear_bias_act the first two, of linear16_nt and its gradient all. */
 #define LL_ACT_NONE 0
 #define LL_ACT_RELU 1
+#define LL_ACT_GELU 2       /* z * (1 + erf(z / sqrt(2))) / 2 */
+#define LL_ACT_GELU_TANH 3  /* z * (1 + tanh(sqrt(2 / pi) * (z + 0.044715 z^3))) / 2 */
+#define LL_ACT_SILU 4       /* z / (1 + exp(-z)) */
 
 /*
  * gemm_f32 — C = alpha * A * B + beta * C in FP32.
@@ -420,6 +423,109 @@ int rmsnorm_residual_grad(int M, int N, int type, const void *DXO, int lddxo, co
 /* Bytes of workspace rmsnorm_residual_grad needs (at most 8 * 1024 * N for N
  * up to 8192); -1 for a negative size. */
 int64_t ll_rmsnorm_grad_workspace_size(int M, int N);
+
+/*
+ * Microscaled 8-bit floating point (MX8): rows of values in blocks of 32 (the last
+ * one may be shorter), a byte a value and a scale byte s a block. A byte is an
+ * E4M3 number (sign, four bits of exponent with bias 7, three of fraction; up
+ * to 448, no infinities, 0x7f and 0xff NaN), the block's values are the
+ * numbers times 2^(s - 127), and s = 255 makes all of them NaN. A row of K values has K
+ * bytes of codes and ceil(K/32) of scales. The encoding is the one that the
+ * OCP Microscaling Formats specification calls MXFP8. Leading dimensions of
+ * codes and scales are in bytes; neither needs any alignment.
+ *
+ * mx8_quantize — X (M-by-K, `type`, ldx >= max(1, K) elements) into MX8. A
+ * block whose largest magnitude is t gets the smallest scale 2^e, e >= -127,
+ * with t <= 448 * 2^e, so no value is clipped, and each value v the code
+ * nearest to v / 2^e, ties to the even code (t = 0: e = -127). A block that holds an
+ * infinity or a NaN gets the scale byte 255 and codes 0.
+ * mx8_dequantize — Y (M-by-K, `type`) = the values that codes and scales
+ * stand for. FP32 holds them exactly down to its smallest subnormal, bfloat16 down
+ * to its own; binary16 rounds those below 2^-14 and overflows to infinity
+ * past 65504.
+ * Outputs must not overlap inputs or each other. M == 0 or K == 0: LL_OK,
+ * touches nothing.
+ */
+int mx8_quantize(int M, int K, int type, const void *X, int ldx,
+                 uint8_t *codes, int ldq, uint8_t *scales, int lds, void *stream);
+int mx8_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *scales, int lds,
+                   int type, void *Y, int ldy, void *stream);
+
+/*
+ * The 16-bit layer: a fully-connected layer with its write-back, and its gradients,
+ * in binary16 or bfloat16 (`type`: LL_TYPE_F16 or LL_TYPE_BF16) with FP32 sums; dense,
+ * or by groups of rows, as the experts of a mixture have them.
+ *
+ *   groups, offsets   NULL with groups 1: one weight for all M rows. Otherwise
+ *           groups + 1 ascending row numbers in DEVICE memory (4-byte aligned):
+ *           group g has the rows offsets[g] .. offsets[g+1] - 1 and a weight of its
+ *           own. A group may be empty. Rows before offsets[0] and from
+ *           offsets[groups] on belong to none: nothing of theirs is read or
+ *           written. The numbers are read by the kernels (no copy to the host); one
+ *           outside 0 .. M is taken as the nearer of the two, and one below its
+ *           predecessor as that. At most LL_MAX_GROUPS groups; 0 groups: nothing happens.
+ *   W       N-by-K of `type` ([out][in]), ldw >= max(1, K); group g's is stride_w * g
+ *           elements after the first (0: one weight for all groups).
+ * Sizes up to 2^31 - 1025 (and as many tiles as one launch takes); operands
+ * need only the alignment of their elements. Where rows of X and W (of dZ and W, of dZ and X) are
+ * whole multiples of 16 bytes on 16 bytes, copies go straight into LDS;
+ * otherwise through registers, more slowly. Sums are taken in an order that
+ * the shape, the alignment and the groups fix: equal calls give equal results.
+ *
+ * linear16_nt — Z = X * W^T + bias, Y = act(Z) + R.
+ *   X       M-by-K of `type`, ldx >= max(1, K).
+ *   bias    groups-by-N fp32, contiguous, or NULL.
+ *   act     LL_ACT_*; ReLU maps z <= 0 (and NaN) to +0.0.
+ *   R, Y    M-by-N of `ytype`, which is `type` or LL_TYPE_F32. R may be NULL
+ *           (nothing is added), or Y itself (same ld).
+ *   Z       M-by-N of `type`, or NULL: Z as the way back needs it, and / or
+ *   ZQ, ZS  the same in MX8 (M-by-N codes, M-by-ceil(N/32) scales), from its
+ *           FP32 sums; both or neither.
+ * Outputs must not overlap inputs or each other otherwise. K == 0: Z = bias.
+ *
+ * linear16_grad_act — dZ = dY * act'(Z), and dbias[g] = the sums of dZ (before its
+ * rounding) over the rows of group g.
+ *   DY      M-by-N of `ytype` (`type` or LL_TYPE_F32).
+ *   Z, or ZQ and ZS   as linear16_nt wrote them; not read, and may all be
+ *           NULL, for LL_ACT_NONE.
+ *   DZ      M-by-N of `type`, or NULL. It may be DY (of that type) or Z itself, same ld.
+ *   dbias   groups-by-N fp32, contiguous, or NULL; an empty group's is 0. It
+ *           needs a workspace of ll_linear16_grad_act_workspace_size(M, N,
+ *           groups) bytes, 16-byte aligned, overlapping nothing; its contents
+ *           need no preparation. Calls that share one must not overlap in time.
+ *
+ * linear16_grad_input — dX (M-by-K of `xtype`: `type` or LL_TYPE_F32) = dZ
+ * (M-by-N of `type`) * W.
+ *
+ * linear16_grad_weight — dW = dZ^T * X + beta * dW, N-by-K of `wtype` (`type` or
+ * LL_TYPE_F32), lddw >= max(1, K); group g's from its own rows, stride_dw * g elements
+ * after the first. With beta == 0 dW is not read; an empty group's is beta * dW.
+ *   X, or XQ and XS   M-by-K of `type`, or in MX8. Values in MX8 enter their
+ *           products as `type` holds them: bfloat16 exactly down to its
+ *           subnormals, binary16 rounded below 2^-14 and held at +-65504.
+ */
+#define LL_MAX_GROUPS (1 << 20)
+int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx,
+                int groups, const int32_t *offsets,
+                const uint16_t *W, int ldw, int64_t stride_w, const float *bias, int act,
+                int ytype, const void *R, int ldr, void *Y, int ldy,
+                uint16_t *Z, int ldz, uint8_t *ZQ, int ldzq, uint8_t *ZS, int ldzs,
+                void *stream);
+int64_t ll_linear16_grad_act_workspace_size(int M, int N, int groups);
+int linear16_grad_act(int M, int N, int type, int act, int ytype, const void *DY, int lddy,
+                      int groups, const int32_t *offsets,
+                      const uint16_t *Z, int ldz, const uint8_t *ZQ, int ldzq, const uint8_t *ZS, int ldzs,
+                      uint16_t *DZ, int lddz, float *dbias,
+                      void *workspace, int64_t workspace_bytes, void *stream);
+int linear16_grad_input(int M, int N, int K, int type, const uint16_t *DZ, int lddz,
+                        int groups, const int32_t *offsets,
+                        const uint16_t *W, int ldw, int64_t stride_w,
+                        int xtype, void *DX, int lddx, void *stream);
+int linear16_grad_weight(int M, int N, int K, int type, const uint16_t *DZ, int lddz,
+                         int groups, const int32_t *offsets,
+                         const uint16_t *X, int ldx, const uint8_t *XQ, int ldxq, const uint8_t *XS, int ldxs,
+                         int wtype, float beta, void *DW, int lddw, int64_t stride_dw,
+                         void *stream);
 
 /* A static, human-readable string for a status code (never NULL). */
 const char *ll_status_string(int status);

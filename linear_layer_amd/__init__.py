@@ -36,6 +36,17 @@ Entry points (same names as the C ABI in ``include/linear_layer.h``):
   step between two blocks: XO = X + alpha*gate*rms(Y)*w_post, H = rms(XO)*w_pre;
   ``rmsnorm_residual_grad`` — its gradient (``rmsnorm_grad_workspace_size`` bytes of
   workspace).
+* ``linear16_nt(X, W, bias, act, R, Y, Z=None, offsets=None)`` — Y = act(X*W^T + bias) + R
+  in float16 or bfloat16 with fp32 sums (Y and R in that type or fp32); Z keeps the
+  activation's input for the way back, in 16 bits or as (codes, scales) in 8.
+  With ``offsets`` (int32, groups + 1 row numbers on the device) the rows are those of
+  experts and W, bias are stacks, one for each.
+* ``linear16_grad_act(DY, Z, act, DZ, dbias=None, offsets=None)``,
+  ``linear16_grad_input(DZ, W, DX, offsets=None)``,
+  ``linear16_grad_weight(DZ, X, DW, beta=0.0, offsets=None)`` — its gradients: DZ = DY *
+  act'(Z) and its sums, DX = DZ*W, DW = DZ^T*X + beta*DW, Z and X in 16 or in 8 bits.
+* ``mx8_quantize(X, codes, scales)``, ``mx8_dequantize(codes, scales, Y)`` — microscaled
+  8-bit floating point (a byte a value, a scale byte a block of 32; ``mx8_shapes``).
 
 Matrices are 2-D, row-major with unit column stride (a row stride larger than
 the width is a leading dimension), on the current CUDA/HIP device. The calls
@@ -55,6 +66,8 @@ __all__ = [
     "mx4_quantize", "mx4_dequantize", "mx4_shapes", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
     "mx4_chosen_kernel", "A_MX4", "A_F16", "A_BF16", "rmsnorm_residual", "rmsnorm_residual_grad", "rmsnorm_grad_workspace_size",
     "TYPE_F32", "TYPE_F16", "TYPE_BF16",
+    "mx8_quantize", "mx8_dequantize", "mx8_shapes", "linear16_nt", "linear16_grad_act", "linear16_grad_input",
+    "linear16_grad_weight", "linear16_grad_act_workspace_size", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "MAX_GROUPS",
     "library_path", "load", "set_tile", "num_tiles", "tile_name", "chosen_tile",
     "set_split_k", "chosen_split_k", "set_stream_k", "chosen_stream_k",
     "ACT_NONE", "ACT_RELU", "DTYPE_F32", "DTYPE_F16", "PLAN_RELU", "PLAN_B_NK", "PLAN_UNALIGNED",
@@ -63,6 +76,8 @@ __all__ = [
 
 OK, ERR_INVALID_VALUE, ERR_NO_DEVICE, ERR_UNSUPPORTED_ARCH, ERR_LAUNCH = 0, 1, 2, 3, 4
 ACT_NONE, ACT_RELU = 0, 1
+ACT_GELU, ACT_GELU_TANH, ACT_SILU = 2, 3, 4   # of linear16_nt and linear16_grad_act
+MAX_GROUPS = 1 << 20   # of rows, in the linear16 calls
 DTYPE_F32, DTYPE_F16 = 0, 1
 TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2   # element types of mx4_quantize, mx4_dequantize and the residual norms
 A_MX4, A_F16, A_BF16 = 0, 1, 2   # the forms of A of the 4-bit products
@@ -88,7 +103,9 @@ EXPORTED = ("gemm_f32", "gemm_f16f32", "gemm_bf16f32", "linear_bias_act", "ll_st
             "mx4_quantize", "mx4_dequantize", "gemm_mx4f32_nt", "gemm_f16mx4f32_nt", "gemm_bf16mx4f32_nt",
             "gemm_mx4f32_nt_ws", "gemm_f16mx4f32_nt_ws", "gemm_bf16mx4f32_nt_ws", "ll_mx4_workspace_size",
             "ll_mx4_chosen_kernel",
-            "rmsnorm_residual", "rmsnorm_residual_grad", "ll_rmsnorm_grad_workspace_size")
+            "rmsnorm_residual", "rmsnorm_residual_grad", "ll_rmsnorm_grad_workspace_size",
+            "mx8_quantize", "mx8_dequantize", "linear16_nt", "linear16_grad_act", "linear16_grad_input",
+            "linear16_grad_weight", "ll_linear16_grad_act_workspace_size")
 
 
 class LinearLayerError(RuntimeError):
@@ -150,6 +167,20 @@ def load():
     lib.rmsnorm_residual_grad.argtypes = [i32, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, f32, vp, i32, vp, f32,
                                           vp, i32, vp, i32, vp, vp, vp, vp, i64, vp]
     lib.rmsnorm_residual.restype = lib.rmsnorm_residual_grad.restype = i32
+    lib.mx8_quantize.argtypes = [i32, i32, i32, vp, i32, vp, i32, vp, i32, vp]
+    lib.mx8_dequantize.argtypes = [i32, i32, vp, i32, vp, i32, i32, vp, i32, vp]
+    lib.linear16_nt.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, i64, vp, i32, i32, vp, i32, vp, i32,
+                                vp, i32, vp, i32, vp, i32, vp]
+    lib.linear16_grad_act.argtypes = [i32, i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, i32, vp, i32, vp,
+                                      vp, i64, vp]
+    lib.linear16_grad_input.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, i64, i32, vp, i32, vp]
+    lib.linear16_grad_weight.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, i32, i32, f32, vp,
+                                         i32, i64, vp]
+    for f in (lib.mx8_quantize, lib.mx8_dequantize, lib.linear16_nt, lib.linear16_grad_act, lib.linear16_grad_input,
+              lib.linear16_grad_weight):
+        f.restype = i32
+    lib.ll_linear16_grad_act_workspace_size.argtypes = [i32, i32, i32]
+    lib.ll_linear16_grad_act_workspace_size.restype = i64
     lib.ll_rmsnorm_grad_workspace_size.argtypes = [i32, i32]
     lib.ll_rmsnorm_grad_workspace_size.restype = i64
     for f in (lib.mx4_quantize, lib.mx4_dequantize, lib.gemm_mx4f32_nt, lib.gemm_f16mx4f32_nt,
@@ -725,3 +756,205 @@ def rmsnorm_residual_grad(DXO, DH, Y, w_post, gate, alpha, X, w_pre, DY, DX, dga
         _stream(stream, X, DXO, DH, Y, w_post, gate, w_pre, DY, DX, dgate, dw_post, dw_pre, workspace)),
         "rmsnorm_residual_grad")
     return DY, DX, dgate, dw_post, dw_pre
+
+
+# ---- microscaled 8-bit floating point ---------------------------------------
+
+def mx8_shapes(rows: int, K: int):
+    """The shapes of the codes and of the scales of a rows x K matrix (both uint8)."""
+    return (rows, K), (rows, (K + 31) // 32)
+
+
+def _packed8(q, M, K, what):
+    """(codes pointer, ld, scales pointer, ld) of an M x K matrix in 8 bits."""
+    torch = _torch()
+    codes, scales = q
+    pq, rows, nq, ldq = _mat(codes, torch.uint8, f"{what} codes")
+    ps, rows2, ns, lds = _mat(scales, torch.uint8, f"{what} scales")
+    want, want_s = mx8_shapes(M, K)
+    if (rows, nq) != want or (rows2, ns) != want_s:
+        raise ValueError(f"{what}: {M} rows of {K} values need codes {want} and scales {want_s}, got "
+                         f"{tuple(codes.shape)} and {tuple(scales.shape)}")
+    return pq, ldq, ps, lds
+
+
+def mx8_quantize(X, codes, scales, stream=None):
+    """Quantise X (float32, float16 or bfloat16; M x K) along its rows into uint8 codes
+    and scales. Returns (codes, scales)."""
+    t = _type_of(X, "X")
+    px, M, K, ldx = _mat(X, X.dtype, "X")
+    packed = _packed8((codes, scales), M, K, "X")
+    _check(load().mx8_quantize(M, K, t, px, ldx, *packed, _stream(stream, X, codes, scales)), "mx8_quantize")
+    return codes, scales
+
+
+def mx8_dequantize(codes, scales, Y, stream=None):
+    """Y (float32, float16 or bfloat16; M x K) = the values codes and scales stand for."""
+    t = _type_of(Y, "Y")
+    py, M, K, ldy = _mat(Y, Y.dtype, "Y")
+    packed = _packed8((codes, scales), M, K, "Y")
+    _check(load().mx8_dequantize(M, K, *packed, t, py, ldy, _stream(stream, Y, codes, scales)), "mx8_dequantize")
+    return Y
+
+
+# ---- the 16-bit layer and its gradients ----------------------------------------
+
+def _type16_of(t, name):
+    kind = _type_of(t, name)
+    if kind == TYPE_F32:
+        raise TypeError(f"{name} must be float16 or bfloat16, got {t.dtype}")
+    return kind
+
+
+def _same_or_f32(t, dtype, name):
+    """The LL_TYPE_* of a tensor that may be of the call's 16-bit dtype or float32."""
+    kind = _type_of(t, name)
+    if kind != TYPE_F32 and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} or float32, got {t.dtype}")
+    return kind
+
+
+def _offsets(offsets):
+    """(groups, pointer) of the groups' row numbers."""
+    torch = _torch()
+    if offsets is None:
+        return 1, None
+    if (not isinstance(offsets, torch.Tensor) or offsets.dtype != torch.int32 or offsets.dim() != 1 or not offsets.is_cuda
+            or offsets.shape[0] < 1 or (offsets.shape[0] > 1 and offsets.stride(0) != 1)):
+        raise ValueError("offsets must be a contiguous 1-D int32 device tensor of groups + 1 row numbers")
+    if offsets.shape[0] - 1 > MAX_GROUPS:
+        raise ValueError(f"at most {MAX_GROUPS} groups")
+    return offsets.shape[0] - 1, offsets.data_ptr()
+
+
+def _weights(W, dtype, groups, grouped, name):
+    """(pointer, N, K, ld, stride) of one weight, or of a stack of them."""
+    if not grouped:
+        return _mat(W, dtype, name) + (0,)
+    p, n, N, K, ld, stride = _bmat(W, dtype, name)
+    if n != groups:
+        raise ValueError(f"{name}: {groups} groups need as many weights, got {n}")
+    return p, N, K, ld, stride
+
+
+def _group_vec(t, groups, grouped, N, name):
+    """Pointer of contiguous fp32 values, N or groups x N, or None."""
+    torch = _torch()
+    if t is None:
+        return None
+    shape = (groups, N) if grouped else (N,)
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_cuda
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous fp32 device tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def _held(v, dtype, M, N, name):
+    """(pointer, ld, codes, ld, scales, ld) of an M x N tensor of dtype or a pair (codes,
+    scales) in 8 bits, or of None; and the tensors."""
+    one = max(N, 1)
+    if v is None:
+        return (None, one, None, one, None, one), ()
+    if isinstance(v, (tuple, list)):
+        if len(v) != 2:
+            raise ValueError(f"{name} must be a tensor or a pair (codes, scales)")
+        return (None, one) + _packed8(v, M, N, name), tuple(v)
+    p, ld = _opt_mat(v, dtype, name, M, N)
+    return (p, ld, None, one, None, one), (v,)
+
+
+def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, stream=None):
+    """Y = act(X*W^T + bias) + R with X (M x K) and W (N x K) in float16 or bfloat16, fp32
+    sums, bias fp32 or None, R and Y (M x N) both of X's dtype or both float32; R may be
+    None or Y. Z, if given, receives X*W^T + bias: a tensor of X's dtype, or a pair (codes,
+    scales) of uint8 tensors (``mx8_shapes``). With ``offsets`` (groups + 1 ascending row
+    numbers, int32, on the device) W is groups x N x K, bias groups x N, and rows outside
+    all groups stay as they are. Returns Y."""
+    t = _type16_of(X, "X")
+    px, M, K, ldx = _mat(X, X.dtype, "X")
+    groups, poff = _offsets(offsets)
+    pw, N, K2, ldw, stride = _weights(W, X.dtype, groups, poff is not None, "W")
+    ty = _same_or_f32(Y, X.dtype, "Y")
+    py, M2, N2, ldy = _mat(Y, Y.dtype, "Y")
+    if groups and (K2 != K or M2 != M or N2 != N):
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, Y {tuple(Y.shape)}")
+    pr, ldr = _opt_mat(R, Y.dtype, "R", M, N)
+    held, zs = _held(Z, X.dtype, M, N, "Z")
+    pb = _group_vec(bias, groups, poff is not None, N, "bias")
+    _check(load().linear16_nt(M, N, K, t, px, ldx, groups, poff, pw, ldw, stride, pb, int(act), ty, pr, ldr, py, ldy,
+                              *held, _stream(stream, X, W, Y, R, bias, offsets, *zs)), "linear16_nt")
+    return Y
+
+
+def linear16_grad_act_workspace_size(M: int, N: int, groups: int = 1) -> int:
+    """Bytes of workspace linear16_grad_act needs for dbias."""
+    if M > _INT_MAX or N > _INT_MAX or groups > MAX_GROUPS:
+        raise ValueError(f"the calls take sizes up to {_INT_MAX} and {MAX_GROUPS} groups")
+    n = load().ll_linear16_grad_act_workspace_size(int(M), int(N), int(groups))
+    if n < 0:
+        raise ValueError("negative size")
+    return n
+
+
+def linear16_grad_act(DY, Z, act: int, DZ, dbias=None, offsets=None, workspace=None, stream=None):
+    """DZ = DY * act'(Z) and dbias = DZ's sums over the rows (of each group): DY (M x N) of
+    DZ's dtype or float32, Z a tensor of DZ's dtype or a pair (codes, scales) in 8 bits (None
+    for ACT_NONE). DZ may be DY or Z. dbias takes a workspace (a contiguous device tensor of
+    linear16_grad_act_workspace_size bytes); without one it comes from torch's allocator, on
+    the current stream only. Returns DZ."""
+    torch = _torch()
+    t = _type16_of(DZ, "DZ")
+    pdz, M, N, lddz = _mat(DZ, DZ.dtype, "DZ")
+    groups, poff = _offsets(offsets)
+    ty = _same_or_f32(DY, DZ.dtype, "DY")
+    pdy, lddy = _opt_mat(DY, DY.dtype, "DY", M, N)
+    held, zs = _held(Z, DZ.dtype, M, N, "Z")
+    pb = _group_vec(dbias, groups, poff is not None, N, "dbias")
+    s = _stream(stream, DZ, DY, dbias, offsets, workspace, *zs)
+    pws, nws = None, 0
+    if pb is not None:
+        if workspace is None:
+            if stream is not None:
+                raise ValueError("dbias on a stream that is given needs a workspace")
+            workspace = torch.empty(linear16_grad_act_workspace_size(M, N, groups), dtype=torch.uint8, device=DZ.device)
+        elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous device tensor")
+        pws, nws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(load().linear16_grad_act(M, N, t, int(act), ty, pdy, lddy, groups, poff, *held, pdz, lddz, pb, pws, nws, s),
+           "linear16_grad_act")
+    return DZ
+
+
+def linear16_grad_input(DZ, W, DX, offsets=None, stream=None):
+    """DX = DZ*W: DZ (M x N) and W (N x K, or groups x N x K) in float16 or bfloat16, DX
+    (M x K) of that dtype or float32. Returns DX."""
+    t = _type16_of(DZ, "DZ")
+    pdz, M, N, lddz = _mat(DZ, DZ.dtype, "DZ")
+    groups, poff = _offsets(offsets)
+    pw, N2, K, ldw, stride = _weights(W, DZ.dtype, groups, poff is not None, "W")
+    tx = _same_or_f32(DX, DZ.dtype, "DX")
+    pdx, M2, K2, lddx = _mat(DX, DX.dtype, "DX")
+    if groups and (N2 != N or M2 != M or K2 != K):
+        raise ValueError(f"shape mismatch: DZ {tuple(DZ.shape)}, W {tuple(W.shape)}, DX {tuple(DX.shape)}")
+    _check(load().linear16_grad_input(M, N, K, t, pdz, lddz, groups, poff, pw, ldw, stride, tx, pdx, lddx,
+                                      _stream(stream, DZ, W, DX, offsets)), "linear16_grad_input")
+    return DX
+
+
+def linear16_grad_weight(DZ, X, DW, beta: float = 0.0, offsets=None, stream=None):
+    """DW = DZ^T*X + beta*DW: DZ (M x N) in float16 or bfloat16, X (M x K) of that dtype or a
+    pair (codes, scales) in 8 bits, DW (N x K, or groups x N x K) of that dtype or float32.
+    Returns DW."""
+    t = _type16_of(DZ, "DZ")
+    pdz, M, N, lddz = _mat(DZ, DZ.dtype, "DZ")
+    groups, poff = _offsets(offsets)
+    tw = _same_or_f32(DW, DZ.dtype, "DW")
+    pdw, N2, K, lddw, stride = _weights(DW, DW.dtype, groups, poff is not None, "DW")
+    held, xs = _held(X, DZ.dtype, M, K, "X")
+    if not xs:
+        raise TypeError("X must be a tensor or a pair (codes, scales)")
+    if groups and N2 != N:
+        raise ValueError(f"shape mismatch: DZ {tuple(DZ.shape)}, DW {tuple(DW.shape)}")
+    _check(load().linear16_grad_weight(M, N, K, t, pdz, lddz, groups, poff, *held, tw, float(beta), pdw, lddw, stride,
+                                       _stream(stream, DZ, DW, offsets, *xs)), "linear16_grad_weight")
+    return DW

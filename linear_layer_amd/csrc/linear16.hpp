@@ -1,0 +1,258 @@
+// The 16-bit layer (linear16_nt), its gradients and the 8-bit format they can
+// read and write: parameter blocks, host-side launchers, and the device code
+// that the kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "common.hpp"
+#include "linear_layer.h"
+#include "mx4.hpp"
+
+namespace ll {
+
+// Rows that belong together (one expert's): group g has the rows from offsets[g]
+// on, up to offsets[g + 1]. offsets == nullptr: one group of all rows.
+struct Groups {
+    const int32_t *offsets;
+    int n;
+};
+
+// One product. Forward: C (M x N) = A (M x K) * W_g^T (N x K) with its write-back.
+// Input gradient: C (M x N) = A (M x K) * W_g (K x N). Weight gradient: C_g (M x N) =
+// A^T * B over the rows of group g, A (K rows in all x M), B (K rows x N).
+struct L16Params {
+    const uint16_t *A;
+    const void *B;              // 16-bit values, or E4M3 codes
+    const uint8_t *BS;          // B's scales
+    void *C;
+    const float *bias;          // groups x N, or null
+    const void *R;              // added after the activation, of C's type, or null
+    uint16_t *Z;                // A * W^T + bias in A's type, or null
+    uint8_t *ZQ, *ZS;           // the same in 8 bits, or null
+    float *ws;                  // room for the shares' sums
+    int64_t lda, ldb, ldc, ldr, ldz;        // elements
+    int64_t ldbs, ldzq, ldzs;               // bytes
+    int64_t stride_b, stride_c;             // elements between groups' weights
+    Groups groups;
+    int M, N, K;
+    int act;
+    int ctype;                  // LL_TYPE_* of C (and R)
+    float beta;
+    int tiles_n, tiles_m;       // set by the launcher
+    int shares;                 // of K (or of the rows), summed through ws
+};
+
+enum L16Op : int { L16_FWD = 0, L16_DX = 1, L16_DW = 2 };
+
+// `vec`: every row of 16-bit operands in whole 16-byte pieces, on 16 bytes.
+hipError_t launch_l16_fwd(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
+hipError_t launch_l16_dx(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
+hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
+
+struct ActGradParams {
+    const void *DY;             // M x N of LL_TYPE_*
+    const uint16_t *Z;          // 16 bits, or
+    const uint8_t *ZQ, *ZS;     // 8 bits, or neither
+    uint16_t *DZ;               // or null
+    float *dbias;               // groups x N, or null
+    float *part;                // partial column sums
+    int64_t lddy, ldz, ldzq, ldzs, lddz;
+    Groups groups;
+    int M, N;
+    int act;
+};
+// Floats of `part`.
+int64_t act_grad_parts(int M, int N, int groups);
+// Most sums, rows and columns that one call may have (their numbers, and those a tile past
+// them, are 32-bit).
+constexpr int kL16Most = 0x7fffffff - 1024;
+hipError_t launch_act_grad(bool bf16, int dytype, ActGradParams p, hipStream_t s);
+
+hipError_t launch_mx8_quantize(int type, const void *X, int64_t ldx, uint8_t *codes, int64_t ldq, uint8_t *scales,
+                               int64_t lds, int M, int K, hipStream_t s);
+hipError_t launch_mx8_dequantize(int type, const uint8_t *codes, int64_t ldq, const uint8_t *scales, int64_t lds,
+                                 void *Y, int64_t ldy, int M, int K, hipStream_t s);
+
+// ---- groups of rows ------------------------------------------------------------
+
+// Where a group begins, whatever stands in `offsets`: values are taken into 0 .. M
+// and a group never begins before the one ahead of it, so wrong offsets give wrong
+// rows but no access outside the matrices and no row in two groups.
+__device__ __forceinline__ int wave_max_scan(int v)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d)
+            v = max(v, o);
+    }
+    return v;
+}
+
+__device__ __forceinline__ int wave_sum_scan(int v)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_up(v, d);
+        if (lane >= d)
+            v += o;
+    }
+    return v;
+}
+
+// The rows [begin, end) of group g. Every lane of the wave takes part.
+__device__ __forceinline__ void group_rows(const Groups &gr, int M, int g, int &begin, int &end)
+{
+    if (gr.offsets == nullptr) {
+        begin = 0;
+        end = M;
+        return;
+    }
+    const int lane = threadIdx.x & 63;
+    int top = 0;
+    for (int i = lane; i <= g; i += 64)
+        top = max(top, gr.offsets[i]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        top = max(top, __shfl_xor(top, d));
+    begin = min(max(top, 0), M);
+    end = min(max(top, gr.offsets[g + 1]), M);
+    begin = __builtin_amdgcn_readfirstlane(begin);
+    end = __builtin_amdgcn_readfirstlane(max(begin, end));
+}
+
+// Rows of all groups cut into chunks of at most `step`, group by group. Returns their
+// number; c: chunk `id` (its group, the group's rows, its number within the group and the
+// id of the group's first chunk), or with BY_GROUP those of group `id` (index: how many
+// chunks it has). An id that is no chunk's leaves c alone. Every lane of the wave takes part.
+struct Chunk {
+    int group, begin, end, index, group_first;
+};
+template <bool BY_GROUP = false>
+__device__ __forceinline__ int find_chunk(const Groups &gr, int M, int step, int id, Chunk &c)
+{
+    if (gr.offsets == nullptr) {
+        c = Chunk{0, 0, M, BY_GROUP ? cdiv(M, step) : id, 0};
+        return cdiv(M, step);
+    }
+    const int lane = threadIdx.x & 63;
+    int top = min(max(gr.offsets[0], 0), M), chunks = 0;
+    for (int g0 = 0; g0 < gr.n; g0 += 64) {
+        const int g = g0 + lane;
+        int e = g < gr.n ? min(max(gr.offsets[g + 1], 0), M) : 0;
+        e = max(wave_max_scan(e), top);
+        const int before = __shfl_up(e, 1);
+        const int b = lane == 0 ? top : before;
+        const int n = g < gr.n ? cdiv(e - b, step) : 0;
+        const int incl = wave_sum_scan(n) + chunks, excl = incl - n;
+        const unsigned long long hit = __ballot(BY_GROUP ? g == id : id >= excl && id < incl);
+        if (hit != 0) {
+            const int src = __ffsll(hit) - 1, first = __shfl(excl, src);
+            c = Chunk{g0 + src, __shfl(b, src), __shfl(e, src), BY_GROUP ? __shfl(n, src) : id - first, first};
+        }
+        top = __shfl(e, 63);
+        chunks = __shfl(incl, 63);
+    }
+    c.group = __builtin_amdgcn_readfirstlane(c.group);
+    c.begin = __builtin_amdgcn_readfirstlane(c.begin);
+    c.end = __builtin_amdgcn_readfirstlane(c.end);
+    c.index = __builtin_amdgcn_readfirstlane(c.index);
+    c.group_first = __builtin_amdgcn_readfirstlane(c.group_first);
+    return __builtin_amdgcn_readfirstlane(chunks);
+}
+
+// ---- activations ----------------------------------------------------------------
+
+constexpr float kGeluA = 0.7978845608028654f;     // sqrt(2 / pi)
+constexpr float kGeluB = 0.044715f;
+
+__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+
+// z times a factor that goes to 0 as z goes to minus infinity.
+__device__ __forceinline__ float damped(float z, float f) { return f == 0.0f ? 0.0f : z * f; }
+
+// act(z). The tanh form of GELU is z * sigmoid(2 u): 0.5 * (1 + tanh(u)) is that.
+__device__ __forceinline__ float activate(float z, int act)
+{
+    switch (act) {
+    case LL_ACT_RELU: return z > 0.0f ? z : 0.0f;
+    case LL_ACT_GELU: return damped(z, 0.5f * (1.0f + erff(z * 0.70710678118654752f)));
+    case LL_ACT_GELU_TANH: return damped(z, sigmoid(2.0f * kGeluA * (z + kGeluB * z * z * z)));
+    case LL_ACT_SILU: return damped(z, sigmoid(z));
+    default: return z;
+    }
+}
+
+// act'(z). Past +-110 every slope here is 0 or 1 in FP32 to the last bit; z is held there so
+// that no product of an infinity and a zero comes up (NaN stays NaN).
+__device__ __forceinline__ float activation_slope(float z, int act)
+{
+    z = z > 110.0f ? 110.0f : z < -110.0f ? -110.0f : z;
+    switch (act) {
+    case LL_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
+    case LL_ACT_GELU:
+        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    case LL_ACT_GELU_TANH: {
+        const float s = sigmoid(2.0f * kGeluA * (z + kGeluB * z * z * z));
+        return s + z * s * (1.0f - s) * 2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
+    }
+    case LL_ACT_SILU: {
+        const float s = sigmoid(z);
+        return s + z * s * (1.0f - s);
+    }
+    default: return 1.0f;
+    }
+}
+
+// ---- 8-bit values -----------------------------------------------------------------
+
+// The scale byte of a block whose largest magnitude has the FP32 pattern `top`:
+// 127 + e with e the smallest exponent, at least -127, for which the magnitude is at
+// most 448 * 2^e (E4M3's largest value), so that nothing is clipped; 255 for a block with
+// an infinity or a NaN. 448 is 1.75 * 2^8: past that fraction the exponent is one more. A
+// subnormal magnitude gives 0.
+__device__ __forceinline__ uint32_t mx8_scale(uint32_t top)
+{
+    const uint32_t e = top >> 23;
+    if (e == 255u)
+        return 255u;
+    const uint32_t up = e + ((top & 0x7fffffu) > 0x600000u ? 1u : 0u);
+    return up > 8u ? up - 8u : 0u;
+}
+
+// Four E4M3 codes of four values under scale byte s (< 255), to nearest, ties to
+// even. The conversion takes the scale from an FP32 value's exponent field (0: 2^-127).
+__device__ __forceinline__ uint32_t mx8_encode4(float v0, float v1, float v2, float v3, uint32_t s)
+{
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    const float sc = __builtin_bit_cast(float, s << 23);
+    s16x2 r = {0, 0};
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v0, v1, sc, false);
+    r = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(r, v2, v3, sc, true);
+    return s == 255u ? 0u : __builtin_bit_cast(uint32_t, r);
+}
+
+// The values of four codes under scale byte s.
+__device__ __forceinline__ void mx8_decode4(uint32_t c, uint32_t s, float *v)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const float sc = __builtin_bit_cast(float, s << 23);
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, sc, false);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, sc, true);
+    v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
+    if (s == 255u)
+        v[0] = v[1] = v[2] = v[3] = __builtin_nanf("");
+}
+
+// The largest of v over groups of four lanes.
+__device__ __forceinline__ uint32_t max_of_quad(uint32_t v)
+{
+    v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xf, 0xf, false));
+    return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xf, 0xf, false));
+}
+
+}  // namespace ll
