@@ -19,8 +19,11 @@ struct Mat {
     bool ld_ok(int64_t cols) const { return p == nullptr || ld >= (cols > 1 ? cols : 1); }
     Range range(int64_t rows, int64_t cols) const { return {p, p != nullptr ? span(rows, cols, ld, elem) : 0}; }
     bool ok(int64_t rows, int64_t cols) const { return p == nullptr || (aligned(p, elem) && range(rows, cols).bytes >= 0); }
-    // every row in whole 16-byte pieces, on 16 bytes
-    bool vec(int64_t cols) const { return aligned(p, 16) && ld * elem % 16 == 0 && cols * elem % 16 == 0; }
+    // every row in whole 16-byte pieces, on 16 bytes, and a tile of them in a buffer's 2 GiB
+    bool vec(int64_t cols) const
+    {
+        return aligned(p, 16) && ld * elem % 16 == 0 && cols * elem % 16 == 0 && ld < (int64_t)1 << 21;
+    }
     bool same(const Mat &o) const { return p != nullptr && p == o.p && ld == o.ld; }
 };
 

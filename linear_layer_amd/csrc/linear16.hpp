@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.hpp"
 #include "linear_layer.h"
 #include "mx4.hpp"
@@ -184,6 +186,23 @@ __device__ __forceinline__ float activate(float z, int act)
     case LL_ACT_GELU_TANH: return damped(z, sigmoid(2.0f * kGeluA * (z + kGeluB * z * z * z)));
     case LL_ACT_SILU: return damped(z, sigmoid(z));
     default: return z;
+    }
+}
+
+// act of eight values: one test of the kind for all.
+__device__ __forceinline__ void activate8(float (&v)[8], int act)
+{
+    auto each = [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = activate(v[e], decltype(kind)::value);
+    };
+    switch (act) {
+    case LL_ACT_RELU: each(std::integral_constant<int, LL_ACT_RELU>{}); break;
+    case LL_ACT_GELU: each(std::integral_constant<int, LL_ACT_GELU>{}); break;
+    case LL_ACT_GELU_TANH: each(std::integral_constant<int, LL_ACT_GELU_TANH>{}); break;
+    case LL_ACT_SILU: each(std::integral_constant<int, LL_ACT_SILU>{}); break;
+    default: break;
     }
 }
 
