@@ -13,12 +13,15 @@
 //   COLS8  as COLS, from E4M3 codes and scales: 16 codes a load into registers, decoded and
 //          stored as the 32-byte unit that they are in 16 bits. Decoding on the way into LDS
 //          is done once a workgroup; after it, by every wave that reads the stage.
-// ROWS and COLS on 16 bytes are copied straight into LDS by buffer loads (16 bytes a lane)
-// whose descriptor ends with the tile's last row and the contracted range, so that what lies
-// past them arrives as zeros without a test; only where a stage crosses the range's end inside
-// the rows do lanes take an offset past the descriptor. Rows off 16 bytes go through registers
-// (DMA false), 16 bytes a load at any alignment, the chunk that crosses the row's end value
-// by value.
+// Every 16 bytes go through registers: loaded a whole stage before they are stored into LDS, and
+// stored up to a stage before they are read, one load and one store after each row of
+// MFMAs. (Copies straight into LDS have to land between two barriers, which leaves them half
+// that time: 8192^3 1.26 PFLOP/s where this reaches 1.5.) Rows on 16 bytes (VEC) are read by
+// buffer loads whose descriptor ends with the tile's last row and the contracted range, so
+// that what lies past them arrives as zeros without a test; only where a stage crosses the
+// range's end inside the rows do lanes take an offset past the descriptor. Rows off 16 bytes
+// are read 16 bytes a load at any alignment, the chunk that crosses the row's end value by
+// value.
 //
 // The MFMA takes the operand of C's columns first, so a lane gets four neighbouring columns
 // of a row; the write-back turns them around in LDS to eight a lane, 128 bytes of a row (16
@@ -50,16 +53,33 @@ __device__ __forceinline__ f32x4 mma(const f16x8 &a, const f16x8 &b, const f32x4
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// c += a * b with c in accumulation registers. One wave a SIMD has 256 of them beside its 256
+// vector registers; left to the compiler, sums wander between the two (500 moves a stage).
+// It takes the statement for any other instruction, so nothing may read or write c
+// close to it but the next of these: see settle().
+template <bool BF16>
+__device__ __forceinline__ void mma_acc(const f16x8 &a, const f16x8 &b, f32x4 &c)
+{
+    if constexpr (BF16)
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+// The wait between mma_acc and what else reads its sums (18 wait states at most), and between what
+// wrote them and the first mma_acc.
+__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
+
 template <bool BF16> constexpr int kType16 = BF16 ? LL_TYPE_BF16 : LL_TYPE_F16;
 
-// Waves, and the block of C that each has: 256 x 256 as 2 x 4 waves of 128 x 64 (two a
+// Waves, and the block of C that each has: 256 x 256 as 2 x 2 waves of 128 x 128 (one a
 // SIMD), 128 x 128 as 2 x 2 of 64 x 64 (two workgroups a CU).
 template <int BM> struct Cfg {
-    static constexpr int WGM = 2, WGN = BM == 256 ? 4 : 2, NW = WGM * WGN, NT = 64 * NW;
-    static constexpr int BK = 64, STEPS = 2;
+    static constexpr int WGM = 2, WGN = 2, NW = WGM * WGN, NT = 64 * NW;
+    static constexpr int WPE = BM == 256 ? 1 : 2;           // waves a SIMD
+    static constexpr int BK = 64;                           // two steps of the MFMA
     static constexpr int WTM = BM / WGM, WTN = BM / WGN, FM = WTM / 16, FN = WTN / 16;
     static constexpr int STAGE = BM * BK;                   // values of an operand's stage
-    static constexpr int COPIES = STAGE * 2 / 1024 / NW;    // KiB copies a wave, operand and stage
+    static constexpr int PIECES = STAGE * 2 / 16 / NT;      // of 16 bytes, a thread's of a stage
 };
 
 // 16-byte chunk c of row `row` of a ROWS stage, and unit u of k-row k of a COLS stage.
@@ -78,19 +98,6 @@ __device__ __forceinline__ void static_for(F f)
     static_for_(std::make_integer_sequence<int, N>{}, f);
 }
 
-// buffer_load_dwordx4 into LDS: this lane's 16 bytes at byte `off` of the buffer go to LDS
-// byte lds_base + 16 * lane, zeros where they lie past its end. Inline assembly, so that the
-// compiler does not take it for an LDS store that every barrier must wait for; the caller
-// counts the copies itself before the barrier that publishes them. The compiler's hazard
-// checks do not look inside: a scalar that a vector instruction wrote (v_readfirstlane) may be
-// read by a load five wait states later, M0 one after its write.
-__device__ __forceinline__ void lds_buffer_16(const u32x4 &buffer, uint32_t off, uint32_t lds_base)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds_base), "v"(off), "s"(buffer)
-                 : "memory", "m0");
-}
 constexpr uint32_t kPastEnd = 0x80000000u;   // past the end of every buffer here: 256 rows of less than 2^21 values
 
 typedef const __attribute__((address_space(3))) f16x8 *LdsF16x8;
@@ -98,142 +105,122 @@ typedef __attribute__((address_space(3))) s16x4 *LdsS16x4;
 
 // One operand's source: `lim` rows or columns of it from the tile's first on exist (more
 // may be asked for), `klen` of the contracted axis.
-template <bool BF16, int BM, int SIDE, bool DMA>
+template <bool BF16, int BM, int SIDE, bool VEC>
 struct Operand {
     using C = Cfg<BM>;
-    // registers of a stage on its way: 16-byte chunks a thread
-    static constexpr int REGS = SIDE == COLS8 ? BM * C::BK / 16 / C::NT : DMA ? 1 : C::STAGE * 2 / 16 / C::NT;
-    static constexpr int KROWS = 512 / BM;   // k-rows of a copy (COLS)
+    static constexpr int PIECES = SIDE == COLS8 ? C::PIECES / 2 : C::PIECES;   // 16-byte pieces of memory a thread and stage
+    static constexpr int KROWS = 512 / BM;   // k-rows of 1 KiB of a COLS stage
     const uint16_t *src;        // the tile's first row (ROWS) or column (COLS), k = 0
     const uint8_t *src8, *scales;
     int64_t ld, lds;
     int lim, klen, col0;
-    uint32_t off[2];            // a lane's offset in a copy: two swizzles take turns
-    u32x4 reg[REGS];
-    uint32_t sc[REGS];
+    uint32_t off[2], cur[2];    // offset of piece 0, and of piece 1 where its swizzle is another; in the stage aimed at
+    __amdgpu_buffer_rsrc_t buf;
+    u32x4 reg[PIECES];
+    uint32_t sc[SIDE == COLS8 ? PIECES : 1];
 
-    // Copy j of a wave fills KiB wave * COPIES + j of a stage: 8 rows of 128 bytes, or KROWS
-    // k-rows of 2 * BM bytes.
-    __device__ __forceinline__ void start(int wave, int lane)
+    // Piece j of a thread fills 16-byte slot (j * NW + wave) * 64 + lane of a stage: a wave fills 8
+    // rows of 128 bytes, or KROWS k-rows of 2 * BM. The swizzles repeat every 16 rows,
+    // which is one piece of each wave or two.
+    static constexpr int STRIDE = C::NW * (SIDE == ROWS ? 8 : KROWS);   // rows from a piece to the next
+    static constexpr int SETS = STRIDE % 16 == 0 ? 1 : 2;
+    static_assert(STRIDE * SETS % 16 == 0, "the pieces' swizzles");
+    // Row, and value within the row, of slot s.
+    __device__ __forceinline__ static int slot_row(int s) { return SIDE == ROWS ? s / 8 : s / (BM / 8); }
+    __device__ __forceinline__ static int slot_col(int s)
     {
-        static_assert(C::COPIES == 4, "the copies' swizzles");
-        if constexpr (DMA && SIDE == ROWS) {
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const int row = (wave * C::COPIES + v) * 8 + lane / 8;
-                off[v] = (uint32_t)row * (uint32_t)(2 * ld) + (((lane & 7) ^ rows_swz(row)) << 4);
-            }
-        } else if constexpr (DMA) {
-            constexpr int LPR = 64 / KROWS;   // lanes of a k-row
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const int k = (wave * C::COPIES + v * (BM == 256 ? 1 : 2)) * KROWS + lane / LPR, u2 = lane % LPR;
-                off[v] = (uint32_t)k * (uint32_t)(2 * ld) + ((((u2 >> 1) ^ cols_swz(k)) << 5) | ((u2 & 1) << 4));
-            }
-        }
-    }
-    // The buffer of the stage at k0.
-    __device__ __forceinline__ u32x4 buffer(int k0) const
-    {
-        const int left = min(klen - k0, C::BK), n = min(lim, BM);
-        const uint64_t at = (uint64_t)(SIDE == ROWS ? src + k0 : src + (int64_t)k0 * ld);
-        const uint32_t bytes = SIDE == ROWS ? (uint32_t)(n - 1) * (uint32_t)(2 * ld) + 2 * left
-                                            : (uint32_t)(left - 1) * (uint32_t)(2 * ld) + 2 * n;
-        return u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, bytes, 0x00020000u};
-    }
-    // Copy j of this wave of that stage to the stage at LDS address `base`.
-    template <int J>
-    __device__ __forceinline__ void copy(const u32x4 &buf, uint32_t base, int k0, int wave, int lane) const
-    {
-        constexpr int v = SIDE == ROWS || BM == 256 ? J & 1 : J >> 1;
-        constexpr int r = SIDE == ROWS ? (J & 2) * 8 : BM == 256 ? (J & 2) * KROWS : (J & 1) * KROWS;   // rows past the swizzle's first copy
-        uint32_t o = off[v] + r * (uint32_t)(2 * ld);
         if constexpr (SIDE == ROWS) {
-            const int row = (wave * C::COPIES + v) * 8 + lane / 8;
-            if (k0 + ((lane & 7) ^ rows_swz(row)) * 8 >= klen)
-                o = kPastEnd;
+            return ((s & 7) ^ rows_swz(s / 8)) * 8;
+        } else {
+            const int u2 = s % (BM / 8);
+            return ((u2 >> 1) ^ cols_swz(s / (BM / 8))) * 16 + (u2 & 1) * 8;
         }
-        lds_buffer_16(buf, o, base + (wave * C::COPIES + J) * 1024);
     }
-
-    // Through registers: every load of the stage at k0, then (`put`) into the stage.
-    __device__ __forceinline__ void fetch(int k0, int tid)
+    __device__ __forceinline__ void start(int tid)
     {
+        if constexpr (VEC && SIDE != COLS8) {
 #pragma unroll
-        for (int i = 0; i < REGS; ++i) {
-            reg[i] = u32x4{0u, 0u, 0u, 0u};
-            const int c = i * C::NT + tid;
-            if constexpr (SIDE == COLS8) {
-                const int k = c / (BM / 16), col = c % (BM / 16) * 16;
-                sc[i] = 0;
-                if (k0 + k < klen && col < lim) {
-                    const uint8_t *p = src8 + (int64_t)(k0 + k) * ld + col;
-                    sc[i] = scales[(int64_t)(k0 + k) * lds + ((col0 + col) >> 5)];
-                    if (col + 16 <= lim) {
-                        reg[i] = load16<u32x4>(p);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (col + e < lim)
-                                reg[i][e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
-                    }
-                }
-            } else {
-                int n;
-                const uint16_t *p;
-                if constexpr (SIDE == ROWS) {
-                    const int row = c / 8, k = k0 + c % 8 * 8;
-                    n = row < lim ? klen - k : 0;
-                    p = src + (int64_t)row * ld + k;
-                } else {
-                    const int k = c / (BM / 8), col = c % (BM / 8) * 8;
-                    n = k0 + k < klen ? lim - col : 0;
-                    p = src + (int64_t)(k0 + k) * ld + col;
-                }
-                if (n >= 8) {
-                    reg[i] = load16<u32x4>(p);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < n)
-                            reg[i][e / 2] |= (uint32_t)p[e] << (16 * (e % 2));
-                }
+            for (int v = 0; v < SETS; ++v) {
+                const int s = v * C::NT + tid;
+                off[v] = (uint32_t)slot_row(s) * (uint32_t)(2 * ld) + 2 * slot_col(s);
             }
         }
     }
-    __device__ __forceinline__ void put(uint16_t *stage, int tid) const
+    // The pieces loaded from now on are of the stage at k0 (past the range: zeros).
+    __device__ __forceinline__ void aim(int k0, int tid)
     {
+        if constexpr (VEC && SIDE != COLS8) {
+            const int left = min(klen - k0, C::BK), n = min(lim, BM);
+            const int bytes = left <= 0 ? 0 : SIDE == ROWS ? (n - 1) * (int)(2 * ld) + 2 * left : (left - 1) * (int)(2 * ld) + 2 * n;
+            const uint16_t *at = SIDE == ROWS ? src + k0 : src + (int64_t)k0 * ld;
+            buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(at), 0, bytes, 0x00020000);
 #pragma unroll
-        for (int i = 0; i < REGS; ++i) {
-            const int c = i * C::NT + tid;
-            if constexpr (SIDE == COLS8) {
-                const int k = c / (BM / 16), u = c % (BM / 16) ^ cols_swz(k);
-                u32x4 w[2];
+            for (int v = 0; v < SETS; ++v)
+                cur[v] = SIDE == ROWS && slot_col(v * C::NT + tid) >= left ? kPastEnd : off[v];
+        }
+    }
+    template <int J>
+    __device__ __forceinline__ void load(int k0, int tid)
+    {
+        if constexpr (VEC && SIDE != COLS8) {
+            constexpr int v = J % SETS;
+            reg[J] = __builtin_amdgcn_raw_buffer_load_b128(buf, cur[v] + (J - v) * STRIDE * (uint32_t)(2 * ld), 0, 0);
+        } else if constexpr (SIDE == COLS8) {
+            reg[J] = u32x4{0u, 0u, 0u, 0u};
+            sc[J] = 0;
+            const int c = J * C::NT + tid, k = k0 + c / (BM / 16), col = c % (BM / 16) * 16;
+            if (k < klen && col < lim) {
+                const uint8_t *p = src8 + (int64_t)k * ld + col;
+                sc[J] = scales[(int64_t)k * lds + ((col0 + col) >> 5)];
+                if (col + 16 <= lim) {
+                    reg[J] = load16<u32x4>(p);
+                } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[4];
-                    mx8_decode4(reg[i][q], sc[i], v);
-                    if constexpr (!BF16) {
-                        // a value that rounding to 8 bits carried past binary16's range
-                        // (65504 becomes 65536) is its largest
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = __builtin_fabsf(v[e]) > 65504.0f ? __builtin_copysignf(65504.0f, v[e]) : v[e];
-                    }
-                    w[q / 2][2 * (q & 1)] = (uint32_t)from_f32<kType16<BF16>>(v[0]) | (uint32_t)from_f32<kType16<BF16>>(v[1]) << 16;
-                    w[q / 2][2 * (q & 1) + 1] = (uint32_t)from_f32<kType16<BF16>>(v[2]) | (uint32_t)from_f32<kType16<BF16>>(v[3]) << 16;
+                    for (int e = 0; e < 16; ++e)
+                        if (col + e < lim)
+                            reg[J][e / 4] |= (uint32_t)p[e] << (8 * (e % 4));
                 }
-                u32x4 *dst = reinterpret_cast<u32x4 *>(stage + k * BM + u * 16);
-                dst[0] = w[0];
-                dst[1] = w[1];
-            } else if constexpr (SIDE == ROWS) {
-                const int row = c / 8, ch = (c & 7) ^ rows_swz(row);
-                *reinterpret_cast<u32x4 *>(stage + row * 64 + ch * 8) = reg[i];
-            } else {
-                const int k = c / (BM / 8), u2 = c % (BM / 8);
-                const int u = (u2 >> 1) ^ cols_swz(k);
-                *reinterpret_cast<u32x4 *>(stage + k * BM + u * 16 + (u2 & 1) * 8) = reg[i];
             }
+        } else {
+            reg[J] = u32x4{0u, 0u, 0u, 0u};
+            const int s = J * C::NT + tid, row = slot_row(s), col = slot_col(s);
+            const int n = SIDE == ROWS ? (row < lim ? klen - k0 - col : 0) : (k0 + row < klen ? lim - col : 0);
+            const uint16_t *p = SIDE == ROWS ? src + (int64_t)row * ld + k0 + col : src + (int64_t)(k0 + row) * ld + col;
+            if (n >= 8) {
+                reg[J] = load16<u32x4>(p);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n)
+                        reg[J][e / 2] |= (uint32_t)p[e] << (16 * (e % 2));
+            }
+        }
+    }
+    template <int J>
+    __device__ __forceinline__ void store(uint16_t *stage, int tid) const
+    {
+        if constexpr (SIDE == COLS8) {
+            const int c = J * C::NT + tid, k = c / (BM / 16), u = c % (BM / 16) ^ cols_swz(k);
+            u32x4 w[2];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[4];
+                mx8_decode4(reg[J][q], sc[J], v);
+                if constexpr (!BF16) {
+                    // a value that rounding to 8 bits carried past binary16's range (65504
+                    // becomes 65536) is its largest
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = __builtin_fabsf(v[e]) > 65504.0f ? __builtin_copysignf(65504.0f, v[e]) : v[e];
+                }
+                w[q / 2][2 * (q & 1)] = (uint32_t)from_f32<kType16<BF16>>(v[0]) | (uint32_t)from_f32<kType16<BF16>>(v[1]) << 16;
+                w[q / 2][2 * (q & 1) + 1] = (uint32_t)from_f32<kType16<BF16>>(v[2]) | (uint32_t)from_f32<kType16<BF16>>(v[3]) << 16;
+            }
+            u32x4 *dst = reinterpret_cast<u32x4 *>(stage + k * BM + u * 16);
+            dst[0] = w[0];
+            dst[1] = w[1];
+        } else {
+            *reinterpret_cast<u32x4 *>(stage + (J * C::NT + tid) * 8) = reg[J];
         }
     }
 
@@ -335,12 +322,11 @@ __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &t
     tn = within / rows;
 }
 
-template <int OP, bool BF16, int BM, int SA, int SB, bool DMA>
-__global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) l16_tile_kernel(L16Params p)
+template <int OP, bool BF16, int BM, int SA, int SB, bool VEC>
+__global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE, Cfg<BM>::WPE))) l16_tile_kernel(L16Params p)
 {
     using C = Cfg<BM>;
-    constexpr bool DMA_A = DMA, DMA_B = DMA && SB != COLS8;
-    constexpr int PITCH = C::WTN + 4;   // floats of a row of the write-back's LDS (64 rows a wave)
+    constexpr int PITCH = 64 + 4;   // floats of a row of the write-back's LDS (64 rows a wave)
     constexpr int TURN_BYTES = C::NW * 64 * PITCH * 4, RING_BYTES = 4 * C::STAGE * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds_bytes[TURN_BYTES > RING_BYTES ? TURN_BYTES : RING_BYTES];
     uint16_t (*ring)[2][C::STAGE] = reinterpret_cast<uint16_t (*)[2][C::STAGE]>(lds_bytes);   // [operand][buffer]
@@ -379,8 +365,8 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         n0 = tn * BM;
     }
 
-    Operand<BF16, BM, SA, DMA_A> a;
-    Operand<BF16, BM, SB, DMA_B> b;
+    Operand<BF16, BM, SA, VEC> a;
+    Operand<BF16, BM, SB, VEC> b;
     a.ld = p.lda;
     a.lim = m_end - m0;
     a.klen = b.klen = klen;
@@ -404,193 +390,231 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         for (int j = 0; j < C::FN; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    a.start(wave, lane);
-    b.start(wave, lane);
+    a.start(tid);
+    b.start(tid);
     const uint32_t base_a = lds_addr(&ring[0][0][0]), base_b = lds_addr(&ring[1][0][0]);
     constexpr uint32_t STAGE_BYTES = C::STAGE * 2;
     uint32_t at_a = base_a + a.lane_addr(wm * C::WTM, lane), at_b = base_b + b.lane_addr(wn * C::WTN, lane);
-    auto read_step = [&](int buf, int s, f16x8 (&fa)[C::FM], f16x8 (&fb)[C::FN]) __attribute__((always_inline)) {
-        const uint32_t xa = at_a + buf * STAGE_BYTES, xb = at_b + buf * STAGE_BYTES;
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-            fb[j] = b.read(xb, j, s);
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-            fa[i] = a.read(xa, i, s);
+    auto read_a = [&](int buf, int s, int i) __attribute__((always_inline)) { return a.read(at_a + buf * STAGE_BYTES, i, s); };
+    auto read_b = [&](int buf, int s, int j) __attribute__((always_inline)) { return b.read(at_b + buf * STAGE_BYTES, j, s); };
+    static_assert(C::FM == C::FN, "a block of each operand a row of products");
+    // Stages go through two buffers, two steps a stage. While a step multiplies, the next step's
+    // operands are read: its blocks of B into a second set of registers, a block of A into the
+    // registers that a row of products has done with (the last one at the step's own start). The
+    // barrier stands after the first rows of a stage's last step, when every operand
+    // of the stage is in registers: it publishes the next stage and frees this one's buffer. In
+    // the rows up to the next barrier the thread's pieces of the stage after next go there, each
+    // followed by the load of its successor. Past the range's end zeros are loaded and
+    // stored, and not used.
+    //
+    // A wave issues an instruction every four cycles and an MFMA occupies the matrix core for
+    // sixteen, so what stands between two MFMAs costs nothing up to three instructions; one
+    // wave a SIMD has no other to fill a longer gap. Hence the operations are dealt out
+    // singly among a row's MFMAs (all of them between rows: 8192^3 1.23 PFLOP/s).
+    constexpr int ROWS2 = 2 * C::FM;   // rows of products, and slots for a piece, of a stage
+    static_assert(C::FM == C::FN && C::PIECES == C::FM && decltype(b)::PIECES * (SB == COLS8 ? 2 : 1) == C::FM, "a piece a row");
+    // Slot r: the r/2nd piece of A, or of B (of COLS8 in every other one of its slots).
+    auto load_piece = [&](auto rr, int k0) __attribute__((always_inline)) {
+        constexpr int r = decltype(rr)::value;
+        if constexpr (r % 2 == 0)
+            a.template load<r / 2>(k0, tid);
+        else if constexpr (SB != COLS8)
+            b.template load<r / 2>(k0, tid);
+        else if constexpr (r % 4 == 1)
+            b.template load<r / 4>(k0, tid);
     };
-    // Rows of blocks in alternating column order: neighbouring MFMAs share an operand, and
-    // the chip, power-limited on 16-bit products, keeps a higher clock.
-    auto mfma_row = [&](int i, const f16x8 (&fa)[C::FM], const f16x8 (&fb)[C::FN]) __attribute__((always_inline)) {
-#pragma unroll
-        for (int jj = 0; jj < C::FN; ++jj) {
-            const int j = (i & 1) ? C::FN - 1 - jj : jj;
-            acc[i][j] = mma<BF16>(fb[j], fa[i], acc[i][j]);
-        }
-    };
-    // The products issued so far stay before this point: left alone, the compiler moves them
-    // behind the barrier and keeps their operands alive.
-    auto pin = [&]() __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-                asm volatile("" : "+v"(acc[i][j]));
-    };
-
-    // Stages go through two buffers and two sets of operand registers. A step's operands are
-    // read while the step before multiplies. The stage's barrier stands before its last
-    // step, whose operands are then in registers: it publishes the next stage and frees this
-    // one's buffer, which is refilled while the last step multiplies. Operands that pass
-    // through registers are stored into the next buffer just before the barrier, a stage
-    // after their loads.
-    const int nk = cdiv(klen, C::BK);
-    constexpr int PER = (DMA_A ? C::COPIES : 0) + (DMA_B ? C::COPIES : 0);
-    u32x4 buf_a, buf_b;
-    auto copies = [&](int buf, int k0, auto first, auto count) __attribute__((always_inline)) {
-        static_for<decltype(count)::value>([&](auto cc) __attribute__((always_inline)) {
-            constexpr int c = decltype(first)::value + decltype(cc)::value;
-            if constexpr (DMA_A && c < C::COPIES)
-                a.template copy<c>(buf_a, base_a + buf * STAGE_BYTES, k0, wave, lane);
-            else
-                b.template copy<c - (DMA_A ? C::COPIES : 0)>(buf_b, base_b + buf * STAGE_BYTES, k0, wave, lane);
-        });
+    auto store_piece = [&](auto rr, int buf) __attribute__((always_inline)) {
+        constexpr int r = decltype(rr)::value;
+        if constexpr (r % 2 == 0)
+            a.template store<r / 2>(ring[0][buf], tid);
+        else if constexpr (SB != COLS8)
+            b.template store<r / 2>(ring[1][buf], tid);
+        else if constexpr (r % 4 == 1)
+            b.template store<r / 4>(ring[1][buf], tid);
     };
     auto aim = [&](int k0) __attribute__((always_inline)) {
-        if constexpr (DMA_A)
-            buf_a = a.buffer(k0);
-        if constexpr (DMA_B)
-            buf_b = b.buffer(k0);
+        a.aim(k0, tid);
+        b.aim(k0, tid);
     };
-    auto fetch = [&](int k0) __attribute__((always_inline)) {
-        if constexpr (!DMA_A)
-            a.fetch(k0, tid);
-        if constexpr (!DMA_B)
-            b.fetch(k0, tid);
-    };
-    auto put = [&](int buf) __attribute__((always_inline)) {
-        if constexpr (!DMA_A)
-            a.put(ring[0][buf], tid);
-        if constexpr (!DMA_B)
-            b.put(ring[1][buf], tid);
-    };
-    constexpr std::integral_constant<int, 0> none{};
-    constexpr std::integral_constant<int, PER> all{};
-    if (nk > 0) {
-        aim(0);
-        copies(0, 0, none, all);
-        fetch(0);
-        put(0);
-        if (nk > 1) {
-            aim(C::BK);
-            copies(1, C::BK, none, all);
-            fetch(C::BK);
-        }
-        if (DMA_A && DMA_B && nk > 1)
-            __builtin_amdgcn_s_waitcnt(LL_VMCNT(PER));
-        else
-            __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));
-    }
+    const int nk = cdiv(klen, C::BK);
+    constexpr int BR = C::FM == 8 ? 2 : 1;        // rows of the last step before the barrier
+    constexpr int AFTER = C::FM - BR;             // and after it
+    aim(0);
+    static_for<ROWS2>([&](auto r) __attribute__((always_inline)) { load_piece(r, 0); });
+    aim(C::BK);
+    static_for<ROWS2>([&](auto r) __attribute__((always_inline)) {
+        store_piece(r, 0);
+        load_piece(r, C::BK);
+    });
+    aim(2 * C::BK);
+    static_for<AFTER>([&](auto r) __attribute__((always_inline)) {
+        store_piece(r, 1);
+        load_piece(r, 2 * C::BK);
+    });
     __syncthreads();
-    f16x8 fa[2][C::FM], fb[2][C::FN];
-    read_step(0, 0, fa[0], fb[0]);
-    auto body = [&](auto more, int kt) __attribute__((always_inline)) {
-        constexpr bool REFILL = decltype(more)::value;   // there is a stage kt + 2
+    f16x8 fa[C::FM], fb[2][C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+        if (i + 1 < C::FM)
+            fa[i] = read_a(0, 0, i);
+        fb[0][i] = read_b(0, 0, i);
+    }
+    // Row i of the products on step s's operands, with op(0), .., op(n - 1) dealt out among its
+    // MFMAs. Rows alternate in column order: neighbouring MFMAs share an operand, and the
+    // chip, power-limited on 16-bit products, keeps a higher clock.
+    auto row = [&](auto ii, const f16x8 (&b_)[C::FN], auto count, auto op) __attribute__((always_inline)) {
+        constexpr int i = decltype(ii)::value, n = decltype(count)::value;
+        static_for<C::FN>([&](auto jj) __attribute__((always_inline)) {
+            constexpr int q = decltype(jj)::value, j = (i & 1) ? C::FN - 1 - q : q;
+            if constexpr (C::WPE == 1)
+                mma_acc<BF16>(b_[j], fa[i], acc[i][j]);
+            else
+                acc[i][j] = mma<BF16>(b_[j], fa[i], acc[i][j]);
+            __builtin_amdgcn_sched_barrier(0);
+            constexpr int lo = q * n / C::FN, hi = (q + 1) * n / C::FN;
+            static_for<hi - lo>([&](auto k) __attribute__((always_inline)) { op(std::integral_constant<int, lo + decltype(k)::value>{}); });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    if constexpr (C::WPE == 1)
+        settle();
+    for (int kt = 0; kt < nk; ++kt) {
         const int buf = kt & 1;
         asm volatile("" : "+v"(at_a), "+v"(at_b));   // (the blocks' addresses are made anew, not kept in registers)
-        read_step(buf, 1, fa[1], fb[1]);
-        __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int i = 0; i < C::FM; ++i)
-            mfma_row(i, fa[0], fb[0]);
-        __builtin_amdgcn_s_setprio(0);
-        pin();
-        if (REFILL || kt + 1 < nk) {
-            put(buf ^ 1);
-            __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));   // stage kt + 1 has landed
-        }
-        __syncthreads();
-        if (REFILL || kt + 1 < nk)
-            read_step(buf ^ 1, 0, fa[0], fb[0]);
-        const int k0 = (kt + 2) * C::BK;
-        if constexpr (REFILL) {
-            aim(k0);
-            fetch(k0);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
-        // the copies follow the first rows of products, not one burst that the matrix cores
-        // would wait through
-        constexpr int CROWS = 2, G = (PER + CROWS - 1) / CROWS;
         static_for<C::FM>([&](auto ii) __attribute__((always_inline)) {
             constexpr int i = decltype(ii)::value;
-            mfma_row(i, fa[1], fb[1]);
-            if constexpr (REFILL && PER > 0 && i < CROWS) {
-                __builtin_amdgcn_sched_barrier(0);
-                copies(buf, k0, std::integral_constant<int, i * G>{}, std::integral_constant<int, G>{});
-                __builtin_amdgcn_sched_barrier(0);
+            row(ii, fb[0], std::integral_constant<int, 4>{}, [&](auto k) __attribute__((always_inline)) {
+                constexpr int o = decltype(k)::value, r = AFTER + i;
+                if constexpr (o == 0) {
+                    if constexpr (i == 0)
+                        fa[C::FM - 1] = read_a(buf, 0, C::FM - 1);
+                    else
+                        fa[i - 1] = read_a(buf, 1, i - 1);
+                } else if constexpr (o == 1) {
+                    fb[1][i] = read_b(buf, 1, i);
+                } else if constexpr (o == 2) {
+                    store_piece(std::integral_constant<int, r>{}, buf ^ 1);
+                } else {
+                    load_piece(std::integral_constant<int, r>{}, (kt + 2) * C::BK);
+                }
+            });
+        });
+        static_for<C::FM>([&](auto ii) __attribute__((always_inline)) {
+            constexpr int i = decltype(ii)::value, after = i - BR;   // rows since the barrier
+            if constexpr (after == 0) {
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                aim((kt + 3) * C::BK);
             }
+            // the last rows have FN blocks of B to read; the first of them two more than one each
+            constexpr int extra = C::FN - AFTER;
+            row(ii, fb[1], std::integral_constant<int, (after >= 0 && after < extra ? 6 : 4)>{}, [&](auto k) __attribute__((always_inline)) {
+                constexpr int o = decltype(k)::value, r = after >= 0 ? after : ROWS2 + after;
+                if constexpr (o == 0) {
+                    if constexpr (i == 0)
+                        fa[C::FM - 1] = read_a(buf, 1, C::FM - 1);
+                    else if constexpr (after >= 0)
+                        fa[i - 1] = read_a(buf ^ 1, 0, i - 1);   // (after the last stage: of no use)
+                } else if constexpr (o == 1) {
+                    if constexpr (after >= 0)
+                        fb[0][after] = read_b(buf ^ 1, 0, after);
+                } else if constexpr (o == 2) {
+                    store_piece(std::integral_constant<int, r>{}, after >= 0 ? buf : buf ^ 1);
+                } else if constexpr (o == 3) {
+                    load_piece(std::integral_constant<int, r>{}, (kt + (after >= 0 ? 3 : 2)) * C::BK);
+                } else if constexpr (o == 4) {
+                    fb[0][AFTER + after] = read_b(buf ^ 1, 0, AFTER + after);
+                } else if constexpr (after < BR - 1) {
+                    fa[after] = read_a(buf ^ 1, 0, after);   // (of the rows before the barrier)
+                }
+            });
         });
         __builtin_amdgcn_s_setprio(0);
-        pin();
-    };
-    int kt = 0;
-    for (; kt + 2 < nk; ++kt)
-        body(std::true_type{}, kt);
-    for (; kt < nk; ++kt)
-        body(std::false_type{}, kt);
+    }
+    if constexpr (C::WPE == 1)
+        settle();
 
-    // The write-back, 64 rows of the wave's block at a time through its own part of the
-    // LDS, then eight rows a turn of a loop. (All of it unrolled is more code than the
-    // instruction cache holds: 2.3 ms where this takes 0.2.) The next turn's R, or C for beta, is
-    // on its way during a turn.
+    // The write-back, 64 x 64 of the wave's block at a time through its own part of the LDS,
+    // a quarter of those rows a turn of a loop: what depends on the quarter is its stores
+    // into LDS alone, and the rest is code once. (All of it unrolled is more than the
+    // instruction cache holds, 2.3 ms for a product that takes 0.2; eight rows at a time one
+    // after the other, with a wait for each, took 37 us a tile of 256 x 256.)
     __syncthreads();   // the ring is read no more
     float *turn = reinterpret_cast<float *>(lds_bytes) + wave * 64 * PITCH;
     const int rl = lane >> 3, cl = (lane & 7) * 8;
-    const int col = n0 + wn * C::WTN + cl, n = p.N - col;
-    static_assert(C::WTN == 64 && C::WTM % 64 == 0, "eight lanes a row");
     const void *more = OP == L16_FWD ? p.R : p.beta != 0.0f ? p.C : nullptr;
     const int64_t more_ld = OP == L16_FWD ? p.ldr : p.ldc;
-    float bias[8];
-    if constexpr (OP == L16_FWD)
-        load_row<LL_TYPE_F32, 8>(p.bias + (int64_t)g * p.N + col, p.bias != nullptr ? n : 0, bias);
-    static_for<C::WTM / 64>([&](auto hh) __attribute__((always_inline)) {
-        constexpr int half = decltype(hh)::value;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j)
-                *reinterpret_cast<f32x4 *>(turn + (16 * i + (lane & 15)) * PITCH + 16 * j + 4 * (lane >> 4)) = acc[4 * half + i][j];
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (the wave's own rows: no barrier)
-        const int row0 = m0 + wm * C::WTM + 64 * half + rl;
-        float next[8];
-        load8<BF16>(p.ctype, more, c_off + (int64_t)row0 * more_ld + col, more != nullptr && row0 < m_end ? n : 0, next);
+    constexpr int QN = C::WTN / 64, QUARTERS = C::WTM / 64 * QN;
+    const bool inside = m0 + BM <= m_end && n0 + BM <= p.N;
 #pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
-            const int row = row0 + 8 * q;
-            float v[8], r[8];
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(turn + (8 * q + rl) * PITCH + cl);
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(turn + (8 * q + rl) * PITCH + cl + 4);
+    for (int quarter = 0; quarter < QUARTERS; ++quarter) {
+        static_for<QUARTERS>([&](auto qq) __attribute__((always_inline)) {
+            constexpr int Q = decltype(qq)::value;
+            if (quarter == Q) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = lo[e], v[4 + e] = hi[e];
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                r[e] = next[e];
-            load8<BF16>(p.ctype, more, c_off + (int64_t)(row + 8) * more_ld + col,
-                        more != nullptr && q < 7 && row + 8 < m_end ? n : 0, next);
-            const bool live = row < m_end && n > 0;
-            if constexpr (OP == L16_FWD) {
-                finish_fwd<BF16>(p, v, bias, r, row, col, n, live);
-            } else if (live) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    v[e] = __builtin_fmaf(p.beta, r[e], v[e]);   // (r is 0 where beta is)
-                store8<BF16>(p.ctype, p.C, c_off + (int64_t)row * p.ldc + col, n, v);
+                    for (int j = 0; j < 4; ++j)
+                        *reinterpret_cast<f32x4 *>(turn + (16 * i + (lane & 15)) * PITCH + 16 * j + 4 * (lane >> 4)) =
+                            acc[4 * (Q / QN) + i][4 * (Q % QN) + j];
+                asm volatile("; quarter %0" ::"n"(Q) : "memory");   // (merged branches would index acc, in memory)
             }
+        });
+        const int col = n0 + wn * C::WTN + 64 * (quarter % QN) + cl, n = p.N - col;
+        const int row0 = m0 + wm * C::WTM + 64 * (quarter / QN) + rl;
+        float bias[8];
+        if constexpr (OP == L16_FWD)
+            load_row<LL_TYPE_F32, 8>(p.bias + (int64_t)g * p.N + col, p.bias != nullptr ? n : 0, bias);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // (the wave's own rows: no barrier)
+        // U eight-row groups from row 8 q of the 64 on
+        auto rows = [&](auto whole, auto uu, int q) __attribute__((always_inline)) {
+            constexpr bool WHOLE = decltype(whole)::value;   // all of them inside C
+            constexpr int U = decltype(uu)::value;
+            float v[U][8], r[U][8];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int row = row0 + 8 * (q + u);
+                if (more != nullptr) {
+                    load8<BF16>(p.ctype, more, c_off + (int64_t)row * more_ld + col, WHOLE ? 8 : row < m_end ? n : 0, r[u]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        r[u][e] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const f32x4 lo = *reinterpret_cast<const f32x4 *>(turn + (8 * (q + u) + rl) * PITCH + cl);
+                const f32x4 hi = *reinterpret_cast<const f32x4 *>(turn + (8 * (q + u) + rl) * PITCH + cl + 4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[u][e] = lo[e], v[u][4 + e] = hi[e];
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int row = row0 + 8 * (q + u);
+                const bool live = WHOLE || (row < m_end && n > 0);
+                if constexpr (OP == L16_FWD) {
+                    finish_fwd<BF16>(p, v[u], bias, r[u], row, col, WHOLE ? 8 : n, live);
+                } else if (live) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        v[u][e] = __builtin_fmaf(p.beta, r[u][e], v[u][e]);   // (r is 0 where beta is)
+                    store8<BF16>(p.ctype, p.C, c_off + (int64_t)row * p.ldc + col, WHOLE ? 8 : n, v[u]);
+                }
+            }
+        };
+        if (inside) {
+#pragma unroll 1
+            for (int q = 0; q < 8; q += 2)
+                rows(std::true_type{}, std::integral_constant<int, 2>{}, q);
+        } else {
+#pragma unroll 1
+            for (int q = 0; q < 8; ++q)
+                rows(std::false_type{}, std::integral_constant<int, 1>{}, q);
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    });
+    }
 }
 
 // ---- launches -------------------------------------------------------------------
@@ -604,7 +628,7 @@ inline bool prefer_256(int64_t t256, int64_t t128, int cus)
 }
 
 // The products whose groups are of C's rows.
-template <int OP, bool BF16, int BM, int SB, bool DMA>
+template <int OP, bool BF16, int BM, int SB, bool VEC>
 hipError_t launch_rows_bm(L16Params p, hipStream_t s)
 {
     p.tiles_n = cdiv(p.N, BM);
@@ -614,7 +638,7 @@ hipError_t launch_rows_bm(L16Params p, hipStream_t s)
     const int64_t tiles = rows * p.tiles_n;
     if (tiles > max_grid_x(Cfg<BM>::NT))
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((l16_tile_kernel<OP, BF16, BM, ROWS, SB, DMA>), dim3((unsigned)tiles), dim3(Cfg<BM>::NT), 0, s, p);
+    hipLaunchKernelGGL((l16_tile_kernel<OP, BF16, BM, ROWS, SB, VEC>), dim3((unsigned)tiles), dim3(Cfg<BM>::NT), 0, s, p);
     return hipGetLastError();
 }
 
