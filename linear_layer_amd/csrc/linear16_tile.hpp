@@ -159,6 +159,13 @@ struct Operand {
                 cur[v] = SIDE == ROWS && slot_col(v * C::NT + tid) >= left ? kPastEnd : off[v];
         }
     }
+    // Piece J, loaded by an operand like this one, with its scale.
+    __device__ __forceinline__ void take(const Operand &o, int j)
+    {
+        reg[j] = o.reg[j];
+        if constexpr (SIDE == COLS8)
+            sc[j] = o.sc[j];
+    }
     template <int J>
     __device__ __forceinline__ void load(int k0, int tid)
     {
@@ -234,13 +241,15 @@ struct Operand {
         else   // (lanes 4 j' .. + 3 of 16 point at the four 8-byte pieces of k-row j')
             return (uint32_t)((8 * grp + (j >> 2)) * 2 * BM + (((o >> 4) ^ cols_swz(8 * grp + (j >> 2))) << 5) + 8 * (j & 3));
     }
-    // Block i of k-step s, `at` being the stage's LDS address plus lane_addr.
-    __device__ __forceinline__ static f16x8 read(uint32_t at, int i, int s)
+    // The stage's LDS address plus lane_addr, for k-step s.
+    __device__ __forceinline__ static uint32_t step_addr(uint32_t at, int s) { return SIDE == ROWS ? at ^ (64u * s) : at + 64u * BM * s; }
+    // Block i, `at` being its step's address.
+    __device__ __forceinline__ static f16x8 read(uint32_t at, int i)
     {
         if constexpr (SIDE == ROWS) {
-            return *(LdsF16x8)(uintptr_t)((at ^ (64u * s)) + 2048u * i);
+            return *(LdsF16x8)(uintptr_t)(at + 2048u * i);
         } else {
-            const uint32_t a = (at ^ (32u * i)) + 64u * BM * s;
+            const uint32_t a = at ^ (32u * i);
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)(uintptr_t)a);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsS16x4)(uintptr_t)(a + 8u * BM));
             return __builtin_bit_cast(f16x8, (short __attribute__((ext_vector_type(8)))){lo[0], lo[1], lo[2], lo[3], hi[0],
@@ -395,17 +404,23 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     const uint32_t base_a = lds_addr(&ring[0][0][0]), base_b = lds_addr(&ring[1][0][0]);
     constexpr uint32_t STAGE_BYTES = C::STAGE * 2;
     uint32_t at_a = base_a + a.lane_addr(wm * C::WTM, lane), at_b = base_b + b.lane_addr(wn * C::WTN, lane);
-    auto read_a = [&](int buf, int s, int i) __attribute__((always_inline)) { return a.read(at_a + buf * STAGE_BYTES, i, s); };
-    auto read_b = [&](int buf, int s, int j) __attribute__((always_inline)) { return b.read(at_b + buf * STAGE_BYTES, j, s); };
+    // Step s of the stage in buffer buf: where its operands are read. (Opaque to the compiler, so
+    // that the blocks are at constant offsets from it and nothing about it is kept in registers
+    // over the loop.)
+    auto step = [&](int buf, int s, uint32_t &xa, uint32_t &xb) __attribute__((always_inline)) {
+        xa = a.step_addr(at_a + buf * STAGE_BYTES, s);
+        xb = b.step_addr(at_b + buf * STAGE_BYTES, s);
+        asm volatile("" : "+v"(xa), "+v"(xb));
+    };
     static_assert(C::FM == C::FN, "a block of each operand a row of products");
     // Stages go through two buffers, two steps a stage. While a step multiplies, the next step's
-    // operands are read: its blocks of B into a second set of registers, a block of A into the
-    // registers that a row of products has done with (the last one at the step's own start). The
-    // barrier stands after the first rows of a stage's last step, when every operand
-    // of the stage is in registers: it publishes the next stage and frees this one's buffer. In
-    // the rows up to the next barrier the thread's pieces of the stage after next go there, each
-    // followed by the load of its successor. Past the range's end zeros are loaded and
-    // stored, and not used.
+    // operands are read: its blocks of B into a second set of registers, in the first rows, as
+    // the next step's first row needs all of them; a block of A into the registers that a
+    // row of products has done with (the last one at the step's own start). The barrier
+    // stands after the first rows of a stage's last step, when every operand of the stage is in
+    // registers: it publishes the next stage and frees this one's buffer. After it the
+    // thread's pieces of the stage after next go there, a row each, each followed by the load of
+    // its successor. Past the range's end zeros are loaded and stored, and not used.
     //
     // A wave issues an instruction every four cycles and an MFMA occupies the matrix core for
     // sixteen, so what stands between two MFMAs costs nothing up to three instructions; one
@@ -442,10 +457,35 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     aim(0);
     static_for<ROWS2>([&](auto r) __attribute__((always_inline)) { load_piece(r, 0); });
     aim(C::BK);
-    static_for<ROWS2>([&](auto r) __attribute__((always_inline)) {
-        store_piece(r, 0);
-        load_piece(r, C::BK);
-    });
+    {
+        // the first pieces of stage 1 on their way with those of stage 0
+        auto a1 = a;
+        auto b1 = b;
+        static_for<AFTER>([&](auto rr) __attribute__((always_inline)) {
+            constexpr int r = decltype(rr)::value;
+            if constexpr (r % 2 == 0)
+                a1.template load<r / 2>(C::BK, tid);
+            else if constexpr (SB != COLS8)
+                b1.template load<r / 2>(C::BK, tid);
+            else if constexpr (r % 4 == 1)
+                b1.template load<r / 4>(C::BK, tid);
+        });
+        static_for<ROWS2>([&](auto rr) __attribute__((always_inline)) {
+            constexpr int r = decltype(rr)::value;
+            store_piece(rr, 0);
+            if constexpr (r >= AFTER)
+                load_piece(rr, C::BK);
+        });
+        static_for<AFTER>([&](auto rr) __attribute__((always_inline)) {
+            constexpr int r = decltype(rr)::value;
+            if constexpr (r % 2 == 0)
+                a.take(a1, r / 2);
+            else if constexpr (SB != COLS8)
+                b.take(b1, r / 2);
+            else if constexpr (r % 4 == 1)
+                b.take(b1, r / 4);
+        });
+    }
     aim(2 * C::BK);
     static_for<AFTER>([&](auto r) __attribute__((always_inline)) {
         store_piece(r, 1);
@@ -453,11 +493,15 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     });
     __syncthreads();
     f16x8 fa[C::FM], fb[2][C::FN];
+    {
+        uint32_t xa, xb;
+        step(0, 0, xa, xb);
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-        if (i + 1 < C::FM)
-            fa[i] = read_a(0, 0, i);
-        fb[0][i] = read_b(0, 0, i);
+        for (int i = 0; i < C::FM; ++i) {
+            if (i + 1 < C::FM)
+                fa[i] = a.read(xa, i);
+            fb[0][i] = b.read(xb, i);
+        }
     }
     // Row i of the products on step s's operands, with op(0), .., op(n - 1) dealt out among its
     // MFMAs. Rows alternate in column order: neighbouring MFMAs share an operand, and the
@@ -478,56 +522,70 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     };
     if constexpr (C::WPE == 1)
         settle();
+    constexpr int F = C::FM;
     for (int kt = 0; kt < nk; ++kt) {
         const int buf = kt & 1;
-        asm volatile("" : "+v"(at_a), "+v"(at_b));   // (the blocks' addresses are made anew, not kept in registers)
+        uint32_t xa0, xa1, xb1, unused;
+        step(buf, 0, xa0, unused);
+        step(buf, 1, xa1, xb1);
         __builtin_amdgcn_s_setprio(1);
-        static_for<C::FM>([&](auto ii) __attribute__((always_inline)) {
+        static_for<F>([&](auto ii) __attribute__((always_inline)) {
+            // two blocks of B in the first rows, two pieces in the last
             constexpr int i = decltype(ii)::value;
-            row(ii, fb[0], std::integral_constant<int, 4>{}, [&](auto k) __attribute__((always_inline)) {
-                constexpr int o = decltype(k)::value, r = AFTER + i;
-                if constexpr (o == 0) {
+            constexpr bool more_b = 2 * i < F, more_p = i >= F - BR;
+            row(ii, fb[0], std::integral_constant<int, 3 + (more_b ? 2 : 0) + (more_p ? 2 : 0)>{}, [&](auto k) __attribute__((always_inline)) {
+                constexpr int o = decltype(k)::value, q = more_b ? o - 2 : o;
+                if constexpr (more_b && o < 2) {
+                    fb[1][2 * i + o] = b.read(xb1, 2 * i + o);
+                } else if constexpr (q == 0) {
                     if constexpr (i == 0)
-                        fa[C::FM - 1] = read_a(buf, 0, C::FM - 1);
+                        fa[F - 1] = a.read(xa0, F - 1);
                     else
-                        fa[i - 1] = read_a(buf, 1, i - 1);
-                } else if constexpr (o == 1) {
-                    fb[1][i] = read_b(buf, 1, i);
-                } else if constexpr (o == 2) {
-                    store_piece(std::integral_constant<int, r>{}, buf ^ 1);
+                        fa[i - 1] = a.read(xa1, i - 1);
                 } else {
-                    load_piece(std::integral_constant<int, r>{}, (kt + 2) * C::BK);
+                    constexpr int r = AFTER + i + (q > 2 ? BR : 0);
+                    if constexpr (q % 2 == 1)
+                        store_piece(std::integral_constant<int, r>{}, buf ^ 1);
+                    else
+                        load_piece(std::integral_constant<int, r>{}, (kt + 2) * C::BK);
                 }
             });
         });
-        static_for<C::FM>([&](auto ii) __attribute__((always_inline)) {
+        uint32_t na, nb;
+        static_for<F>([&](auto ii) __attribute__((always_inline)) {
             constexpr int i = decltype(ii)::value, after = i - BR;   // rows since the barrier
-            if constexpr (after == 0) {
+            if constexpr (after == 0)
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-                aim((kt + 3) * C::BK);
+            if constexpr (after < 0) {
+                row(ii, fb[1], std::integral_constant<int, 4>{}, [&](auto k) __attribute__((always_inline)) {
+                    constexpr int o = decltype(k)::value;
+                    if constexpr (i == 0 && o == 0)
+                        fa[F - 1] = a.read(xa1, F - 1);
+                    else if constexpr (i == 0 && o == 1)
+                        step(buf ^ 1, 0, na, nb);
+                    else if constexpr (i == BR - 1 && o == 2)
+                        a.aim((kt + 3) * C::BK, tid);
+                    else if constexpr (i == BR - 1 && o == 3)
+                        b.aim((kt + 3) * C::BK, tid);
+                });
+            } else {
+                // (after the last stage what is read here is of no use)
+                constexpr bool more_b = 2 * after < F;
+                constexpr bool more_a = after < BR - 1;          // of the rows before the barrier
+                row(ii, fb[1], std::integral_constant<int, 3 + (more_b ? 2 : 0) + (more_a ? 1 : 0)>{}, [&](auto k) __attribute__((always_inline)) {
+                    constexpr int o = decltype(k)::value, q = more_b ? o - 2 : o;
+                    if constexpr (more_b && o < 2)
+                        fb[0][2 * after + o] = b.read(nb, 2 * after + o);
+                    else if constexpr (q == 0)
+                        fa[i - 1] = a.read(na, i - 1);
+                    else if constexpr (q == 1)
+                        store_piece(std::integral_constant<int, after>{}, buf);
+                    else if constexpr (q == 2)
+                        load_piece(std::integral_constant<int, after>{}, (kt + 3) * C::BK);
+                    else
+                        fa[after] = a.read(na, after);
+                });
             }
-            // the last rows have FN blocks of B to read; the first of them two more than one each
-            constexpr int extra = C::FN - AFTER;
-            row(ii, fb[1], std::integral_constant<int, (after >= 0 && after < extra ? 6 : 4)>{}, [&](auto k) __attribute__((always_inline)) {
-                constexpr int o = decltype(k)::value, r = after >= 0 ? after : ROWS2 + after;
-                if constexpr (o == 0) {
-                    if constexpr (i == 0)
-                        fa[C::FM - 1] = read_a(buf, 1, C::FM - 1);
-                    else if constexpr (after >= 0)
-                        fa[i - 1] = read_a(buf ^ 1, 0, i - 1);   // (after the last stage: of no use)
-                } else if constexpr (o == 1) {
-                    if constexpr (after >= 0)
-                        fb[0][after] = read_b(buf ^ 1, 0, after);
-                } else if constexpr (o == 2) {
-                    store_piece(std::integral_constant<int, r>{}, after >= 0 ? buf : buf ^ 1);
-                } else if constexpr (o == 3) {
-                    load_piece(std::integral_constant<int, r>{}, (kt + (after >= 0 ? 3 : 2)) * C::BK);
-                } else if constexpr (o == 4) {
-                    fb[0][AFTER + after] = read_b(buf ^ 1, 0, AFTER + after);
-                } else if constexpr (after < BR - 1) {
-                    fa[after] = read_a(buf ^ 1, 0, after);   // (of the rows before the barrier)
-                }
-            });
         });
         __builtin_amdgcn_s_setprio(0);
     }
@@ -606,8 +664,8 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         };
         if (inside) {
 #pragma unroll 1
-            for (int q = 0; q < 8; q += 2)
-                rows(std::true_type{}, std::integral_constant<int, 2>{}, q);
+            for (int q = 0; q < 8; q += 4)
+                rows(std::true_type{}, std::integral_constant<int, 4>{}, q);
         } else {
 #pragma unroll 1
             for (int q = 0; q < 8; ++q)
