@@ -13,15 +13,12 @@
 //   COLS8  as COLS, from E4M3 codes and scales: 16 codes a load into registers, decoded and
 //          stored as the 32-byte unit that they are in 16 bits. Decoding on the way into LDS
 //          is done once a workgroup; after it, by every wave that reads the stage.
-// Every 16 bytes go through registers: loaded a whole stage before they are stored into LDS, and
-// stored up to a stage before they are read, one load and one store after each row of
-// MFMAs. (Copies straight into LDS have to land between two barriers, which leaves them half
-// that time: 8192^3 1.26 PFLOP/s where this reaches 1.5.) Rows on 16 bytes (VEC) are read by
-// buffer loads whose descriptor ends with the tile's last row and the contracted range, so
-// that what lies past them arrives as zeros without a test; only where a stage crosses the
-// range's end inside the rows do lanes take an offset past the descriptor. Rows off 16 bytes
-// are read 16 bytes a load at any alignment, the chunk that crosses the row's end value by
-// value.
+// ROWS and COLS on 16 bytes (VEC) are copied straight into LDS by buffer loads, 16 bytes a
+// lane, whose descriptor ends with the tile's last row and the contracted range: what lies
+// past them arrives as zeros without a test, and only where a stage crosses the range's end
+// inside the rows do lanes take an offset past the descriptor. Rows off 16 bytes and COLS8
+// go through registers, loaded a whole stage before they are stored into LDS: 16 bytes a load
+// at any alignment, the chunk that crosses the row's end value by value.
 //
 // The MFMA takes the operand of C's columns first, so a lane gets four neighbouring columns
 // of a row; the write-back turns them around in LDS to eight a lane, 128 bytes of a row (16
@@ -100,6 +97,21 @@ __device__ __forceinline__ void static_for(F f)
 
 constexpr uint32_t kPastEnd = 0x80000000u;   // past the end of every buffer here: 256 rows of less than 2^21 values
 
+// buffer_load_dwordx4 into LDS: this lane's 16 bytes at byte `off` of the buffer go to LDS
+// byte lds_base + 16 * lane, zeros where they lie past its end. Inline assembly, so that the
+// compiler does not take it for an LDS store that every LDS read must wait for; the caller
+// waits for the copies before the barrier that publishes them. The compiler's hazard checks
+// do not look inside: M0 may be used one wait state after its write. (Four more, for a
+// descriptor that v_readfirstlane might have written just before, would cost the matrix
+// cores as much as all the copies; descriptors here are made by scalar instructions.)
+__device__ __forceinline__ void lds_buffer_16(const u32x4 &buffer, uint32_t off, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds_base), "v"(off), "s"(buffer)
+                 : "memory", "m0");
+}
+
 typedef const __attribute__((address_space(3))) f16x8 *LdsF16x8;
 typedef __attribute__((address_space(3))) s16x4 *LdsS16x4;
 
@@ -108,6 +120,7 @@ typedef __attribute__((address_space(3))) s16x4 *LdsS16x4;
 template <bool BF16, int BM, int SIDE, bool VEC>
 struct Operand {
     using C = Cfg<BM>;
+    static constexpr bool DMA = VEC && SIDE != COLS8;
     static constexpr int PIECES = SIDE == COLS8 ? C::PIECES / 2 : C::PIECES;   // 16-byte pieces of memory a thread and stage
     static constexpr int KROWS = 512 / BM;   // k-rows of 1 KiB of a COLS stage
     const uint16_t *src;        // the tile's first row (ROWS) or column (COLS), k = 0
@@ -115,8 +128,8 @@ struct Operand {
     int64_t ld, lds;
     int lim, klen, col0;
     uint32_t off[2], cur[2];    // offset of piece 0, and of piece 1 where its swizzle is another; in the stage aimed at
-    __amdgpu_buffer_rsrc_t buf;
-    u32x4 reg[PIECES];
+    u32x4 buf;
+    u32x4 reg[DMA ? 1 : PIECES];
     uint32_t sc[SIDE == COLS8 ? PIECES : 1];
 
     // Piece j of a thread fills 16-byte slot (j * NW + wave) * 64 + lane of a stage: a wave fills 8
@@ -138,7 +151,7 @@ struct Operand {
     }
     __device__ __forceinline__ void start(int tid)
     {
-        if constexpr (VEC && SIDE != COLS8) {
+        if constexpr (DMA) {
 #pragma unroll
             for (int v = 0; v < SETS; ++v) {
                 const int s = v * C::NT + tid;
@@ -149,30 +162,28 @@ struct Operand {
     // The pieces loaded from now on are of the stage at k0 (past the range: zeros).
     __device__ __forceinline__ void aim(int k0, int tid)
     {
-        if constexpr (VEC && SIDE != COLS8) {
+        if constexpr (DMA) {
             const int left = min(klen - k0, C::BK), n = min(lim, BM);
             const int bytes = left <= 0 ? 0 : SIDE == ROWS ? (n - 1) * (int)(2 * ld) + 2 * left : (left - 1) * (int)(2 * ld) + 2 * n;
             const uint16_t *at = SIDE == ROWS ? src + k0 : src + (int64_t)k0 * ld;
-            buf = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(at), 0, bytes, 0x00020000);
+            buf = u32x4{(uint32_t)(uint64_t)at, (uint32_t)((uint64_t)at >> 32), (uint32_t)bytes, 0x00020000u};   // (addresses have 48 bits)
 #pragma unroll
             for (int v = 0; v < SETS; ++v)
                 cur[v] = SIDE == ROWS && slot_col(v * C::NT + tid) >= left ? kPastEnd : off[v];
         }
     }
-    // Piece J, loaded by an operand like this one, with its scale.
-    __device__ __forceinline__ void take(const Operand &o, int j)
+    // Copy J of this wave of the stage aimed at to the stage at LDS address `base`.
+    template <int J>
+    __device__ __forceinline__ void copy(uint32_t base, int wave) const
     {
-        reg[j] = o.reg[j];
-        if constexpr (SIDE == COLS8)
-            sc[j] = o.sc[j];
+        constexpr int v = J % SETS;
+        lds_buffer_16(buf, cur[v] + (J - v) * STRIDE * (uint32_t)(2 * ld), base + (J * C::NW + wave) * 1024);
     }
+    // The same through registers: its load, and a stage later its store.
     template <int J>
     __device__ __forceinline__ void load(int k0, int tid)
     {
-        if constexpr (VEC && SIDE != COLS8) {
-            constexpr int v = J % SETS;
-            reg[J] = __builtin_amdgcn_raw_buffer_load_b128(buf, cur[v] + (J - v) * STRIDE * (uint32_t)(2 * ld), 0, 0);
-        } else if constexpr (SIDE == COLS8) {
+        if constexpr (SIDE == COLS8) {
             reg[J] = u32x4{0u, 0u, 0u, 0u};
             sc[J] = 0;
             const int c = J * C::NT + tid, k = k0 + c / (BM / 16), col = c % (BM / 16) * 16;
@@ -418,87 +429,80 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     // the next step's first row needs all of them; a block of A into the registers that a
     // row of products has done with (the last one at the step's own start). The barrier
     // stands after the first rows of a stage's last step, when every operand of the stage is in
-    // registers: it publishes the next stage and frees this one's buffer. After it the
-    // thread's pieces of the stage after next go there, a row each, each followed by the load of
-    // its successor. Past the range's end zeros are loaded and stored, and not used.
+    // registers: it publishes the next stage and frees this one's buffer, which takes the stage
+    // after next: copies in the first half of the rows up to the next barrier, so that they have
+    // the other half to land in; pieces through registers in any of them, each followed by the
+    // load of its successor (those of COLS8, which are fewer, in the first half too: a wait for
+    // copies is one for them). Past the range's end come zeros, and are not used.
     //
     // A wave issues an instruction every four cycles and an MFMA occupies the matrix core for
     // sixteen, so what stands between two MFMAs costs nothing up to three instructions; one
     // wave a SIMD has no other to fill a longer gap. Hence the operations are dealt out
-    // singly among a row's MFMAs (all of them between rows: 8192^3 1.23 PFLOP/s).
-    constexpr int ROWS2 = 2 * C::FM;   // rows of products, and slots for a piece, of a stage
-    static_assert(C::FM == C::FN && C::PIECES == C::FM && decltype(b)::PIECES * (SB == COLS8 ? 2 : 1) == C::FM, "a piece a row");
-    // Slot r: the r/2nd piece of A, or of B (of COLS8 in every other one of its slots).
-    auto load_piece = [&](auto rr, int k0) __attribute__((always_inline)) {
-        constexpr int r = decltype(rr)::value;
-        if constexpr (r % 2 == 0)
-            a.template load<r / 2>(k0, tid);
-        else if constexpr (SB != COLS8)
-            b.template load<r / 2>(k0, tid);
-        else if constexpr (r % 4 == 1)
-            b.template load<r / 4>(k0, tid);
+    // singly among a row's MFMAs.
+    constexpr int F = C::FM, ROWS2 = 2 * F;       // rows of products of a step, of a stage
+    constexpr int BR = F == 8 ? 2 : 1;            // rows of the last step before the barrier
+    constexpr int AFTER = F - BR;                 // and after it
+    using OpA = decltype(a);
+    using OpB = decltype(b);
+    static_assert(C::FM == C::FN && C::PIECES == F, "a piece of each operand in two rows");
+    // The operations of row w after a barrier, A's and then B's.
+    struct Window {
+        static constexpr int a(int w) { return OpA::DMA ? w < F : w % 2 == 0 ? 2 : 0; }
+        static constexpr int b(int w)
+        {
+            return OpB::DMA ? w < F : w % 2 == 0 || (OpB::PIECES < F && w >= F) ? 0 : 2;
+        }
+        static constexpr int n(int w) { return a(w) + b(w); }
     };
-    auto store_piece = [&](auto rr, int buf) __attribute__((always_inline)) {
-        constexpr int r = decltype(rr)::value;
-        if constexpr (r % 2 == 0)
-            a.template store<r / 2>(ring[0][buf], tid);
-        else if constexpr (SB != COLS8)
-            b.template store<r / 2>(ring[1][buf], tid);
-        else if constexpr (r % 4 == 1)
-            b.template store<r / 4>(ring[1][buf], tid);
+    // Operation o of them: into buffer buf; the stage that registers are loaded with begins at k0.
+    auto window = [&](auto ww, auto oo, int buf, int k0) __attribute__((always_inline)) {
+        constexpr int w = decltype(ww)::value, o = decltype(oo)::value, q = o - Window::a(w);
+        if constexpr (q < 0) {
+            if constexpr (OpA::DMA)
+                a.template copy<w>(base_a + buf * STAGE_BYTES, wave);
+            else if constexpr (o == 0)
+                a.template store<w / 2>(ring[0][buf], tid);
+            else
+                a.template load<w / 2>(k0, tid);
+        } else {
+            if constexpr (OpB::DMA)
+                b.template copy<w>(base_b + buf * STAGE_BYTES, wave);
+            else if constexpr (q == 0)
+                b.template store<w / 2>(ring[1][buf], tid);
+            else
+                b.template load<w / 2>(k0, tid);
+        }
     };
-    auto aim = [&](int k0) __attribute__((always_inline)) {
-        a.aim(k0, tid);
-        b.aim(k0, tid);
+    // All of rows first .. first + count - 1's, at once.
+    auto windows = [&](auto first, auto count, int buf, int k0) __attribute__((always_inline)) {
+        static_for<decltype(count)::value>([&](auto i) __attribute__((always_inline)) {
+            constexpr int w = decltype(first)::value + decltype(i)::value;
+            static_for<Window::n(w)>([&](auto o) __attribute__((always_inline)) { window(std::integral_constant<int, w>{}, o, buf, k0); });
+        });
     };
     const int nk = cdiv(klen, C::BK);
-    constexpr int BR = C::FM == 8 ? 2 : 1;        // rows of the last step before the barrier
-    constexpr int AFTER = C::FM - BR;             // and after it
-    aim(0);
-    static_for<ROWS2>([&](auto r) __attribute__((always_inline)) { load_piece(r, 0); });
-    aim(C::BK);
-    {
-        // the first pieces of stage 1 on their way with those of stage 0
-        auto a1 = a;
-        auto b1 = b;
-        static_for<AFTER>([&](auto rr) __attribute__((always_inline)) {
-            constexpr int r = decltype(rr)::value;
-            if constexpr (r % 2 == 0)
-                a1.template load<r / 2>(C::BK, tid);
-            else if constexpr (SB != COLS8)
-                b1.template load<r / 2>(C::BK, tid);
-            else if constexpr (r % 4 == 1)
-                b1.template load<r / 4>(C::BK, tid);
-        });
-        static_for<ROWS2>([&](auto rr) __attribute__((always_inline)) {
-            constexpr int r = decltype(rr)::value;
-            store_piece(rr, 0);
-            if constexpr (r >= AFTER)
-                load_piece(rr, C::BK);
-        });
-        static_for<AFTER>([&](auto rr) __attribute__((always_inline)) {
-            constexpr int r = decltype(rr)::value;
-            if constexpr (r % 2 == 0)
-                a.take(a1, r / 2);
-            else if constexpr (SB != COLS8)
-                b.take(b1, r / 2);
-            else if constexpr (r % 4 == 1)
-                b.take(b1, r / 4);
-        });
-    }
-    aim(2 * C::BK);
-    static_for<AFTER>([&](auto r) __attribute__((always_inline)) {
-        store_piece(r, 1);
-        load_piece(r, 2 * C::BK);
-    });
-    __syncthreads();
-    f16x8 fa[C::FM], fb[2][C::FN];
+    if constexpr (!OpA::DMA)
+        static_for<OpA::PIECES>([&](auto j) __attribute__((always_inline)) { a.template load<decltype(j)::value>(0, tid); });
+    if constexpr (!OpB::DMA)
+        static_for<OpB::PIECES>([&](auto j) __attribute__((always_inline)) { b.template load<decltype(j)::value>(0, tid); });
+    a.aim(0, tid);
+    b.aim(0, tid);
+    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, ROWS2>{}, 0, C::BK);
+    a.aim(C::BK, tid);
+    b.aim(C::BK, tid);
+    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, AFTER>{}, 1, 2 * C::BK);
+    if constexpr (OpA::DMA && OpB::DMA)
+        __builtin_amdgcn_s_waitcnt(LL_VMCNT(2 * AFTER));   // (stage 1's copies may still be on their way)
+    else if constexpr (OpA::DMA || OpB::DMA)
+        __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    f16x8 fa[F], fb[2][F];
     {
         uint32_t xa, xb;
         step(0, 0, xa, xb);
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-            if (i + 1 < C::FM)
+        for (int i = 0; i < F; ++i) {
+            if (i + 1 < F)
                 fa[i] = a.read(xa, i);
             fb[0][i] = b.read(xb, i);
         }
@@ -522,7 +526,6 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     };
     if constexpr (C::WPE == 1)
         settle();
-    constexpr int F = C::FM;
     for (int kt = 0; kt < nk; ++kt) {
         const int buf = kt & 1;
         uint32_t xa0, xa1, xb1, unused;
@@ -530,60 +533,59 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         step(buf, 1, xa1, xb1);
         __builtin_amdgcn_s_setprio(1);
         static_for<F>([&](auto ii) __attribute__((always_inline)) {
-            // two blocks of B in the first rows, two pieces in the last
-            constexpr int i = decltype(ii)::value;
-            constexpr bool more_b = 2 * i < F, more_p = i >= F - BR;
-            row(ii, fb[0], std::integral_constant<int, 3 + (more_b ? 2 : 0) + (more_p ? 2 : 0)>{}, [&](auto k) __attribute__((always_inline)) {
-                constexpr int o = decltype(k)::value, q = more_b ? o - 2 : o;
-                if constexpr (more_b && o < 2) {
+            // two blocks of B in the first rows, and one of A; the last rows have the operations
+            // of those before the barrier too
+            constexpr int i = decltype(ii)::value, nb = 2 * i < F ? 2 : 0, w = AFTER + i, w2 = w + BR;
+            constexpr int n = Window::n(w), n2 = i >= F - BR ? Window::n(w2) : 0;
+            row(ii, fb[0], std::integral_constant<int, nb + 1 + n + n2>{}, [&](auto k) __attribute__((always_inline)) {
+                constexpr int o = decltype(k)::value, q = o - nb - 1;
+                if constexpr (o < nb) {
                     fb[1][2 * i + o] = b.read(xb1, 2 * i + o);
-                } else if constexpr (q == 0) {
+                } else if constexpr (q < 0) {
                     if constexpr (i == 0)
                         fa[F - 1] = a.read(xa0, F - 1);
                     else
                         fa[i - 1] = a.read(xa1, i - 1);
+                } else if constexpr (q < n) {
+                    window(std::integral_constant<int, w>{}, std::integral_constant<int, q>{}, buf ^ 1, (kt + 2) * C::BK);
                 } else {
-                    constexpr int r = AFTER + i + (q > 2 ? BR : 0);
-                    if constexpr (q % 2 == 1)
-                        store_piece(std::integral_constant<int, r>{}, buf ^ 1);
-                    else
-                        load_piece(std::integral_constant<int, r>{}, (kt + 2) * C::BK);
+                    window(std::integral_constant<int, w2>{}, std::integral_constant<int, q - n>{}, buf ^ 1, (kt + 2) * C::BK);
                 }
             });
         });
-        uint32_t na, nb;
+        uint32_t xan, xbn;
         static_for<F>([&](auto ii) __attribute__((always_inline)) {
             constexpr int i = decltype(ii)::value, after = i - BR;   // rows since the barrier
-            if constexpr (after == 0)
+            if constexpr (after == 0) {
+                if constexpr (OpA::DMA || OpB::DMA)
+                    __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));   // stage kt + 1 has landed
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            }
             if constexpr (after < 0) {
                 row(ii, fb[1], std::integral_constant<int, 4>{}, [&](auto k) __attribute__((always_inline)) {
                     constexpr int o = decltype(k)::value;
                     if constexpr (i == 0 && o == 0)
                         fa[F - 1] = a.read(xa1, F - 1);
                     else if constexpr (i == 0 && o == 1)
-                        step(buf ^ 1, 0, na, nb);
+                        step(buf ^ 1, 0, xan, xbn);
                     else if constexpr (i == BR - 1 && o == 2)
-                        a.aim((kt + 3) * C::BK, tid);
+                        a.aim((kt + 2) * C::BK, tid);
                     else if constexpr (i == BR - 1 && o == 3)
-                        b.aim((kt + 3) * C::BK, tid);
+                        b.aim((kt + 2) * C::BK, tid);
                 });
             } else {
                 // (after the last stage what is read here is of no use)
-                constexpr bool more_b = 2 * after < F;
-                constexpr bool more_a = after < BR - 1;          // of the rows before the barrier
-                row(ii, fb[1], std::integral_constant<int, 3 + (more_b ? 2 : 0) + (more_a ? 1 : 0)>{}, [&](auto k) __attribute__((always_inline)) {
-                    constexpr int o = decltype(k)::value, q = more_b ? o - 2 : o;
-                    if constexpr (more_b && o < 2)
-                        fb[0][2 * after + o] = b.read(nb, 2 * after + o);
-                    else if constexpr (q == 0)
-                        fa[i - 1] = a.read(na, i - 1);
-                    else if constexpr (q == 1)
-                        store_piece(std::integral_constant<int, after>{}, buf);
-                    else if constexpr (q == 2)
-                        load_piece(std::integral_constant<int, after>{}, (kt + 3) * C::BK);
+                constexpr int nb = 2 * after < F ? 2 : 0, na = after < BR - 1 ? 2 : 1;   // (a block of A of the rows before the barrier)
+                row(ii, fb[1], std::integral_constant<int, nb + na + Window::n(after)>{}, [&](auto k) __attribute__((always_inline)) {
+                    constexpr int o = decltype(k)::value, q = o - nb - na;
+                    if constexpr (o < nb)
+                        fb[0][2 * after + o] = b.read(xbn, 2 * after + o);
+                    else if constexpr (o == nb)
+                        fa[i - 1] = a.read(xan, i - 1);
+                    else if constexpr (q < 0)
+                        fa[after] = a.read(xan, after);
                     else
-                        fa[after] = a.read(na, after);
+                        window(std::integral_constant<int, after>{}, std::integral_constant<int, q>{}, buf, (kt + 3) * C::BK);
                 });
             }
         });
@@ -597,7 +599,8 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     // into LDS alone, and the rest is code once. (All of it unrolled is more than the
     // instruction cache holds, 2.3 ms for a product that takes 0.2; eight rows at a time one
     // after the other, with a wait for each, took 37 us a tile of 256 x 256.)
-    __syncthreads();   // the ring is read no more
+    __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));   // (the zeros past the last stage are on their way into the ring)
+    __syncthreads();                           // nobody reads the ring any more
     float *turn = reinterpret_cast<float *>(lds_bytes) + wave * 64 * PITCH;
     const int rl = lane >> 3, cl = (lane & 7) * 8;
     const void *more = OP == L16_FWD ? p.R : p.beta != 0.0f ? p.C : nullptr;
