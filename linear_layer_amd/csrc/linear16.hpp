@@ -172,7 +172,28 @@ __device__ __forceinline__ int find_chunk(const Groups &gr, int M, int step, int
 constexpr float kGeluA = 0.7978845608028654f;     // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + __expf(-v)); }
+// 1 / (1 + exp(-v)). The reciprocal and the exponential are the hardware's (one unit in the
+// last place): a full division takes ten instructions, and a tile's write-back has a wave to itself.
+__device__ __forceinline__ float sigmoid(float v)
+{
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+}
+
+// The normal distribution function at z, and e = exp(-z^2 / 2). For x = |z| / sqrt(2) and t = 1 /
+// (1 + p x), erfc(x) is a polynomial of t times exp(-x^2) to 1.5e-7 (Abramowitz and Stegun, Handbook
+// of Mathematical Functions, 7.1.26), which has no cancellation on the negative side.
+__device__ __forceinline__ float normal_cdf(float z, float &e)
+{
+    const float x = __builtin_fabsf(z) * 0.70710678118654752f;
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3275911f, x, 1.0f));
+    float q = __builtin_fmaf(1.061405429f, t, -1.453152027f);
+    q = __builtin_fmaf(q, t, 1.421413741f);
+    q = __builtin_fmaf(q, t, -0.284496736f);
+    q = __builtin_fmaf(q, t, 0.254829592f);
+    e = __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
+    const float h = 0.5f * q * t * e;
+    return z > 0.0f ? 1.0f - h : h;
+}
 
 // z times a factor that goes to 0 as z goes to minus infinity.
 __device__ __forceinline__ float damped(float z, float f) { return f == 0.0f ? 0.0f : z * f; }
@@ -180,9 +201,10 @@ __device__ __forceinline__ float damped(float z, float f) { return f == 0.0f ? 0
 // act(z). The tanh form of GELU is z * sigmoid(2 u): 0.5 * (1 + tanh(u)) is that.
 __device__ __forceinline__ float activate(float z, int act)
 {
+    float e;
     switch (act) {
     case LL_ACT_RELU: return z > 0.0f ? z : 0.0f;
-    case LL_ACT_GELU: return damped(z, 0.5f * (1.0f + erff(z * 0.70710678118654752f)));
+    case LL_ACT_GELU: return damped(z, normal_cdf(z, e));
     case LL_ACT_GELU_TANH: return damped(z, sigmoid(2.0f * kGeluA * (z + kGeluB * z * z * z)));
     case LL_ACT_SILU: return damped(z, sigmoid(z));
     default: return z;
@@ -213,8 +235,11 @@ __device__ __forceinline__ float activation_slope(float z, int act)
     z = z > 110.0f ? 110.0f : z < -110.0f ? -110.0f : z;
     switch (act) {
     case LL_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case LL_ACT_GELU:
-        return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) + z * 0.3989422804014327f * __expf(-0.5f * z * z);
+    case LL_ACT_GELU: {
+        float e;
+        const float c = normal_cdf(z, e);
+        return __builtin_fmaf(z * 0.3989422804014327f, e, c);
+    }
     case LL_ACT_GELU_TANH: {
         const float s = sigmoid(2.0f * kGeluA * (z + kGeluB * z * z * z));
         return s + z * s * (1.0f - s) * 2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z);

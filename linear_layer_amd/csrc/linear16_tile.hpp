@@ -606,7 +606,6 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     const void *more = OP == L16_FWD ? p.R : p.beta != 0.0f ? p.C : nullptr;
     const int64_t more_ld = OP == L16_FWD ? p.ldr : p.ldc;
     constexpr int QN = C::WTN / 64, QUARTERS = C::WTM / 64 * QN;
-    const bool inside = m0 + BM <= m_end && n0 + BM <= p.N;
 #pragma unroll 1
     for (int quarter = 0; quarter < QUARTERS; ++quarter) {
         static_for<QUARTERS>([&](auto qq) __attribute__((always_inline)) {
@@ -665,14 +664,18 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
                 }
             }
         };
-        if (inside) {
+        // 32 rows at a time where all of them and the 64 columns exist, else eight
+        const int first = m0 + wm * C::WTM + 64 * (quarter / QN);   // of the 64
+        const bool whole_cols = n0 + wn * C::WTN + 64 * (quarter % QN) + 64 <= p.N;
 #pragma unroll 1
-            for (int q = 0; q < 8; q += 4)
+        for (int q = 0; q < 8 && first + 8 * q < m_end;) {
+            if (whole_cols && first + 8 * q + 32 <= m_end) {
                 rows(std::true_type{}, std::integral_constant<int, 4>{}, q);
-        } else {
-#pragma unroll 1
-            for (int q = 0; q < 8; ++q)
+                q += 4;
+            } else {
                 rows(std::false_type{}, std::integral_constant<int, 1>{}, q);
+                ++q;
+            }
         }
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
