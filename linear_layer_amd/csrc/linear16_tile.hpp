@@ -347,9 +347,11 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
 {
     using C = Cfg<BM>;
     constexpr int PITCH = 64 + 4;   // floats of a row of the write-back's LDS (64 rows a wave)
-    constexpr int TURN_BYTES = C::NW * 64 * PITCH * 4, RING_BYTES = 4 * C::STAGE * 2;
+    constexpr int NB = Operand<BF16, BM, SB, VEC>::DMA ? 3 : 2;   // buffers of B's stages
+    constexpr int TURN_BYTES = C::NW * 64 * PITCH * 4, RING_BYTES = (2 + NB) * C::STAGE * 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds_bytes[TURN_BYTES > RING_BYTES ? TURN_BYTES : RING_BYTES];
-    uint16_t (*ring)[2][C::STAGE] = reinterpret_cast<uint16_t (*)[2][C::STAGE]>(lds_bytes);   // [operand][buffer]
+    uint16_t (*ring_a)[C::STAGE] = reinterpret_cast<uint16_t (*)[C::STAGE]>(lds_bytes);
+    uint16_t (*ring_b)[C::STAGE] = ring_a + 2;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / C::WGN, wn = wave % C::WGN;
@@ -412,28 +414,31 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
 
     a.start(tid);
     b.start(tid);
-    const uint32_t base_a = lds_addr(&ring[0][0][0]), base_b = lds_addr(&ring[1][0][0]);
+    const uint32_t base_a = lds_addr(ring_a), base_b = lds_addr(ring_b);
     constexpr uint32_t STAGE_BYTES = C::STAGE * 2;
     uint32_t at_a = base_a + a.lane_addr(wm * C::WTM, lane), at_b = base_b + b.lane_addr(wn * C::WTN, lane);
     // Step s of the stage in buffer buf: where its operands are read. (Opaque to the compiler, so
     // that the blocks are at constant offsets from it and nothing about it is kept in registers
     // over the loop.)
-    auto step = [&](int buf, int s, uint32_t &xa, uint32_t &xb) __attribute__((always_inline)) {
-        xa = a.step_addr(at_a + buf * STAGE_BYTES, s);
-        xb = b.step_addr(at_b + buf * STAGE_BYTES, s);
+    auto step = [&](int bufa, int bufb, int s, uint32_t &xa, uint32_t &xb) __attribute__((always_inline)) {
+        xa = a.step_addr(at_a + bufa * STAGE_BYTES, s);
+        xb = b.step_addr(at_b + bufb * STAGE_BYTES, s);
         asm volatile("" : "+v"(xa), "+v"(xb));
     };
     static_assert(C::FM == C::FN, "a block of each operand a row of products");
-    // Stages go through two buffers, two steps a stage. While a step multiplies, the next step's
-    // operands are read: its blocks of B into a second set of registers, in the first rows, as
-    // the next step's first row needs all of them; a block of A into the registers that a
-    // row of products has done with (the last one at the step's own start). The barrier
-    // stands after the first rows of a stage's last step, when every operand of the stage is in
-    // registers: it publishes the next stage and frees this one's buffer, which takes the stage
-    // after next: copies in the first half of the rows up to the next barrier, so that they have
-    // the other half to land in; pieces through registers in any of them, each followed by the
-    // load of its successor (those of COLS8, which are fewer, in the first half too: a wait for
-    // copies is one for them). Past the range's end come zeros, and are not used.
+    // A stage is two steps. While a step multiplies, the next step's operands are read: its
+    // blocks of B into a second set of registers, in the first rows, as the next step's first
+    // row needs all of them; a block of A into the registers that a row of products has done
+    // with (the last one at the step's own start). The barrier stands after the first rows of
+    // a stage's last step, when every operand of the stage is in registers: it publishes the
+    // next stage and frees this one's buffers. Then come the copies, in the first half of the
+    // rows up to the next barrier: A's of the stage after next into one of two buffers, which
+    // have the rest of that time to land in, and B's (weights, mostly, and from memory) of the
+    // stage after that into one of three, which fill the LDS and have a whole stage more.
+    // (With two for both, operands that no cache holds: 2048 x 11008 x 4096 226 us.)
+    // Pieces through registers go in any row, each followed by the load of its successor (those
+    // of COLS8, which are fewer, in the first half too: a wait for copies is one for them).
+    // Past the range's end come zeros, and are not used.
     //
     // A wave issues an instruction every four cycles and an MFMA occupies the matrix core for
     // sixteen, so what stands between two MFMAs costs nothing up to three instructions; one
@@ -447,37 +452,38 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     static_assert(C::FM == C::FN && C::PIECES == F, "a piece of each operand in two rows");
     // The operations of row w after a barrier, A's and then B's.
     struct Window {
-        static constexpr int a(int w) { return OpA::DMA ? w < F : w % 2 == 0 ? 2 : 0; }
+        static constexpr int a(int w) { return OpA::DMA ? (w < F / 2 ? 2 : 0) : w % 2 == 0 ? 2 : 0; }
         static constexpr int b(int w)
         {
-            return OpB::DMA ? w < F : w % 2 == 0 || (OpB::PIECES < F && w >= F) ? 0 : 2;
+            return OpB::DMA ? (w >= F / 2 && w < F ? 2 : 0) : w % 2 == 0 || (OpB::PIECES < F && w >= F) ? 0 : 2;
         }
         static constexpr int n(int w) { return a(w) + b(w); }
     };
-    // Operation o of them: into buffer buf; the stage that registers are loaded with begins at k0.
-    auto window = [&](auto ww, auto oo, int buf, int k0) __attribute__((always_inline)) {
+    // Operation o of them: into buffers bufa and bufb; the stage that registers are loaded with
+    // begins at k0.
+    auto window = [&](auto ww, auto oo, int bufa, int bufb, int k0) __attribute__((always_inline)) {
         constexpr int w = decltype(ww)::value, o = decltype(oo)::value, q = o - Window::a(w);
         if constexpr (q < 0) {
             if constexpr (OpA::DMA)
-                a.template copy<w>(base_a + buf * STAGE_BYTES, wave);
+                a.template copy<2 * w + o>(base_a + bufa * STAGE_BYTES, wave);
             else if constexpr (o == 0)
-                a.template store<w / 2>(ring[0][buf], tid);
+                a.template store<w / 2>(ring_a[bufa], tid);
             else
                 a.template load<w / 2>(k0, tid);
         } else {
             if constexpr (OpB::DMA)
-                b.template copy<w>(base_b + buf * STAGE_BYTES, wave);
+                b.template copy<2 * w - F + q>(base_b + bufb * STAGE_BYTES, wave);
             else if constexpr (q == 0)
-                b.template store<w / 2>(ring[1][buf], tid);
+                b.template store<w / 2>(ring_b[bufb], tid);
             else
                 b.template load<w / 2>(k0, tid);
         }
     };
     // All of rows first .. first + count - 1's, at once.
-    auto windows = [&](auto first, auto count, int buf, int k0) __attribute__((always_inline)) {
+    auto windows = [&](auto first, auto count, int bufa, int bufb, int k0) __attribute__((always_inline)) {
         static_for<decltype(count)::value>([&](auto i) __attribute__((always_inline)) {
             constexpr int w = decltype(first)::value + decltype(i)::value;
-            static_for<Window::n(w)>([&](auto o) __attribute__((always_inline)) { window(std::integral_constant<int, w>{}, o, buf, k0); });
+            static_for<Window::n(w)>([&](auto o) __attribute__((always_inline)) { window(std::integral_constant<int, w>{}, o, bufa, bufb, k0); });
         });
     };
     const int nk = cdiv(klen, C::BK);
@@ -485,21 +491,27 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         static_for<OpA::PIECES>([&](auto j) __attribute__((always_inline)) { a.template load<decltype(j)::value>(0, tid); });
     if constexpr (!OpB::DMA)
         static_for<OpB::PIECES>([&](auto j) __attribute__((always_inline)) { b.template load<decltype(j)::value>(0, tid); });
+    // stage 0, and what the rows after a barrier before it would have begun: copies in the order of
+    // their need
     a.aim(0, tid);
     b.aim(0, tid);
-    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, ROWS2>{}, 0, C::BK);
+    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, ROWS2>{}, 0, 0, C::BK);
     a.aim(C::BK, tid);
     b.aim(C::BK, tid);
-    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, AFTER>{}, 1, 2 * C::BK);
+    if constexpr (OpB::DMA) {
+        static_for<F>([&](auto j) __attribute__((always_inline)) { b.template copy<decltype(j)::value>(base_b + STAGE_BYTES, wave); });
+        b.aim(2 * C::BK, tid);
+    }
+    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, AFTER>{}, 1, NB - 1, 2 * C::BK);
     if constexpr (OpA::DMA && OpB::DMA)
-        __builtin_amdgcn_s_waitcnt(LL_VMCNT(2 * AFTER));   // (stage 1's copies may still be on their way)
+        __builtin_amdgcn_s_waitcnt(LL_VMCNT(2 * F + 2 * (AFTER - F / 2)));   // (those of the stages after the first)
     else if constexpr (OpA::DMA || OpB::DMA)
         __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     f16x8 fa[F], fb[2][F];
     {
         uint32_t xa, xb;
-        step(0, 0, xa, xb);
+        step(0, 0, 0, xa, xb);
 #pragma unroll
         for (int i = 0; i < F; ++i) {
             if (i + 1 < F)
@@ -526,11 +538,12 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     };
     if constexpr (C::WPE == 1)
         settle();
+    int bufb = 0, nextb = 1, lastb = NB - 1;   // B's buffers of stages kt, kt + 1, and kt + 2 (kt + 1 where there are two)
     for (int kt = 0; kt < nk; ++kt) {
         const int buf = kt & 1;
         uint32_t xa0, xa1, xb1, unused;
-        step(buf, 0, xa0, unused);
-        step(buf, 1, xa1, xb1);
+        step(buf, bufb, 0, xa0, unused);
+        step(buf, bufb, 1, xa1, xb1);
         __builtin_amdgcn_s_setprio(1);
         static_for<F>([&](auto ii) __attribute__((always_inline)) {
             // two blocks of B in the first rows, and one of A; the last rows have the operations
@@ -547,9 +560,9 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
                     else
                         fa[i - 1] = a.read(xa1, i - 1);
                 } else if constexpr (q < n) {
-                    window(std::integral_constant<int, w>{}, std::integral_constant<int, q>{}, buf ^ 1, (kt + 2) * C::BK);
+                    window(std::integral_constant<int, w>{}, std::integral_constant<int, q>{}, buf ^ 1, lastb, (kt + 2) * C::BK);
                 } else {
-                    window(std::integral_constant<int, w2>{}, std::integral_constant<int, q - n>{}, buf ^ 1, (kt + 2) * C::BK);
+                    window(std::integral_constant<int, w2>{}, std::integral_constant<int, q - n>{}, buf ^ 1, lastb, (kt + 2) * C::BK);
                 }
             });
         });
@@ -557,8 +570,11 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         static_for<F>([&](auto ii) __attribute__((always_inline)) {
             constexpr int i = decltype(ii)::value, after = i - BR;   // rows since the barrier
             if constexpr (after == 0) {
-                if constexpr (OpA::DMA || OpB::DMA)
-                    __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));   // stage kt + 1 has landed
+                // stage kt + 1 has landed; B's copies of the one after may be on their way
+                if constexpr (OpA::DMA && OpB::DMA)
+                    __builtin_amdgcn_s_waitcnt(LL_VMCNT(F));
+                else if constexpr (OpA::DMA || OpB::DMA)
+                    __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             }
             if constexpr (after < 0) {
@@ -567,11 +583,11 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
                     if constexpr (i == 0 && o == 0)
                         fa[F - 1] = a.read(xa1, F - 1);
                     else if constexpr (i == 0 && o == 1)
-                        step(buf ^ 1, 0, xan, xbn);
+                        step(buf ^ 1, nextb, 0, xan, xbn);
                     else if constexpr (i == BR - 1 && o == 2)
                         a.aim((kt + 2) * C::BK, tid);
                     else if constexpr (i == BR - 1 && o == 3)
-                        b.aim((kt + 2) * C::BK, tid);
+                        b.aim((kt + NB) * C::BK, tid);
                 });
             } else {
                 // (after the last stage what is read here is of no use)
@@ -585,11 +601,15 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
                     else if constexpr (q < 0)
                         fa[after] = a.read(xan, after);
                     else
-                        window(std::integral_constant<int, after>{}, std::integral_constant<int, q>{}, buf, (kt + 3) * C::BK);
+                        window(std::integral_constant<int, after>{}, std::integral_constant<int, q>{}, buf, bufb, (kt + 3) * C::BK);
                 });
             }
         });
         __builtin_amdgcn_s_setprio(0);
+        const int done = bufb;
+        bufb = nextb;
+        nextb = NB == 3 ? lastb : done;
+        lastb = NB == 3 ? done : nextb;
     }
     if constexpr (C::WPE == 1)
         settle();
