@@ -20,7 +20,7 @@ OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "gemm_f32.hip", "gemm_f32_nt.hip", "gemm_f16.hip", "elementwise.hip",
            "api_mx4.hip", "mx4.hip", "gemm_mx4.hip", "gemm_mx4_tile.hip", "api_norm.hip", "rmsnorm.hip",
-           "api_linear16.hip", "linear16_fwd.hip", "linear16_dx.hip", "linear16_dw.hip", "mx8.hip"]
+           "api_linear16.hip", "linear16_fwd.hip", "linear16_rows.hip", "linear16_dx.hip", "linear16_dw.hip", "mx8.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

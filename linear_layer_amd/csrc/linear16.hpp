@@ -50,6 +50,7 @@ enum L16Op : int { L16_FWD = 0, L16_DX = 1, L16_DW = 2 };
 
 // `vec`: every row of 16-bit operands in whole 16-byte pieces, on 16 bytes.
 hipError_t launch_l16_fwd(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
+hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, hipStream_t s);   // of L16_FWD, few rows a group
 hipError_t launch_l16_dx(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 
@@ -199,56 +200,56 @@ __device__ __forceinline__ float normal_cdf(float z, float &e)
 __device__ __forceinline__ float damped(float z, float f) { return f == 0.0f ? 0.0f : z * f; }
 
 // act(z). The tanh form of GELU is z * sigmoid(2 u): 0.5 * (1 + tanh(u)) is that.
-__device__ __forceinline__ float activate(float z, int act)
+template <int ACT>
+__device__ __forceinline__ float activate(float z)
 {
-    float e;
-    switch (act) {
-    case LL_ACT_RELU: return z > 0.0f ? z : 0.0f;
-    case LL_ACT_GELU: return damped(z, normal_cdf(z, e));
-    case LL_ACT_GELU_TANH: return damped(z, sigmoid(2.0f * kGeluA * (z + kGeluB * z * z * z)));
-    case LL_ACT_SILU: return damped(z, sigmoid(z));
-    default: return z;
+    if constexpr (ACT == LL_ACT_RELU) {
+        return z > 0.0f ? z : 0.0f;
+    } else if constexpr (ACT == LL_ACT_GELU) {
+        float e;
+        return damped(z, normal_cdf(z, e));
+    } else if constexpr (ACT == LL_ACT_GELU_TANH) {
+        return damped(z, sigmoid(2.0f * kGeluA * __builtin_fmaf(kGeluB * z * z, z, z)));
+    } else if constexpr (ACT == LL_ACT_SILU) {
+        return damped(z, sigmoid(z));
+    } else {
+        return z;
     }
 }
 
-// act of eight values: one test of the kind for all.
-__device__ __forceinline__ void activate8(float (&v)[8], int act)
+// act'(z). Past +-110 every slope here is 0 or 1 in FP32 to the last bit; as a factor z is held
+// there, so that no product of an infinity and a zero comes up (NaN stays NaN through the other).
+template <int ACT>
+__device__ __forceinline__ float activation_slope(float z)
 {
-    auto each = [&](auto kind) __attribute__((always_inline)) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = activate(v[e], decltype(kind)::value);
-    };
-    switch (act) {
-    case LL_ACT_RELU: each(std::integral_constant<int, LL_ACT_RELU>{}); break;
-    case LL_ACT_GELU: each(std::integral_constant<int, LL_ACT_GELU>{}); break;
-    case LL_ACT_GELU_TANH: each(std::integral_constant<int, LL_ACT_GELU_TANH>{}); break;
-    case LL_ACT_SILU: each(std::integral_constant<int, LL_ACT_SILU>{}); break;
-    default: break;
-    }
-}
-
-// act'(z). Past +-110 every slope here is 0 or 1 in FP32 to the last bit; z is held there so
-// that no product of an infinity and a zero comes up (NaN stays NaN).
-__device__ __forceinline__ float activation_slope(float z, int act)
-{
-    z = z > 110.0f ? 110.0f : z < -110.0f ? -110.0f : z;
-    switch (act) {
-    case LL_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case LL_ACT_GELU: {
+    const float f = __builtin_amdgcn_fmed3f(z, -110.0f, 110.0f);
+    if constexpr (ACT == LL_ACT_RELU) {
+        return z > 0.0f ? 1.0f : 0.0f;
+    } else if constexpr (ACT == LL_ACT_GELU) {
         float e;
         const float c = normal_cdf(z, e);
-        return __builtin_fmaf(z * 0.3989422804014327f, e, c);
-    }
-    case LL_ACT_GELU_TANH: {
-        const float s = sigmoid(2.0f * kGeluA * (z + kGeluB * z * z * z));
-        return s + z * s * (1.0f - s) * 2.0f * kGeluA * (1.0f + 3.0f * kGeluB * z * z);
-    }
-    case LL_ACT_SILU: {
+        return __builtin_fmaf(f * 0.3989422804014327f, e, c);
+    } else if constexpr (ACT == LL_ACT_GELU_TANH) {
+        const float s = sigmoid(2.0f * kGeluA * __builtin_fmaf(kGeluB * z * z, z, z));
+        return __builtin_fmaf(f * s * (1.0f - s), 2.0f * kGeluA * __builtin_fmaf(3.0f * kGeluB * f, f, 1.0f), s);
+    } else if constexpr (ACT == LL_ACT_SILU) {
         const float s = sigmoid(z);
-        return s + z * s * (1.0f - s);
+        return __builtin_fmaf(f * s, 1.0f - s, s);
+    } else {
+        return 1.0f;
     }
-    default: return 1.0f;
+}
+
+// f(std::integral_constant<int, act>): one test of the kind for all that f does with it.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f)
+{
+    switch (act) {
+    case LL_ACT_RELU: f(std::integral_constant<int, LL_ACT_RELU>{}); break;
+    case LL_ACT_GELU: f(std::integral_constant<int, LL_ACT_GELU>{}); break;
+    case LL_ACT_GELU_TANH: f(std::integral_constant<int, LL_ACT_GELU_TANH>{}); break;
+    case LL_ACT_SILU: f(std::integral_constant<int, LL_ACT_SILU>{}); break;
+    default: f(std::integral_constant<int, LL_ACT_NONE>{}); break;
     }
 }
 

@@ -1,0 +1,92 @@
+// What the kernels of the 16-bit layer's products share: the matrix instruction, and the
+// write-back of eight sums.
+#pragma once
+
+#include "linear16.hpp"
+
+namespace ll {
+namespace l16 {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+template <bool BF16> constexpr int kType16 = BF16 ? LL_TYPE_BF16 : LL_TYPE_F16;
+
+template <bool BF16>
+__device__ __forceinline__ f32x4 mma(const f16x8 &a, const f16x8 &b, const f32x4 &c)
+{
+    if constexpr (BF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                       0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// Eight values of a matrix of LL_TYPE_F32 or the 16-bit type, the first n of them inside it.
+template <bool BF16>
+__device__ __forceinline__ void load8(int type, const void *base, int64_t at, int64_t n, float (&v)[8])
+{
+    if (type == LL_TYPE_F32)
+        load_row<LL_TYPE_F32, 8>(static_cast<const float *>(base) + at, n, v);
+    else
+        load_row<kType16<BF16>, 8>(static_cast<const uint16_t *>(base) + at, n, v);
+}
+template <bool BF16>
+__device__ __forceinline__ void store8(int type, void *base, int64_t at, int64_t n, const float (&v)[8])
+{
+    if (type == LL_TYPE_F32)
+        store_row<LL_TYPE_F32, 8>(static_cast<float *>(base) + at, n, v);
+    else
+        store_row<kType16<BF16>, 8>(static_cast<uint16_t *>(base) + at, n, v);
+}
+
+// Eight sums of row `row`, columns col .. col + 7, to the forward product's outputs. n of
+// them are inside (8 or more: all); r: what is added after the activation. Lanes without a row
+// (live false) take part in the blocks' maxima of their neighbours' row only.
+template <bool BF16>
+__device__ __forceinline__ void finish_fwd(const L16Params &p, float (&v)[8], const float (&bias)[8], const float (&r)[8],
+                                           int64_t row, int col, int n, bool live)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] += bias[e];
+    if (p.ZQ != nullptr) {
+        // blocks of 32: four neighbouring lanes, which are of one row
+        uint32_t top = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            top = max(top, e < n ? __builtin_bit_cast(uint32_t, v[e]) & 0x7fffffffu : 0u);
+        const uint32_t s = mx8_scale(max_of_quad(top));
+        if (live) {
+            const uint32_t lo = mx8_encode4(v[0], v[1], v[2], v[3], s), hi = mx8_encode4(v[4], v[5], v[6], v[7], s);
+            const uint64_t q = (uint64_t)hi << 32 | lo;
+            uint8_t *dst = p.ZQ + row * p.ldzq + col;
+            if (n >= 8) {
+                __builtin_memcpy(dst, &q, 8);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < n)
+                        dst[e] = (uint8_t)(q >> (8 * e));
+            }
+            if ((col & 31) == 0)
+                p.ZS[row * p.ldzs + (col >> 5)] = (uint8_t)s;
+        }
+    }
+    if (!live)
+        return;
+    if (p.Z != nullptr)
+        store_row<kType16<BF16>, 8>(p.Z + row * p.ldz + col, n, v);
+    with_activation(p.act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = activate<decltype(kind)::value>(v[e]);
+    });
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] += r[e];
+    store8<BF16>(p.ctype, p.C, row * p.ldc + col, n, v);
+}
+
+}  // namespace l16
+}  // namespace ll

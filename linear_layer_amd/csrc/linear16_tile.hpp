@@ -30,25 +30,12 @@
 #include <utility>
 
 #include "launch.hpp"
-#include "linear16.hpp"
+#include "linear16_finish.hpp"
 
 namespace ll {
 namespace l16 {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-
 enum Side : int { ROWS = 0, COLS = 1, COLS8 = 2 };
-
-template <bool BF16>
-__device__ __forceinline__ f32x4 mma(const f16x8 &a, const f16x8 &b, const f32x4 &c)
-{
-    if constexpr (BF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
-                                                       0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
 
 // c += a * b with c in accumulation registers. One wave a SIMD has 256 of them beside its 256
 // vector registers; left to the compiler, sums wander between the two (500 moves a stage).
@@ -65,8 +52,6 @@ __device__ __forceinline__ void mma_acc(const f16x8 &a, const f16x8 &b, f32x4 &c
 // The wait between mma_acc and what else reads its sums (18 wait states at most), and between what
 // wrote them and the first mma_acc.
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
-
-template <bool BF16> constexpr int kType16 = BF16 ? LL_TYPE_BF16 : LL_TYPE_F16;
 
 // Waves, and the block of C that each has: 256 x 256 as 2 x 2 waves of 128 x 128 (one a
 // SIMD), 128 x 128 as 2 x 2 of 64 x 64 (two workgroups a CU).
@@ -268,68 +253,6 @@ struct Operand {
         }
     }
 };
-
-// Eight values of a matrix of LL_TYPE_F32 or the 16-bit type, the first n of them inside it.
-template <bool BF16>
-__device__ __forceinline__ void load8(int type, const void *base, int64_t at, int64_t n, float (&v)[8])
-{
-    if (type == LL_TYPE_F32)
-        load_row<LL_TYPE_F32, 8>(static_cast<const float *>(base) + at, n, v);
-    else
-        load_row<kType16<BF16>, 8>(static_cast<const uint16_t *>(base) + at, n, v);
-}
-template <bool BF16>
-__device__ __forceinline__ void store8(int type, void *base, int64_t at, int64_t n, const float (&v)[8])
-{
-    if (type == LL_TYPE_F32)
-        store_row<LL_TYPE_F32, 8>(static_cast<float *>(base) + at, n, v);
-    else
-        store_row<kType16<BF16>, 8>(static_cast<uint16_t *>(base) + at, n, v);
-}
-
-// Eight sums of row `row`, columns col .. col + 7, to the forward product's outputs. n of
-// them are inside (8 or more: all); r: what is added after the activation. Lanes without a row
-// (live false) take part in the blocks' maxima of their neighbours' row only.
-template <bool BF16>
-__device__ __forceinline__ void finish_fwd(const L16Params &p, float (&v)[8], const float (&bias)[8], const float (&r)[8],
-                                           int64_t row, int col, int n, bool live)
-{
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] += bias[e];
-    if (p.ZQ != nullptr) {
-        // blocks of 32: four neighbouring lanes, which are of one row
-        uint32_t top = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            top = max(top, e < n ? __builtin_bit_cast(uint32_t, v[e]) & 0x7fffffffu : 0u);
-        const uint32_t s = mx8_scale(max_of_quad(top));
-        if (live) {
-            const uint32_t lo = mx8_encode4(v[0], v[1], v[2], v[3], s), hi = mx8_encode4(v[4], v[5], v[6], v[7], s);
-            const uint64_t q = (uint64_t)hi << 32 | lo;
-            uint8_t *dst = p.ZQ + row * p.ldzq + col;
-            if (n >= 8) {
-                __builtin_memcpy(dst, &q, 8);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (e < n)
-                        dst[e] = (uint8_t)(q >> (8 * e));
-            }
-            if ((col & 31) == 0)
-                p.ZS[row * p.ldzs + (col >> 5)] = (uint8_t)s;
-        }
-    }
-    if (!live)
-        return;
-    if (p.Z != nullptr)
-        store_row<kType16<BF16>, 8>(p.Z + row * p.ldz + col, n, v);
-    activate8(v, p.act);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        v[e] += r[e];
-    store8<BF16>(p.ctype, p.C, row * p.ldc + col, n, v);
-}
 
 // Tile `id` of tiles_m x tiles_n in groups of four rows of tiles, column by column, so that
 // the tiles an XCD has at a time share their operands in its L2.

@@ -207,20 +207,26 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradParams p, int step
                 scale[i] = live > 0 ? p.ZS[m * p.ldzs + col / kMxBlock] : 0;
             }
         }
+        if constexpr (ZF == Z_8) {
+#pragma unroll
+            for (int i = 0; i < kActRows; ++i) {
+                mx8_decode4((uint32_t)codes[i], scale[i], z[i]);
+                mx8_decode4((uint32_t)(codes[i] >> 32), scale[i], z[i] + 4);
+            }
+        }
+        if constexpr (ZF != Z_NONE)
+            with_activation(p.act, [&](auto kind) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < kActRows; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dy[i][e] *= activation_slope<decltype(kind)::value>(z[i][e]);
+            });
 #pragma unroll
         for (int i = 0; i < kActRows; ++i) {
             const int64_t m = r + i * rows;
             if (m >= r1 || n <= 0)
                 continue;
-            if constexpr (ZF == Z_8) {
-                mx8_decode4((uint32_t)codes[i], scale[i], z[i]);
-                mx8_decode4((uint32_t)(codes[i] >> 32), scale[i], z[i] + 4);
-            }
-            if constexpr (ZF != Z_NONE) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    dy[i][e] *= activation_slope(z[i][e], p.act);
-            }
             if (p.DZ != nullptr)
                 store_row<T, 8>(p.DZ + m * p.lddz + col, n, dy[i]);
 #pragma unroll
