@@ -481,6 +481,11 @@ int mx8_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
  *   Z       M-by-N of `type`, or NULL: Z as the way back needs it, and / or
  *   ZQ, ZS  the same in MX8 (M-by-N codes, M-by-ceil(N/32) scales), from its
  *           FP32 sums; both or neither.
+ *   workspace   NULL, or at least ll_linear16_workspace_size(M, N, K, groups) bytes
+ *           (on the current device; 0: none helps), 16-byte aligned, overlapping
+ *           nothing; its contents need no preparation. With one, a product of few
+ *           rows and columns shares K out over workgroups. Calls that share one
+ *           must not overlap in time.
  * Outputs must not overlap inputs or each other otherwise. K == 0: Z = bias.
  *
  * linear16_grad_act — dZ = dY * act'(Z), and dbias[g] = the sums of dZ (before its
@@ -510,7 +515,8 @@ int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx,
                 const uint16_t *W, int ldw, int64_t stride_w, const float *bias, int act,
                 int ytype, const void *R, int ldr, void *Y, int ldy,
                 uint16_t *Z, int ldz, uint8_t *ZQ, int ldzq, uint8_t *ZS, int ldzs,
-                void *stream);
+                void *workspace, int64_t workspace_bytes, void *stream);
+int64_t ll_linear16_workspace_size(int M, int N, int K, int groups);
 int64_t ll_linear16_grad_act_workspace_size(int M, int N, int groups);
 int linear16_grad_act(int M, int N, int type, int act, int ytype, const void *DY, int lddy,
                       int groups, const int32_t *offsets,

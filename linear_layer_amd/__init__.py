@@ -67,7 +67,7 @@ __all__ = [
     "mx4_chosen_kernel", "A_MX4", "A_F16", "A_BF16", "rmsnorm_residual", "rmsnorm_residual_grad", "rmsnorm_grad_workspace_size",
     "TYPE_F32", "TYPE_F16", "TYPE_BF16",
     "mx8_quantize", "mx8_dequantize", "mx8_shapes", "linear16_nt", "linear16_grad_act", "linear16_grad_input",
-    "linear16_grad_weight", "linear16_grad_act_workspace_size", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "MAX_GROUPS",
+    "linear16_grad_weight", "linear16_grad_act_workspace_size", "linear16_workspace_size", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "MAX_GROUPS",
     "library_path", "load", "set_tile", "num_tiles", "tile_name", "chosen_tile",
     "set_split_k", "chosen_split_k", "set_stream_k", "chosen_stream_k",
     "ACT_NONE", "ACT_RELU", "DTYPE_F32", "DTYPE_F16", "PLAN_RELU", "PLAN_B_NK", "PLAN_UNALIGNED",
@@ -105,7 +105,7 @@ EXPORTED = ("gemm_f32", "gemm_f16f32", "gemm_bf16f32", "linear_bias_act", "ll_st
             "ll_mx4_chosen_kernel",
             "rmsnorm_residual", "rmsnorm_residual_grad", "ll_rmsnorm_grad_workspace_size",
             "mx8_quantize", "mx8_dequantize", "linear16_nt", "linear16_grad_act", "linear16_grad_input",
-            "linear16_grad_weight", "ll_linear16_grad_act_workspace_size")
+            "linear16_grad_weight", "ll_linear16_grad_act_workspace_size", "ll_linear16_workspace_size")
 
 
 class LinearLayerError(RuntimeError):
@@ -170,7 +170,9 @@ def load():
     lib.mx8_quantize.argtypes = [i32, i32, i32, vp, i32, vp, i32, vp, i32, vp]
     lib.mx8_dequantize.argtypes = [i32, i32, vp, i32, vp, i32, i32, vp, i32, vp]
     lib.linear16_nt.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, i64, vp, i32, i32, vp, i32, vp, i32,
-                                vp, i32, vp, i32, vp, i32, vp]
+                                vp, i32, vp, i32, vp, i32, vp, i64, vp]
+    lib.ll_linear16_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.ll_linear16_workspace_size.restype = i64
     lib.linear16_grad_act.argtypes = [i32, i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, i32, vp, i32, vp,
                                       vp, i64, vp]
     lib.linear16_grad_input.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, i64, i32, vp, i32, vp]
@@ -863,13 +865,32 @@ def _held(v, dtype, M, N, name):
     return (p, ld, None, one, None, one), (v,)
 
 
-def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, stream=None):
+def _workspace(t):
+    """(pointer, bytes) of a workspace tensor."""
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def linear16_workspace_size(M: int, N: int, K: int, groups: int = 1) -> int:
+    """Bytes of workspace that linear16_nt gains from on the current device (0: none)."""
+    if max(M, N, K) > _INT_MAX or groups > MAX_GROUPS:
+        raise ValueError(f"the calls take sizes up to {_INT_MAX} and {MAX_GROUPS} groups")
+    n = load().ll_linear16_workspace_size(int(M), int(N), int(K), int(groups))
+    if n < 0:
+        raise ValueError("negative size")
+    return n
+
+
+def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None, stream=None):
     """Y = act(X*W^T + bias) + R with X (M x K) and W (N x K) in float16 or bfloat16, fp32
     sums, bias fp32 or None, R and Y (M x N) both of X's dtype or both float32; R may be
     None or Y. Z, if given, receives X*W^T + bias: a tensor of X's dtype, or a pair (codes,
     scales) of uint8 tensors (``mx8_shapes``). With ``offsets`` (groups + 1 ascending row
     numbers, int32, on the device) W is groups x N x K, bias groups x N, and rows outside
-    all groups stay as they are. Returns Y."""
+    all groups stay as they are. A product of few rows and columns gains from a workspace of
+    linear16_workspace_size bytes: on the current stream it comes from torch's allocator, with
+    ``stream`` given the call runs without one unless it is given too. Returns Y."""
     t = _type16_of(X, "X")
     px, M, K, ldx = _mat(X, X.dtype, "X")
     groups, poff = _offsets(offsets)
@@ -881,8 +902,14 @@ def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, stream=None):
     pr, ldr = _opt_mat(R, Y.dtype, "R", M, N)
     held, zs = _held(Z, X.dtype, M, N, "Z")
     pb = _group_vec(bias, groups, poff is not None, N, "bias")
+    s = _stream(stream, X, W, Y, R, bias, offsets, workspace, *zs)
+    if workspace is None and stream is None and M <= 64 * groups:   # (longer groups gain from none)
+        need = load().ll_linear16_workspace_size(M, N, K, groups)
+        if need > 0:
+            workspace = _torch().empty(need, dtype=_torch().uint8, device=X.device)
+    pws, nws = (None, 0) if workspace is None else _workspace(workspace)
     _check(load().linear16_nt(M, N, K, t, px, ldx, groups, poff, pw, ldw, stride, pb, int(act), ty, pr, ldr, py, ldy,
-                              *held, _stream(stream, X, W, Y, R, bias, offsets, *zs)), "linear16_nt")
+                              *held, pws, nws, s), "linear16_nt")
     return Y
 
 
@@ -917,9 +944,7 @@ def linear16_grad_act(DY, Z, act: int, DZ, dbias=None, offsets=None, workspace=N
             if stream is not None:
                 raise ValueError("dbias on a stream that is given needs a workspace")
             workspace = torch.empty(linear16_grad_act_workspace_size(M, N, groups), dtype=torch.uint8, device=DZ.device)
-        elif not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous device tensor")
-        pws, nws = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        pws, nws = _workspace(workspace)
     _check(load().linear16_grad_act(M, N, t, int(act), ty, pdy, lddy, groups, poff, *held, pdz, lddz, pb, pws, nws, s),
            "linear16_grad_act")
     return DZ

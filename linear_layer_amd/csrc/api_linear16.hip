@@ -97,11 +97,20 @@ int mx8_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
     return status(launch_mx8_dequantize(type, codes, ldq, scales, lds, Y, ldy, M, K, static_cast<hipStream_t>(stream)));
 }
 
+int64_t ll_linear16_workspace_size(int M, int N, int K, int groups)
+{
+    if (M < 0 || N < 0 || K < 0 || groups < 0 || groups > LL_MAX_GROUPS)
+        return -1;
+    const Device dev = current_device();
+    return l16_workspace(M, N, K, groups, dev.status == LL_OK ? dev.cus : 256);
+}
+
 int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx, int groups, const int32_t *offsets,
                 const uint16_t *W, int ldw, int64_t stride_w, const float *bias, int act, int ytype, const void *R, int ldr,
-                void *Y, int ldy, uint16_t *Z, int ldz, uint8_t *ZQ, int ldzq, uint8_t *ZS, int ldzs, void *stream)
+                void *Y, int ldy, uint16_t *Z, int ldz, uint8_t *ZQ, int ldzq, uint8_t *ZS, int ldzs, void *workspace,
+                int64_t workspace_bytes, void *stream)
 {
-    if (!type16(type) || !out_type(ytype, type) || M < 0 || N < 0 || K < 0 || act < LL_ACT_NONE || act > LL_ACT_SILU ||
+    if (!type16(type) || !out_type(ytype, type) || workspace_bytes < 0 || M < 0 || N < 0 || K < 0 || act < LL_ACT_NONE || act > LL_ACT_SILU ||
         !groups_ok(offsets, groups) || stride_w < 0 || (ZQ == nullptr) != (ZS == nullptr))
         return LL_ERR_INVALID_VALUE;
     const int es = type_bytes(ytype);
@@ -122,10 +131,18 @@ int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx, int g
     const Range rr = r.range(M, N);
     if (any_overlap(out, 4, in, 4) || any_overlap(out, 3, &rr, 1) || (!y.same(r) && overlap(out[3], rr)))
         return LL_ERR_INVALID_VALUE;
+    if (workspace != nullptr && !aligned(workspace, 16))
+        return LL_ERR_INVALID_VALUE;
     const Device dev = current_device();
     if (dev.status != LL_OK)
         return dev.status;
+    const int64_t need = workspace != nullptr ? l16_workspace(M, N, K, groups, dev.cus) : 0;
+    const Range ws = {workspace, need};
+    if (need > 0 && (workspace_bytes < need || any_overlap(&ws, 1, in, 4) || any_overlap(&ws, 1, out, 4) || overlap(ws, rr)))
+        return LL_ERR_INVALID_VALUE;
     L16Params p{};
+    p.ws = static_cast<float *>(workspace);
+    p.shares = need > 0 ? l16_row_shares(M, N, K, groups, dev.cus) : 1;
     p.A = X;
     p.B = W;
     p.C = Y;

@@ -50,7 +50,12 @@ enum L16Op : int { L16_FWD = 0, L16_DX = 1, L16_DW = 2 };
 
 // `vec`: every row of 16-bit operands in whole 16-byte pieces, on 16 bytes.
 hipError_t launch_l16_fwd(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
-hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, hipStream_t s);   // of L16_FWD, few rows a group
+// The forward product of few rows a group (p.shares of K, through p.ws where more than one);
+// how many shares a workspace is worth, and its bytes.
+bool l16_takes_rows(int M, int groups);
+int l16_row_shares(int M, int N, int K, int groups, int cus);
+int64_t l16_workspace(int M, int N, int K, int groups, int cus);
+hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, hipStream_t s);
 hipError_t launch_l16_dx(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 

@@ -1,6 +1,9 @@
-// What the kernels of the 16-bit layer's products share: the matrix instruction, and the
-// write-back of eight sums.
+// What the kernels of the 16-bit layer's products share: the matrix instruction, copies into
+// LDS and the order of 16-byte pieces in it, and the write-back of eight sums.
 #pragma once
+
+#include <type_traits>
+#include <utility>
 
 #include "linear16.hpp"
 
@@ -20,6 +23,39 @@ __device__ __forceinline__ f32x4 mma(const f16x8 &a, const f16x8 &b, const f32x4
                                                        0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// 16-byte chunk c of row `row` of a ROWS stage, and unit u of k-row k of a COLS stage.
+__device__ __forceinline__ int rows_swz(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int cols_swz(int k) { return 2 * (k & 3) + ((k >> 3) & 1); }
+
+template <int... I, class F>
+__device__ __forceinline__ void static_for_(std::integer_sequence<int, I...>, F f)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+// f(0), .., f(N - 1) with constants for arguments.
+template <int N, class F>
+__device__ __forceinline__ void static_for(F f)
+{
+    static_for_(std::make_integer_sequence<int, N>{}, f);
+}
+
+constexpr uint32_t kPastEnd = 0x80000000u;   // past the end of every buffer here: 256 rows of less than 2^21 values
+
+// buffer_load_dwordx4 into LDS: this lane's 16 bytes at byte `off` of the buffer go to LDS
+// byte lds_base + 16 * lane, zeros where they lie past its end. Inline assembly, so that the
+// compiler does not take it for an LDS store that every LDS read must wait for; the caller
+// waits for the copies before the barrier that publishes them. The compiler's hazard checks
+// do not look inside: M0 may be used one wait state after its write. (Four more, for a
+// descriptor that v_readfirstlane might have written just before, would cost the matrix
+// cores as much as all the copies; descriptors here are made by scalar instructions.)
+__device__ __forceinline__ void lds_buffer_16(const u32x4 &buffer, uint32_t off, uint32_t lds_base)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds_base), "v"(off), "s"(buffer)
+                 : "memory", "m0");
 }
 
 // Eight values of a matrix of LL_TYPE_F32 or the 16-bit type, the first n of them inside it.

@@ -1,14 +1,17 @@
 // The 16-bit layer for few rows: every weight is read once for at most 64 rows, so memory bounds
 // the product and the matrix cores have time to spare.
 //
-// A workgroup of NW waves computes MT x 16 rows by NB x 16 columns. Its waves share the inner
-// dimension out in turns of 64 values: wave w takes turns w, w + NW, ... and reads its operands
-// straight into the matrix instruction's registers, 16 bytes a lane (the instruction has four
-// lanes to a row, so a load covers 64 bytes of 16 rows of W and the next one the other half of
-// their lines). W's rows of DEPTH turns are on their way at a time. X's rows come from L2, where
-// the other workgroups' reads have brought them; lanes past the last row read that row again,
-// which costs no traffic. At the end the waves' sums meet in LDS and are added in the waves'
-// order, and the write-back is that of the tile kernel.
+// A workgroup of four waves computes MT x 16 rows by 64 columns, over all of the inner dimension
+// or a share of it. Its waves share that out in turns of 64 values, a whole line of a row: wave
+// w takes turns w, w + 4, ... and copies 64 rows of W and the rows of X straight into a ring of
+// its own in LDS (DEPTH turns, 8 + 2 MT KiB each, in the tile kernel's order), so that no wave
+// waits for another and all of a CU's LDS but the turn in use is on its way from memory. At the end
+// the waves' sums meet in LDS and are added in the waves' order. Shares of K go through the
+// workspace and are added in order by a second launch, where a product has fewer than half as
+// many workgroups as the GPU has CUs.
+//
+// (Loads straight into the matrix instruction's registers, 64 bytes of 16 rows each, reach 3 TB/s
+// where this reaches 5; they are what rows off 16 bytes take.)
 #include "launch.hpp"
 #include "linear16_finish.hpp"
 
@@ -16,16 +19,186 @@ namespace ll {
 
 using namespace l16;
 
-constexpr int kTurn = 64;   // values of the inner dimension a wave takes at a time
+constexpr int kTurn = 64;     // values of the inner dimension a wave takes at a time
+constexpr int kCols = 64;     // columns of a workgroup
+constexpr int kWaves = 4;
+constexpr int kPitch = kCols + 4;
 
-// Eight values of a row from k on; zeros past K. VEC: rows are whole 16-byte pieces.
-template <bool VEC>
+// The waves' sums added, and the write-back or the share's sums. The sums are at part[wave][row][column].
+template <bool BF16, int MT, int THREADS>
+__device__ __forceinline__ void finish_rows(const L16Params &p, const float *part, const Chunk &c, int m0, int n0, int share)
+{
+    for (int s = threadIdx.x; s < MT * 16 * 8; s += THREADS) {
+        const int rl = s / 8, cl = s % 8 * 8, row = m0 + rl, col = n0 + cl, n = p.N - col;
+        const bool live = row < c.end && n > 0;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWaves; ++k) {
+            const f32x4 lo = *reinterpret_cast<const f32x4 *>(&part[(k * MT * 16 + rl) * kPitch + cl]);
+            const f32x4 hi = *reinterpret_cast<const f32x4 *>(&part[(k * MT * 16 + rl) * kPitch + cl + 4]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] += lo[e], v[4 + e] += hi[e];
+        }
+        if (p.shares > 1) {
+            if (live)
+                store_row<LL_TYPE_F32, 8>(p.ws + ((int64_t)share * p.M + row) * p.N + col, n, v);
+            continue;
+        }
+        float bias[8], r[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            r[e] = 0.0f;
+        load_row<LL_TYPE_F32, 8>(p.bias + (int64_t)c.group * p.N + col, p.bias != nullptr ? n : 0, bias);
+        if (p.R != nullptr)
+            load8<BF16>(p.ctype, p.R, (int64_t)row * p.ldr + col, live ? n : 0, r);
+        finish_fwd<BF16>(p, v, bias, r, row, col, n, live);
+    }
+}
+
+// The shares of K added in order, and the write-back: 16 rows by 64 columns a workgroup.
+template <bool BF16>
+__global__ void __launch_bounds__(128) l16_join_kernel(L16Params p, int tiles_n)
+{
+    Chunk c{};
+    const int id = blockIdx.x / tiles_n;
+    if (id >= find_chunk(p.groups, p.M, 16, id, c))
+        return;
+    const int row = c.begin + c.index * 16 + (int)threadIdx.x / 8;
+    const int col = (int)(blockIdx.x % tiles_n) * kCols + (int)threadIdx.x % 8 * 8, n = p.N - col;
+    const bool live = row < c.end && n > 0;
+    float v[8], bias[8], r[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        v[e] = r[e] = 0.0f;
+    load_row<LL_TYPE_F32, 8>(p.bias + (int64_t)c.group * p.N + col, p.bias != nullptr ? n : 0, bias);
+    if (p.R != nullptr)
+        load8<BF16>(p.ctype, p.R, (int64_t)row * p.ldr + col, live ? n : 0, r);
+#pragma unroll 4
+    for (int s = 0; s < p.shares; ++s) {
+        float u[8];
+        load_row<LL_TYPE_F32, 8>(p.ws + ((int64_t)s * p.M + row) * p.N + col, live ? n : 0, u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] += u[e];
+    }
+    finish_fwd<BF16>(p, v, bias, r, row, col, n, live);
+}
+
+template <bool BF16, int MT, int DEPTH>
+__global__ void __launch_bounds__(64 * kWaves) l16_rows_kernel(L16Params p, int tiles_n)
+{
+    constexpr int PT = 8 + 2 * MT;            // copies of a turn, 1 KiB each: eight rows of 128 bytes
+    constexpr int TURN = PT * 512;            // its values
+    static_assert(kWaves * DEPTH * TURN * 2 <= 160 * 1024 && (DEPTH - 1) * PT <= 63, "the rings fit the LDS, the copies the counter");
+    static_assert(kWaves * MT * 16 * kPitch * 4 <= kWaves * DEPTH * TURN * 2, "the waves' sums fit the rings");
+    __shared__ __attribute__((aligned(1024))) uint16_t ring[kWaves][DEPTH][TURN];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int share = blockIdx.y;
+    Chunk c{};
+    const int id = blockIdx.x / tiles_n;
+    if (id >= find_chunk(p.groups, p.M, MT * 16, id, c))
+        return;
+    const int m0 = c.begin + c.index * MT * 16, n0 = (int)(blockIdx.x % tiles_n) * kCols;
+
+    // this share's turns, and this wave's among them: t0, t0 + 4, ...
+    const int all = cdiv(p.K, kTurn), each = cdiv(all, p.shares);
+    const int t_end = min(all, (share + 1) * each), t0 = share * each + wave;
+    const int turns = cdiv(each, kWaves);   // the same in every wave; past the end zeros come
+    const uint16_t *w = static_cast<const uint16_t *>(p.B) + c.group * p.stride_b + (int64_t)n0 * p.ldb;
+    const uint16_t *x = p.A + (int64_t)m0 * p.lda;
+    const int wrows = min(p.N - n0, kCols), xrows = min(c.end - m0, MT * 16);
+    // copy j: rows 8 j + lane / 8; pieces of 16 bytes XORed by (row / 2) % 8, which for eight rows
+    // is one of two orders
+    const int r8 = lane >> 3;
+    int piece[2];
+    uint32_t woff[2], xoff[2];
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        piece[v] = ((lane & 7) ^ rows_swz(8 * v + r8)) * 8;
+        woff[v] = (uint32_t)(8 * v + r8) * (uint32_t)(2 * p.ldb) + 2 * piece[v];
+        xoff[v] = (uint32_t)(8 * v + r8) * (uint32_t)(2 * p.lda) + 2 * piece[v];
+    }
+    const uint32_t base = lds_addr(&ring[wave][0][0]);
+    auto copy = [&](int slot, int i) __attribute__((always_inline)) {
+        const int t = t0 + i * kWaves, left = t < t_end ? min(p.K - t * kTurn, kTurn) : 0;
+        const int64_t k0 = (int64_t)t * kTurn;
+        const uint64_t wat = (uint64_t)(w + k0), xat = (uint64_t)(x + k0);
+        const u32x4 wbuf = {(uint32_t)wat, (uint32_t)(wat >> 32), left > 0 ? (uint32_t)(wrows - 1) * (uint32_t)(2 * p.ldb) + 2 * left : 0u, 0x00020000u};
+        const u32x4 xbuf = {(uint32_t)xat, (uint32_t)(xat >> 32), left > 0 ? (uint32_t)(xrows - 1) * (uint32_t)(2 * p.lda) + 2 * left : 0u, 0x00020000u};
+        uint32_t wo[2], xo[2];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            wo[v] = piece[v] < left ? woff[v] : kPastEnd;
+            xo[v] = piece[v] < left ? xoff[v] : kPastEnd;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            lds_buffer_16(wbuf, wo[j & 1] + (j >> 1) * 16 * (uint32_t)(2 * p.ldb), base + (slot * PT + j) * 1024);
+#pragma unroll
+        for (int j = 0; j < 2 * MT; ++j)
+            lds_buffer_16(xbuf, xo[j & 1] + (j >> 1) * 16 * (uint32_t)(2 * p.lda), base + (slot * PT + 8 + j) * 1024);
+    };
+    f32x4 acc[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d)
+        copy(d, d);
+    const int r16 = lane & 15, grp = lane >> 4;
+    int slot = 0;
+#pragma unroll 1
+    for (int i = 0; i < turns; ++i) {
+        __builtin_amdgcn_s_waitcnt(LL_VMCNT((DEPTH - 1) * PT));   // this turn's copies have landed
+        asm volatile("" ::: "memory");
+        const uint16_t *at = &ring[wave][0][0] + slot * TURN;
+        f16x8 fw[2][4], fx[2][MT];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                fw[s][j] = *reinterpret_cast<const f16x8 *>(at + (16 * j + r16) * 64 + ((4 * s + grp) ^ rows_swz(r16)) * 8);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+                fx[s][m] = *reinterpret_cast<const f16x8 *>(at + (64 + 16 * m + r16) * 64 + ((4 * s + grp) ^ rows_swz(r16)) * 8);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");        // read: the slot may be filled again
+        copy(slot, i + DEPTH);
+        slot = slot == DEPTH - 1 ? 0 : slot + 1;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    acc[m][j] = mma<BF16>(fw[s][j], fx[s][m], acc[m][j]);
+    }
+    __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));   // (the zeros past the last turn are on their way into the rings)
+    __syncthreads();
+    float *part = reinterpret_cast<float *>(&ring[0][0][0]);
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4 *>(&part[(wave * MT * 16 + 16 * m + r16) * kPitch + 16 * j + 4 * grp]) = acc[m][j];
+    __syncthreads();
+    finish_rows<BF16, MT, 64 * kWaves>(p, part, c, m0, n0, share);
+}
+
+// Rows off 16 bytes: operands straight into the matrix instruction's registers, 16 bytes a load at
+// any alignment, what crosses a row's end value by value.
 __device__ __forceinline__ f16x8 load8_at(const uint16_t *row, int64_t k, int K)
 {
     u32x4 v = {0u, 0u, 0u, 0u};
-    if (VEC ? k < K : k + 8 <= K) {
+    if (k + 8 <= K) {
         v = load16<u32x4>(row + k);
-    } else if (!VEC) {
+    } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (k + e < K)
@@ -34,125 +207,132 @@ __device__ __forceinline__ f16x8 load8_at(const uint16_t *row, int64_t k, int K)
     return __builtin_bit_cast(f16x8, v);
 }
 
-template <bool BF16, int MT, int NB, int NW, int DEPTH, bool VEC>
-__global__ void __launch_bounds__(64 * NW) l16_rows_kernel(L16Params p, int tiles_n)
+template <bool BF16, int MT>
+__global__ void __launch_bounds__(64 * kWaves) l16_rows_any_kernel(L16Params p, int tiles_n)
 {
-    constexpr int PITCH = NB * 16 + 4;
-    __shared__ float part[NW][MT * 16 * PITCH];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int DEPTH = 2;
+    __shared__ float part[kWaves * MT * 16 * kPitch];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int share = blockIdx.y;
     Chunk c{};
     const int id = blockIdx.x / tiles_n;
     if (id >= find_chunk(p.groups, p.M, MT * 16, id, c))
         return;
-    const int m0 = c.begin + c.index * MT * 16, n0 = (int)(blockIdx.x % tiles_n) * NB * 16;
+    const int m0 = c.begin + c.index * MT * 16, n0 = (int)(blockIdx.x % tiles_n) * kCols;
     const int grp = lane >> 4, r16 = lane & 15;
+    const int all = cdiv(p.K, kTurn), each = cdiv(all, p.shares);
+    const int t_end = min(all, (share + 1) * each), t0 = share * each + wave, turns = cdiv(each, kWaves);
     const uint16_t *w = static_cast<const uint16_t *>(p.B) + c.group * p.stride_b;
-    const uint16_t *wrow[NB], *xrow[MT];
+    const uint16_t *wrow[4], *xrow[MT];
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-        wrow[j] = w + (int64_t)min(n0 + 16 * j + r16, p.N - 1) * p.ldb + 8 * grp;
+    for (int j = 0; j < 4; ++j)
+        wrow[j] = w + (int64_t)min(n0 + 16 * j + r16, p.N - 1) * p.ldb;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
-        xrow[i] = p.A + (int64_t)min(m0 + 16 * i + r16, c.end - 1) * p.lda + 8 * grp;
-    const int K = p.K - 8 * grp;   // this lane's values of a row
-
-    f32x4 acc[MT][NB];
+        xrow[i] = p.A + (int64_t)min(m0 + 16 * i + r16, c.end - 1) * p.lda;
+    f32x4 acc[MT][4];
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
+        for (int j = 0; j < 4; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // (turns past K load nothing and add zeros: every wave has as many)
-    const int turns = cdiv(cdiv(p.K, kTurn), NW);
-    f16x8 wv[DEPTH][2][NB], xv[DEPTH][2][MT];
-    auto fetch = [&](int t, f16x8 (&wd)[2][NB], f16x8 (&xd)[2][MT]) __attribute__((always_inline)) {
-        const int64_t k = ((int64_t)t * NW + wave) * kTurn;
+    f16x8 wv[DEPTH][2][4], xv[DEPTH][2][MT];
+    auto fetch = [&](int i, f16x8 (&wd)[2][4], f16x8 (&xd)[2][MT]) __attribute__((always_inline)) {
+        const int t = t0 + i * kWaves, end = t < t_end ? p.K : 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            const int64_t k = (int64_t)t * kTurn + 32 * h + 8 * grp;
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
-                wd[h][j] = load8_at<VEC>(wrow[j], k + 32 * h, K);
+            for (int j = 0; j < 4; ++j)
+                wd[h][j] = load8_at(wrow[j], k, end);
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-                xd[h][i] = load8_at<VEC>(xrow[i], k + 32 * h, K);
+            for (int m = 0; m < MT; ++m)
+                xd[h][m] = load8_at(xrow[m], k, end);
         }
     };
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d)
         fetch(d, wv[d], xv[d]);
-    for (int t = 0; t < turns; t += DEPTH) {
+    for (int i = 0; i < turns; i += DEPTH) {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {   // (past the last turn: zeros)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < MT; ++i)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                    for (int j = 0; j < NB; ++j)
-                        acc[i][j] = mma<BF16>(wv[d][h][j], xv[d][h][i], acc[i][j]);
-            fetch(t + d + DEPTH, wv[d], xv[d]);
+                    for (int j = 0; j < 4; ++j)
+                        acc[m][j] = mma<BF16>(wv[d][h][j], xv[d][h][m], acc[m][j]);
+            fetch(i + d + DEPTH, wv[d], xv[d]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int j = 0; j < NB; ++j)
-            *reinterpret_cast<f32x4 *>(&part[wave][(16 * i + r16) * PITCH + 16 * j + 4 * grp]) = acc[i][j];
+        for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<f32x4 *>(&part[(wave * MT * 16 + 16 * m + r16) * kPitch + 16 * j + 4 * grp]) = acc[m][j];
     __syncthreads();
-    // eight columns a lane; four lanes are a block of 32
-    constexpr int LPR = NB * 2;
-    static_assert(LPR % 4 == 0, "whole blocks of Z's 8 bits");
-    for (int s = tid; s < MT * 16 * LPR; s += 64 * NW) {
-        const int rl = s / LPR, cl = s % LPR * 8, row = m0 + rl, col = n0 + cl, n = p.N - col;
-        const bool live = row < c.end && n > 0;
-        float v[8], bias[8], r[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            v[e] = r[e] = 0.0f;
-        load_row<LL_TYPE_F32, 8>(p.bias + (int64_t)c.group * p.N + col, p.bias != nullptr ? n : 0, bias);
-        if (p.R != nullptr)
-            load8<BF16>(p.ctype, p.R, (int64_t)row * p.ldr + col, live ? n : 0, r);
-#pragma unroll
-        for (int k = 0; k < NW; ++k) {
-            const f32x4 lo = *reinterpret_cast<const f32x4 *>(&part[k][rl * PITCH + cl]);
-            const f32x4 hi = *reinterpret_cast<const f32x4 *>(&part[k][rl * PITCH + cl + 4]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] += lo[e], v[4 + e] += hi[e];
-        }
-        finish_fwd<BF16>(p, v, bias, r, row, col, n, live);
-    }
+    finish_rows<BF16, MT, 64 * kWaves>(p, part, c, m0, n0, share);
 }
 
-template <bool BF16, int MT, int NB, int NW, int DEPTH, bool VEC>
-static hipError_t launch_mt(const L16Params &p, hipStream_t s)
+// ---- which of them, and in how many shares ------------------------------------------
+
+// Tiles of 16 rows a workgroup has: those of a group of average length, up to four.
+static int row_tiles(int M, int groups)
 {
-    const int tiles_n = cdiv(p.N, NB * 16);
-    const int64_t rows = p.groups.offsets == nullptr ? cdiv(p.M, MT * 16)
-                                                     : (int64_t)(p.M / (MT * 16)) + (p.groups.n < p.M ? p.groups.n : p.M);
-    if (rows * tiles_n > max_grid_x(64 * NW))
+    const int64_t each = ((int64_t)M + groups - 1) / groups;
+    return each <= 16 ? 1 : each <= 32 ? 2 : 4;
+}
+
+bool l16_takes_rows(int M, int groups) { return groups > 0 && ((int64_t)M + groups - 1) / groups <= 64; }
+
+static int64_t row_chunks(int M, int groups, int rows) { return (int64_t)M / rows + (groups < M ? groups : M); }
+
+// Shares of K with a workspace: as many as fill the CUs once, with eight turns at least to a
+// wave; none where the workgroups fill half of them by themselves.
+int l16_row_shares(int M, int N, int K, int groups, int cus)
+{
+    if (M == 0 || N == 0 || !l16_takes_rows(M, groups))
+        return 1;
+    const int64_t work = (int64_t)cdiv(N, kCols) * (groups < M ? groups : M);
+    const int64_t most = K / (8 * kWaves * kTurn), fill = cus / work;
+    const int64_t s = fill < most ? fill : most;
+    return s < 2 ? 1 : s < 16 ? (int)s : 16;
+}
+
+int64_t l16_workspace(int M, int N, int K, int groups, int cus)
+{
+    const int s = l16_row_shares(M, N, K, groups, cus);
+    return s > 1 ? (int64_t)s * M * N * 4 : 0;
+}
+
+template <bool BF16, int MT>
+static hipError_t launch_mt(const L16Params &p, bool vec, hipStream_t s)
+{
+    const int tiles_n = cdiv(p.N, kCols);
+    const int64_t grid = (p.groups.offsets == nullptr ? cdiv(p.M, MT * 16) : row_chunks(p.M, p.groups.n, MT * 16)) * tiles_n;
+    const int64_t join = (p.groups.offsets == nullptr ? cdiv(p.M, 16) : row_chunks(p.M, p.groups.n, 16)) * tiles_n;
+    if (grid > max_grid_x(64 * kWaves) || join > max_grid_x(128))
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((l16_rows_kernel<BF16, MT, NB, NW, DEPTH, VEC>), dim3((unsigned)(rows * tiles_n)), dim3(64 * NW), 0, s,
-                       p, tiles_n);
+    const dim3 d((unsigned)grid, (unsigned)p.shares), b(64 * kWaves);
+    constexpr int DEPTH = MT == 1 ? 4 : MT == 2 ? 3 : 2;
+    if (vec)
+        hipLaunchKernelGGL((l16_rows_kernel<BF16, MT, DEPTH>), d, b, 0, s, p, tiles_n);
+    else
+        hipLaunchKernelGGL((l16_rows_any_kernel<BF16, MT>), d, b, 0, s, p, tiles_n);
+    if (p.shares > 1)
+        hipLaunchKernelGGL(l16_join_kernel<BF16>, dim3((unsigned)join), dim3(128), 0, s, p, tiles_n);
     return hipGetLastError();
-}
-
-template <bool BF16, bool VEC>
-static hipError_t launch_rows16(const L16Params &p, hipStream_t s)
-{
-    const int each = cdiv(p.M, p.groups.n < p.M ? p.groups.n : p.M);
-    if (each <= 16)
-        return launch_mt<BF16, 1, 2, 8, 3, VEC>(p, s);
-    if (each <= 32)
-        return launch_mt<BF16, 2, 2, 8, 3, VEC>(p, s);
-    return launch_mt<BF16, 4, 2, 8, 2, VEC>(p, s);
 }
 
 hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, hipStream_t s)
 {
-    if (vec)
-        return bf16 ? launch_rows16<true, true>(p, s) : launch_rows16<false, true>(p, s);
-    return bf16 ? launch_rows16<true, false>(p, s) : launch_rows16<false, false>(p, s);
+    const int mt = row_tiles(p.M, p.groups.n);
+    if (mt == 1)
+        return bf16 ? launch_mt<true, 1>(p, vec, s) : launch_mt<false, 1>(p, vec, s);
+    if (mt == 2)
+        return bf16 ? launch_mt<true, 2>(p, vec, s) : launch_mt<false, 2>(p, vec, s);
+    return bf16 ? launch_mt<true, 4>(p, vec, s) : launch_mt<false, 4>(p, vec, s);
 }
 
 }  // namespace ll

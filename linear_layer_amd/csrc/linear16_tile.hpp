@@ -26,9 +26,6 @@
 // in which four lanes hold one block of 32 of Z's 8 bits.
 #pragma once
 
-#include <type_traits>
-#include <utility>
-
 #include "launch.hpp"
 #include "linear16_finish.hpp"
 
@@ -63,39 +60,6 @@ template <int BM> struct Cfg {
     static constexpr int STAGE = BM * BK;                   // values of an operand's stage
     static constexpr int PIECES = STAGE * 2 / 16 / NT;      // of 16 bytes, a thread's of a stage
 };
-
-// 16-byte chunk c of row `row` of a ROWS stage, and unit u of k-row k of a COLS stage.
-__device__ __forceinline__ int rows_swz(int row) { return (row >> 1) & 7; }
-__device__ __forceinline__ int cols_swz(int k) { return 2 * (k & 3) + ((k >> 3) & 1); }
-
-template <int... I, class F>
-__device__ __forceinline__ void static_for_(std::integer_sequence<int, I...>, F f)
-{
-    (f(std::integral_constant<int, I>{}), ...);
-}
-// f(0), .., f(N - 1) with constants for arguments.
-template <int N, class F>
-__device__ __forceinline__ void static_for(F f)
-{
-    static_for_(std::make_integer_sequence<int, N>{}, f);
-}
-
-constexpr uint32_t kPastEnd = 0x80000000u;   // past the end of every buffer here: 256 rows of less than 2^21 values
-
-// buffer_load_dwordx4 into LDS: this lane's 16 bytes at byte `off` of the buffer go to LDS
-// byte lds_base + 16 * lane, zeros where they lie past its end. Inline assembly, so that the
-// compiler does not take it for an LDS store that every LDS read must wait for; the caller
-// waits for the copies before the barrier that publishes them. The compiler's hazard checks
-// do not look inside: M0 may be used one wait state after its write. (Four more, for a
-// descriptor that v_readfirstlane might have written just before, would cost the matrix
-// cores as much as all the copies; descriptors here are made by scalar instructions.)
-__device__ __forceinline__ void lds_buffer_16(const u32x4 &buffer, uint32_t off, uint32_t lds_base)
-{
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds_base), "v"(off), "s"(buffer)
-                 : "memory", "m0");
-}
 
 typedef const __attribute__((address_space(3))) f16x8 *LdsF16x8;
 typedef __attribute__((address_space(3))) s16x4 *LdsS16x4;

@@ -24,12 +24,13 @@ def args(k, lds):
     return p, {n: k.get("ld" + n, w) for n, w in lds.items()}
 
 
-def fwd(M=4, N=64, K=32, type=BF16, ytype=BF16, act=0, groups=1, stride=0, **k):
+def fwd(M=4, N=64, K=32, type=BF16, ytype=BF16, act=0, groups=1, stride=0, ws_bytes=0, **k):
     k.setdefault("offsets", None)
+    k.setdefault("ws", None)
     p, ld = args(k, {"X": max(K, 1), "W": max(K, 1), **{n: max(N, 1) for n in ("R", "Y", "Z", "ZQ")}, "ZS": max(-(-N // 32), 1)})
     return ll.load().linear16_nt(M, N, K, type, p["X"], ld["X"], groups, p["offsets"], p["W"], ld["W"], stride, p["bias"],
                                  act, ytype, p["R"], ld["R"], p["Y"], ld["Y"], p["Z"], ld["Z"], p["ZQ"], ld["ZQ"], p["ZS"],
-                                 ld["ZS"], None)
+                                 ld["ZS"], p["ws"], ws_bytes, None)
 
 
 def gact(M=4, N=64, type=BF16, ytype=BF16, act=4, groups=1, ws_bytes=1 << 20, **k):
