@@ -55,7 +55,7 @@ hipError_t launch_l16_fwd(bool bf16, L16Params p, bool vec, int cus, hipStream_t
 bool l16_takes_rows(int M, int groups);
 int l16_row_shares(int M, int N, int K, int groups, int cus);
 int64_t l16_workspace(int M, int N, int K, int groups, int cus);
-hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, hipStream_t s);
+hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, int cus, hipStream_t s);
 hipError_t launch_l16_dx(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 

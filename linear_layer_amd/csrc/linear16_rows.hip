@@ -1,9 +1,9 @@
 // The 16-bit layer for few rows: every weight is read once for at most 64 rows, so memory bounds
 // the product and the matrix cores have time to spare.
 //
-// A workgroup of four waves computes MT x 16 rows by 64 columns, over all of the inner dimension
+// A workgroup of NW waves computes MT x 16 rows by 64 columns, over all of the inner dimension
 // or a share of it. Its waves share that out in turns of 64 values, a whole line of a row: wave
-// w takes turns w, w + 4, ... and copies 64 rows of W and the rows of X straight into a ring of
+// w takes turns w, w + NW, ... and copies 64 rows of W and the rows of X straight into a ring of
 // its own in LDS (DEPTH turns, 8 + 2 MT KiB each, in the tile kernel's order), so that no wave
 // waits for another and all of a CU's LDS but the turn in use is on its way from memory. At the end
 // the waves' sums meet in LDS and are added in the waves' order. Shares of K go through the
@@ -21,14 +21,13 @@ using namespace l16;
 
 constexpr int kTurn = 64;     // values of the inner dimension a wave takes at a time
 constexpr int kCols = 64;     // columns of a workgroup
-constexpr int kWaves = 4;
 constexpr int kPitch = kCols + 4;
 
 // The waves' sums added, and the write-back or the share's sums. The sums are at part[wave][row][column].
-template <bool BF16, int MT, int THREADS>
+template <bool BF16, int MT, int NW>
 __device__ __forceinline__ void finish_rows(const L16Params &p, const float *part, const Chunk &c, int m0, int n0, int share)
 {
-    for (int s = threadIdx.x; s < MT * 16 * 8; s += THREADS) {
+    for (int s = threadIdx.x; s < MT * 16 * 8; s += 64 * NW) {
         const int rl = s / 8, cl = s % 8 * 8, row = m0 + rl, col = n0 + cl, n = p.N - col;
         const bool live = row < c.end && n > 0;
         float v[8];
@@ -36,7 +35,7 @@ __device__ __forceinline__ void finish_rows(const L16Params &p, const float *par
         for (int e = 0; e < 8; ++e)
             v[e] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < kWaves; ++k) {
+        for (int k = 0; k < NW; ++k) {
             const f32x4 lo = *reinterpret_cast<const f32x4 *>(&part[(k * MT * 16 + rl) * kPitch + cl]);
             const f32x4 hi = *reinterpret_cast<const f32x4 *>(&part[(k * MT * 16 + rl) * kPitch + cl + 4]);
 #pragma unroll
@@ -88,14 +87,14 @@ __global__ void __launch_bounds__(128) l16_join_kernel(L16Params p, int tiles_n)
     finish_fwd<BF16>(p, v, bias, r, row, col, n, live);
 }
 
-template <bool BF16, int MT, int DEPTH>
-__global__ void __launch_bounds__(64 * kWaves) l16_rows_kernel(L16Params p, int tiles_n)
+template <bool BF16, int MT, int NW, int DEPTH>
+__global__ void __launch_bounds__(64 * NW) l16_rows_kernel(L16Params p, int tiles_n)
 {
     constexpr int PT = 8 + 2 * MT;            // copies of a turn, 1 KiB each: eight rows of 128 bytes
     constexpr int TURN = PT * 512;            // its values
-    static_assert(kWaves * DEPTH * TURN * 2 <= 160 * 1024 && (DEPTH - 1) * PT <= 63, "the rings fit the LDS, the copies the counter");
-    static_assert(kWaves * MT * 16 * kPitch * 4 <= kWaves * DEPTH * TURN * 2, "the waves' sums fit the rings");
-    __shared__ __attribute__((aligned(1024))) uint16_t ring[kWaves][DEPTH][TURN];
+    static_assert(NW * DEPTH * TURN * 2 <= 160 * 1024 && (DEPTH - 1) * PT <= 63, "the rings fit the LDS, the copies the counter");
+    static_assert(NW * MT * 16 * kPitch * 4 <= NW * DEPTH * TURN * 2, "the waves' sums fit the rings");
+    __shared__ __attribute__((aligned(1024))) uint16_t ring[NW][DEPTH][TURN];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int share = blockIdx.y;
     Chunk c{};
@@ -107,7 +106,7 @@ __global__ void __launch_bounds__(64 * kWaves) l16_rows_kernel(L16Params p, int 
     // this share's turns, and this wave's among them: t0, t0 + 4, ...
     const int all = cdiv(p.K, kTurn), each = cdiv(all, p.shares);
     const int t_end = min(all, (share + 1) * each), t0 = share * each + wave;
-    const int turns = cdiv(each, kWaves);   // the same in every wave; past the end zeros come
+    const int turns = cdiv(each, NW);   // the same in every wave; past the end zeros come
     const uint16_t *w = static_cast<const uint16_t *>(p.B) + c.group * p.stride_b + (int64_t)n0 * p.ldb;
     const uint16_t *x = p.A + (int64_t)m0 * p.lda;
     const int wrows = min(p.N - n0, kCols), xrows = min(c.end - m0, MT * 16);
@@ -124,7 +123,7 @@ __global__ void __launch_bounds__(64 * kWaves) l16_rows_kernel(L16Params p, int 
     }
     const uint32_t base = lds_addr(&ring[wave][0][0]);
     auto copy = [&](int slot, int i) __attribute__((always_inline)) {
-        const int t = t0 + i * kWaves, left = t < t_end ? min(p.K - t * kTurn, kTurn) : 0;
+        const int t = t0 + i * NW, left = t < t_end ? min(p.K - t * kTurn, kTurn) : 0;
         const int64_t k0 = (int64_t)t * kTurn;
         const uint64_t wat = (uint64_t)(w + k0), xat = (uint64_t)(x + k0);
         const u32x4 wbuf = {(uint32_t)wat, (uint32_t)(wat >> 32), left > 0 ? (uint32_t)(wrows - 1) * (uint32_t)(2 * p.ldb) + 2 * left : 0u, 0x00020000u};
@@ -188,7 +187,7 @@ __global__ void __launch_bounds__(64 * kWaves) l16_rows_kernel(L16Params p, int 
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<f32x4 *>(&part[(wave * MT * 16 + 16 * m + r16) * kPitch + 16 * j + 4 * grp]) = acc[m][j];
     __syncthreads();
-    finish_rows<BF16, MT, 64 * kWaves>(p, part, c, m0, n0, share);
+    finish_rows<BF16, MT, NW>(p, part, c, m0, n0, share);
 }
 
 // Rows off 16 bytes: operands straight into the matrix instruction's registers, 16 bytes a load at
@@ -207,11 +206,11 @@ __device__ __forceinline__ f16x8 load8_at(const uint16_t *row, int64_t k, int K)
     return __builtin_bit_cast(f16x8, v);
 }
 
-template <bool BF16, int MT>
-__global__ void __launch_bounds__(64 * kWaves) l16_rows_any_kernel(L16Params p, int tiles_n)
+template <bool BF16, int MT, int NW>
+__global__ void __launch_bounds__(64 * NW) l16_rows_any_kernel(L16Params p, int tiles_n)
 {
     constexpr int DEPTH = 2;
-    __shared__ float part[kWaves * MT * 16 * kPitch];
+    __shared__ float part[NW * MT * 16 * kPitch];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int share = blockIdx.y;
     Chunk c{};
@@ -221,7 +220,7 @@ __global__ void __launch_bounds__(64 * kWaves) l16_rows_any_kernel(L16Params p, 
     const int m0 = c.begin + c.index * MT * 16, n0 = (int)(blockIdx.x % tiles_n) * kCols;
     const int grp = lane >> 4, r16 = lane & 15;
     const int all = cdiv(p.K, kTurn), each = cdiv(all, p.shares);
-    const int t_end = min(all, (share + 1) * each), t0 = share * each + wave, turns = cdiv(each, kWaves);
+    const int t_end = min(all, (share + 1) * each), t0 = share * each + wave, turns = cdiv(each, NW);
     const uint16_t *w = static_cast<const uint16_t *>(p.B) + c.group * p.stride_b;
     const uint16_t *wrow[4], *xrow[MT];
 #pragma unroll
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(64 * kWaves) l16_rows_any_kernel(L16Params p, 
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     f16x8 wv[DEPTH][2][4], xv[DEPTH][2][MT];
     auto fetch = [&](int i, f16x8 (&wd)[2][4], f16x8 (&xd)[2][MT]) __attribute__((always_inline)) {
-        const int t = t0 + i * kWaves, end = t < t_end ? p.K : 0;
+        const int t = t0 + i * NW, end = t < t_end ? p.K : 0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int64_t k = (int64_t)t * kTurn + 32 * h + 8 * grp;
@@ -272,7 +271,7 @@ __global__ void __launch_bounds__(64 * kWaves) l16_rows_any_kernel(L16Params p, 
         for (int j = 0; j < 4; ++j)
             *reinterpret_cast<f32x4 *>(&part[(wave * MT * 16 + 16 * m + r16) * kPitch + 16 * j + 4 * grp]) = acc[m][j];
     __syncthreads();
-    finish_rows<BF16, MT, 64 * kWaves>(p, part, c, m0, n0, share);
+    finish_rows<BF16, MT, NW>(p, part, c, m0, n0, share);
 }
 
 // ---- which of them, and in how many shares ------------------------------------------
@@ -295,7 +294,7 @@ int l16_row_shares(int M, int N, int K, int groups, int cus)
     if (M == 0 || N == 0 || !l16_takes_rows(M, groups))
         return 1;
     const int64_t work = (int64_t)cdiv(N, kCols) * (groups < M ? groups : M);
-    const int64_t most = K / (8 * kWaves * kTurn), fill = cus / work;
+    const int64_t most = K / (8 * 4 * kTurn), fill = cus / work;
     const int64_t s = fill < most ? fill : most;
     return s < 2 ? 1 : s < 16 ? (int)s : 16;
 }
@@ -306,33 +305,41 @@ int64_t l16_workspace(int M, int N, int K, int groups, int cus)
     return s > 1 ? (int64_t)s * M * N * 4 : 0;
 }
 
-template <bool BF16, int MT>
-static hipError_t launch_mt(const L16Params &p, bool vec, hipStream_t s)
+template <bool BF16, int MT, int NW>
+static hipError_t launch_nw(const L16Params &p, bool vec, int64_t grid, hipStream_t s)
 {
     const int tiles_n = cdiv(p.N, kCols);
-    const int64_t grid = (p.groups.offsets == nullptr ? cdiv(p.M, MT * 16) : row_chunks(p.M, p.groups.n, MT * 16)) * tiles_n;
     const int64_t join = (p.groups.offsets == nullptr ? cdiv(p.M, 16) : row_chunks(p.M, p.groups.n, 16)) * tiles_n;
-    if (grid > max_grid_x(64 * kWaves) || join > max_grid_x(128))
+    if (grid > max_grid_x(64 * NW) || join > max_grid_x(128))
         return hipErrorInvalidValue;
-    const dim3 d((unsigned)grid, (unsigned)p.shares), b(64 * kWaves);
+    const dim3 d((unsigned)grid, (unsigned)p.shares), b(64 * NW);
     constexpr int DEPTH = MT == 1 ? 4 : MT == 2 ? 3 : 2;
     if (vec)
-        hipLaunchKernelGGL((l16_rows_kernel<BF16, MT, DEPTH>), d, b, 0, s, p, tiles_n);
+        hipLaunchKernelGGL((l16_rows_kernel<BF16, MT, NW, DEPTH>), d, b, 0, s, p, tiles_n);
     else
-        hipLaunchKernelGGL((l16_rows_any_kernel<BF16, MT>), d, b, 0, s, p, tiles_n);
+        hipLaunchKernelGGL((l16_rows_any_kernel<BF16, MT, NW>), d, b, 0, s, p, tiles_n);
     if (p.shares > 1)
         hipLaunchKernelGGL(l16_join_kernel<BF16>, dim3((unsigned)join), dim3(128), 0, s, p, tiles_n);
     return hipGetLastError();
 }
 
-hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, hipStream_t s)
+// Four waves, one workgroup a CU, where the CUs are not filled; else two waves and two workgroups,
+// one of which reads on while the other begins or ends.
+template <bool BF16, int MT>
+static hipError_t launch_mt(const L16Params &p, bool vec, int cus, hipStream_t s)
+{
+    const int64_t grid = (p.groups.offsets == nullptr ? cdiv(p.M, MT * 16) : row_chunks(p.M, p.groups.n, MT * 16)) * cdiv(p.N, kCols);
+    return grid * p.shares <= cus ? launch_nw<BF16, MT, 4>(p, vec, grid, s) : launch_nw<BF16, MT, 2>(p, vec, grid, s);
+}
+
+hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, int cus, hipStream_t s)
 {
     const int mt = row_tiles(p.M, p.groups.n);
     if (mt == 1)
-        return bf16 ? launch_mt<true, 1>(p, vec, s) : launch_mt<false, 1>(p, vec, s);
+        return bf16 ? launch_mt<true, 1>(p, vec, cus, s) : launch_mt<false, 1>(p, vec, cus, s);
     if (mt == 2)
-        return bf16 ? launch_mt<true, 2>(p, vec, s) : launch_mt<false, 2>(p, vec, s);
-    return bf16 ? launch_mt<true, 4>(p, vec, s) : launch_mt<false, 4>(p, vec, s);
+        return bf16 ? launch_mt<true, 2>(p, vec, cus, s) : launch_mt<false, 2>(p, vec, cus, s);
+    return bf16 ? launch_mt<true, 4>(p, vec, cus, s) : launch_mt<false, 4>(p, vec, cus, s);
 }
 
 }  // namespace ll
