@@ -140,12 +140,13 @@ __device__ __forceinline__ void group_rows(const Groups &gr, int M, int g, int &
 struct Chunk {
     int group, begin, end, index, group_first;
 };
-template <bool BY_GROUP = false>
-__device__ __forceinline__ int find_chunk(const Groups &gr, int M, int step, int id, Chunk &c)
+// find_chunk_by: a group of r rows has count(r) of them, in whatever form.
+template <bool BY_GROUP = false, class Count>
+__device__ __forceinline__ int find_chunk_by(const Groups &gr, int M, Count count, int id, Chunk &c)
 {
     if (gr.offsets == nullptr) {
-        c = Chunk{0, 0, M, BY_GROUP ? cdiv(M, step) : id, 0};
-        return cdiv(M, step);
+        c = Chunk{0, 0, M, BY_GROUP ? count(M) : id, 0};
+        return count(M);
     }
     const int lane = threadIdx.x & 63;
     int top = min(max(gr.offsets[0], 0), M), chunks = 0;
@@ -155,7 +156,7 @@ __device__ __forceinline__ int find_chunk(const Groups &gr, int M, int step, int
         e = max(wave_max_scan(e), top);
         const int before = __shfl_up(e, 1);
         const int b = lane == 0 ? top : before;
-        const int n = g < gr.n ? cdiv(e - b, step) : 0;
+        const int n = g < gr.n ? count(e - b) : 0;
         const int incl = wave_sum_scan(n) + chunks, excl = incl - n;
         const unsigned long long hit = __ballot(BY_GROUP ? g == id : id >= excl && id < incl);
         if (hit != 0) {
@@ -171,6 +172,11 @@ __device__ __forceinline__ int find_chunk(const Groups &gr, int M, int step, int
     c.index = __builtin_amdgcn_readfirstlane(c.index);
     c.group_first = __builtin_amdgcn_readfirstlane(c.group_first);
     return __builtin_amdgcn_readfirstlane(chunks);
+}
+template <bool BY_GROUP = false>
+__device__ __forceinline__ int find_chunk(const Groups &gr, int M, int step, int id, Chunk &c)
+{
+    return find_chunk_by<BY_GROUP>(gr, M, [step](int rows) { return cdiv(rows, step); }, id, c);
 }
 
 // ---- activations ----------------------------------------------------------------

@@ -50,15 +50,9 @@ __device__ __forceinline__ void mma_acc(const f16x8 &a, const f16x8 &b, f32x4 &c
 // wrote them and the first mma_acc.
 __device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
 
-// Waves, and the block of C that each has: 256 x 256 as 2 x 2 waves of 128 x 128 (one a
-// SIMD), 128 x 128 as 2 x 2 of 64 x 64 (two workgroups a CU).
-template <int BM> struct Cfg {
-    static constexpr int WGM = 2, WGN = 2, NW = WGM * WGN, NT = 64 * NW;
-    static constexpr int WPE = BM == 256 ? 1 : 2;           // waves a SIMD
-    static constexpr int BK = 64;                           // two steps of the MFMA
-    static constexpr int WTM = BM / WGM, WTN = BM / WGN, FM = WTM / 16, FN = WTN / 16;
-    static constexpr int STAGE = BM * BK;                   // values of an operand's stage
-    static constexpr int PIECES = STAGE * 2 / 16 / NT;      // of 16 bytes, a thread's of a stage
+// A workgroup: 2 x 2 waves, each with a quarter of its tile; stages of two steps of the MFMA.
+struct Block {
+    static constexpr int NW = 4, NT = 64 * NW, BK = 64;
 };
 
 typedef const __attribute__((address_space(3))) f16x8 *LdsF16x8;
@@ -68,9 +62,10 @@ typedef __attribute__((address_space(3))) s16x4 *LdsS16x4;
 // may be asked for), `klen` of the contracted axis.
 template <bool BF16, int BM, int SIDE, bool VEC>
 struct Operand {
-    using C = Cfg<BM>;
+    using C = Block;
     static constexpr bool DMA = VEC && SIDE != COLS8;
-    static constexpr int PIECES = SIDE == COLS8 ? C::PIECES / 2 : C::PIECES;   // 16-byte pieces of memory a thread and stage
+    static constexpr int STAGE = BM * C::BK;                     // values of a stage
+    static constexpr int PIECES = SIDE == COLS8 ? BM / 64 : BM / 32;   // 16-byte pieces of memory a thread and stage
     static constexpr int KROWS = 512 / BM;   // k-rows of 1 KiB of a COLS stage
     const uint16_t *src;        // the tile's first row (ROWS) or column (COLS), k = 0
     const uint8_t *src8, *scales;
@@ -229,53 +224,40 @@ __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &t
     tn = within / rows;
 }
 
-template <int OP, bool BF16, int BM, int SA, int SB, bool VEC>
-__global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE, Cfg<BM>::WPE))) l16_tile_kernel(L16Params p)
+// A tile: C's rows m0 .. m_end - 1 (at most BM of them) and columns from n0 on, over klen of the
+// contracted axis from k_begin on, for group g.
+struct Job {
+    int g, m0, m_end, n0, k_begin, klen;
+    int64_t c_off;
+};
+
+// LDS of a tile: the rings, or the write-back's 64 rows of each wave.
+constexpr int kPitch = 64 + 4;   // floats of one of them
+template <int BM, int BN, int NA, int NB>
+constexpr int tile_lds()
 {
-    using C = Cfg<BM>;
-    constexpr int PITCH = 64 + 4;   // floats of a row of the write-back's LDS (64 rows a wave)
-    constexpr int NB = Operand<BF16, BM, SB, VEC>::DMA ? 3 : 2;   // buffers of B's stages
-    constexpr int TURN_BYTES = C::NW * 64 * PITCH * 4, RING_BYTES = (2 + NB) * C::STAGE * 2;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds_bytes[TURN_BYTES > RING_BYTES ? TURN_BYTES : RING_BYTES];
-    uint16_t (*ring_a)[C::STAGE] = reinterpret_cast<uint16_t (*)[C::STAGE]>(lds_bytes);
-    uint16_t (*ring_b)[C::STAGE] = ring_a + 2;
+    constexpr int ring = (NA * BM + NB * BN) * Block::BK * 2, turn = Block::NW * 64 * kPitch * 4;
+    return ring > turn ? ring : turn;
+}
+
+// Computes one. WPE: waves a SIMD, one (sums in accumulation registers) or two. NA, NB: buffers of
+// the operands' stages, two or (of those copied straight into LDS) three.
+template <int OP, bool BF16, int BM, int BN, int WPE, int NA, int NB, int SA, int SB, bool VEC>
+__device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uint8_t *lds_bytes)
+{
+    using C = Block;
+    constexpr int WTM = BM / 2, WTN = BN / 2, FM = WTM / 16, FN = WTN / 16;   // a wave's block of C
+    constexpr int PITCH = kPitch;
+    uint16_t (*ring_a)[BM * C::BK] = reinterpret_cast<uint16_t (*)[BM * C::BK]>(lds_bytes);
+    uint16_t (*ring_b)[BN * C::BK] = reinterpret_cast<uint16_t (*)[BN * C::BK]>(ring_a + NA);
 
     const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / C::WGN, wn = wave % C::WGN;
-
-    // the tile: C's rows [m0, m_end) and columns from n0, contracted range [k_begin, k_begin + klen)
-    int g = 0, m0, m_end, n0, k_begin = 0, klen = p.K;
-    int64_t c_off = 0;
-    if constexpr (OP == L16_DW) {
-        const int per = p.tiles_m * p.tiles_n, total = per * p.groups.n;
-        const int id = block_index(blockIdx.x, total);
-        g = id / per;
-        int tm, tn, end;
-        tile_at(id - g * per, p.tiles_m, p.tiles_n, tm, tn);
-        group_rows(p.groups, p.K, g, k_begin, end);
-        klen = end - k_begin;
-        m0 = tm * BM;
-        m_end = p.M;
-        n0 = tn * BM;
-        c_off = (int64_t)g * p.stride_c;
-    } else {
-        // rows of tiles of all groups; workgroups past the last have nothing to do
-        Chunk c{};
-        const int rows = find_chunk(p.groups, p.M, BM, -1, c), total = rows * p.tiles_n;
-        if ((int)blockIdx.x >= total)
-            return;
-        const int id = block_index(blockIdx.x, total);
-        find_chunk(p.groups, p.M, BM, id / p.tiles_n, c);
-        int tm, tn;
-        tile_at(id - c.group_first * p.tiles_n, cdiv(c.end - c.begin, BM), p.tiles_n, tm, tn);
-        g = c.group;
-        m0 = c.begin + tm * BM;
-        m_end = c.end;
-        n0 = tn * BM;
-    }
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / 2, wn = wave % 2;
+    const int g = job.g, m0 = job.m0, m_end = job.m_end, n0 = job.n0, k_begin = job.k_begin, klen = job.klen;
+    const int64_t c_off = job.c_off;
 
     Operand<BF16, BM, SA, VEC> a;
-    Operand<BF16, BM, SB, VEC> b;
+    Operand<BF16, BN, SB, VEC> b;
     a.ld = p.lda;
     a.lim = m_end - m0;
     a.klen = b.klen = klen;
@@ -292,37 +274,36 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         b.src = SB == ROWS ? w + (int64_t)n0 * p.ldb : w + (int64_t)k_begin * p.ldb + n0;
     }
 
-    f32x4 acc[C::FM][C::FN];
+    f32x4 acc[FM][FN];
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
+        for (int j = 0; j < FN; ++j)
             acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     a.start(tid);
     b.start(tid);
     const uint32_t base_a = lds_addr(ring_a), base_b = lds_addr(ring_b);
-    constexpr uint32_t STAGE_BYTES = C::STAGE * 2;
-    uint32_t at_a = base_a + a.lane_addr(wm * C::WTM, lane), at_b = base_b + b.lane_addr(wn * C::WTN, lane);
+    constexpr uint32_t A_BYTES = BM * C::BK * 2, B_BYTES = BN * C::BK * 2;   // of a stage
+    uint32_t at_a = base_a + a.lane_addr(wm * WTM, lane), at_b = base_b + b.lane_addr(wn * WTN, lane);
     // Step s of the stage in buffer buf: where its operands are read. (Opaque to the compiler, so
     // that the blocks are at constant offsets from it and nothing about it is kept in registers
     // over the loop.)
     auto step = [&](int bufa, int bufb, int s, uint32_t &xa, uint32_t &xb) __attribute__((always_inline)) {
-        xa = a.step_addr(at_a + bufa * STAGE_BYTES, s);
-        xb = b.step_addr(at_b + bufb * STAGE_BYTES, s);
+        xa = a.step_addr(at_a + bufa * A_BYTES, s);
+        xb = b.step_addr(at_b + bufb * B_BYTES, s);
         asm volatile("" : "+v"(xa), "+v"(xb));
     };
-    static_assert(C::FM == C::FN, "a block of each operand a row of products");
     // A stage is two steps. While a step multiplies, the next step's operands are read: its
     // blocks of B into a second set of registers, in the first rows, as the next step's first
     // row needs all of them; a block of A into the registers that a row of products has done
     // with (the last one at the step's own start). The barrier stands after the first rows of
     // a stage's last step, when every operand of the stage is in registers: it publishes the
     // next stage and frees this one's buffers. Then come the copies, in the first half of the
-    // rows up to the next barrier: A's of the stage after next into one of two buffers, which
-    // have the rest of that time to land in, and B's (weights, mostly, and from memory) of the
-    // stage after that into one of three, which fill the LDS and have a whole stage more.
-    // (With two for both, operands that no cache holds: 2048 x 11008 x 4096 226 us.)
+    // rows up to the next barrier: with two buffers those of the stage after next, which have
+    // the rest of that time to land in, with three those of the stage after that, which have a
+    // whole stage more. (256 x 256 fills the LDS with two of A's and three of B's, which are
+    // weights, mostly, and from memory; 2048 x 11008 x 4096 from memory 226 us with two for both.)
     // Pieces through registers go in any row, each followed by the load of its successor (those
     // of COLS8, which are fewer, in the first half too: a wait for copies is one for them).
     // Past the range's end come zeros, and are not used.
@@ -331,19 +312,26 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     // sixteen, so what stands between two MFMAs costs nothing up to three instructions; one
     // wave a SIMD has no other to fill a longer gap. Hence the operations are dealt out
     // singly among a row's MFMAs.
-    constexpr int F = C::FM, ROWS2 = 2 * F;       // rows of products of a step, of a stage
+    constexpr int F = FM, ROWS2 = 2 * F;          // rows of products of a step, of a stage
     constexpr int BR = F == 8 ? 2 : 1;            // rows of the last step before the barrier
     constexpr int AFTER = F - BR;                 // and after it
+    constexpr int PB = 2 * FN / FM;               // of B's blocks, and copies, a row of half the rows
     using OpA = decltype(a);
     using OpB = decltype(b);
-    static_assert(C::FM == C::FN && C::PIECES == F, "a piece of each operand in two rows");
+    static_assert(FN % (FM / 2) == 0 && (VEC || (FM == FN && NA == 2 && NB == 2)), "the operations' rows");
+    static_assert((NA == 2 || OpA::DMA) && (NB == 2 || OpB::DMA), "through registers there are two buffers");
     // The operations of row w after a barrier, A's and then B's.
     struct Window {
         static constexpr int a(int w) { return OpA::DMA ? (w < F / 2 ? 2 : 0) : w % 2 == 0 ? 2 : 0; }
         static constexpr int b(int w)
         {
-            return OpB::DMA ? (w >= F / 2 && w < F ? 2 : 0) : w % 2 == 0 || (OpB::PIECES < F && w >= F) ? 0 : 2;
+            if (OpB::DMA)
+                return w >= F / 2 && w < F ? PB : 0;
+            if (SB == COLS8 && w >= F)
+                return 0;
+            return (SB == COLS8 && OpB::PIECES == F) || w % 2 == 1 ? 2 : 0;
         }
+        static constexpr int b_piece(int w) { return SB == COLS8 && OpB::PIECES == F ? w : w / 2; }
         static constexpr int n(int w) { return a(w) + b(w); }
     };
     // Operation o of them: into buffers bufa and bufb; the stage that registers are loaded with
@@ -352,18 +340,18 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         constexpr int w = decltype(ww)::value, o = decltype(oo)::value, q = o - Window::a(w);
         if constexpr (q < 0) {
             if constexpr (OpA::DMA)
-                a.template copy<2 * w + o>(base_a + bufa * STAGE_BYTES, wave);
+                a.template copy<2 * w + o>(base_a + bufa * A_BYTES, wave);
             else if constexpr (o == 0)
                 a.template store<w / 2>(ring_a[bufa], tid);
             else
                 a.template load<w / 2>(k0, tid);
         } else {
             if constexpr (OpB::DMA)
-                b.template copy<2 * w - F + q>(base_b + bufb * STAGE_BYTES, wave);
+                b.template copy<(w - F / 2) * PB + q>(base_b + bufb * B_BYTES, wave);
             else if constexpr (q == 0)
-                b.template store<w / 2>(ring_b[bufb], tid);
+                b.template store<Window::b_piece(w)>(ring_b[bufb], tid);
             else
-                b.template load<w / 2>(k0, tid);
+                b.template load<Window::b_piece(w)>(k0, tid);
         }
     };
     // All of rows first .. first + count - 1's, at once.
@@ -380,76 +368,87 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         static_for<OpB::PIECES>([&](auto j) __attribute__((always_inline)) { b.template load<decltype(j)::value>(0, tid); });
     // stage 0, and what the rows after a barrier before it would have begun: copies in the order of
     // their need
+    // stage 0, and what the rows after a barrier before it would have begun: copies in the order of
+    // their need
     a.aim(0, tid);
     b.aim(0, tid);
     windows(std::integral_constant<int, 0>{}, std::integral_constant<int, ROWS2>{}, 0, 0, C::BK);
     a.aim(C::BK, tid);
     b.aim(C::BK, tid);
-    if constexpr (OpB::DMA) {
-        static_for<F>([&](auto j) __attribute__((always_inline)) { b.template copy<decltype(j)::value>(base_b + STAGE_BYTES, wave); });
+    if constexpr (NA == 3) {
+        static_for<OpA::PIECES>([&](auto j) __attribute__((always_inline)) { a.template copy<decltype(j)::value>(base_a + A_BYTES, wave); });
+        a.aim(2 * C::BK, tid);
+    }
+    if constexpr (NB == 3) {
+        static_for<OpB::PIECES>([&](auto j) __attribute__((always_inline)) { b.template copy<decltype(j)::value>(base_b + B_BYTES, wave); });
         b.aim(2 * C::BK, tid);
     }
-    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, AFTER>{}, 1, NB - 1, 2 * C::BK);
+    windows(std::integral_constant<int, 0>{}, std::integral_constant<int, AFTER>{}, NA - 1, NB - 1, 2 * C::BK);
+    // copies that may be on their way: at a barrier those past the next stage, in front of the first
+    // stage those past it
+    constexpr int LATER = (NA - 2) * OpA::PIECES + (NB - 2) * OpB::PIECES;
+    constexpr int BEGUN = LATER + OpA::PIECES + (AFTER - F / 2) * PB;
+    static_assert(BEGUN <= 63, "the counter's range");
     if constexpr (OpA::DMA && OpB::DMA)
-        __builtin_amdgcn_s_waitcnt(LL_VMCNT(2 * F + 2 * (AFTER - F / 2)));   // (those of the stages after the first)
+        __builtin_amdgcn_s_waitcnt(LL_VMCNT(BEGUN));
     else if constexpr (OpA::DMA || OpB::DMA)
         __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    f16x8 fa[F], fb[2][F];
+    f16x8 fa[FM], fb[2][FN];
     {
         uint32_t xa, xb;
         step(0, 0, 0, xa, xb);
 #pragma unroll
-        for (int i = 0; i < F; ++i) {
-            if (i + 1 < F)
-                fa[i] = a.read(xa, i);
-            fb[0][i] = b.read(xb, i);
-        }
+        for (int i = 0; i + 1 < FM; ++i)
+            fa[i] = a.read(xa, i);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            fb[0][j] = b.read(xb, j);
     }
     // Row i of the products on step s's operands, with op(0), .., op(n - 1) dealt out among its
     // MFMAs. Rows alternate in column order: neighbouring MFMAs share an operand, and the
     // chip, power-limited on 16-bit products, keeps a higher clock.
-    auto row = [&](auto ii, const f16x8 (&b_)[C::FN], auto count, auto op) __attribute__((always_inline)) {
+    auto row = [&](auto ii, const f16x8 (&b_)[FN], auto count, auto op) __attribute__((always_inline)) {
         constexpr int i = decltype(ii)::value, n = decltype(count)::value;
-        static_for<C::FN>([&](auto jj) __attribute__((always_inline)) {
-            constexpr int q = decltype(jj)::value, j = (i & 1) ? C::FN - 1 - q : q;
-            if constexpr (C::WPE == 1)
+        static_for<FN>([&](auto jj) __attribute__((always_inline)) {
+            constexpr int q = decltype(jj)::value, j = (i & 1) ? FN - 1 - q : q;
+            if constexpr (WPE == 1)
                 mma_acc<BF16>(b_[j], fa[i], acc[i][j]);
             else
                 acc[i][j] = mma<BF16>(b_[j], fa[i], acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
-            constexpr int lo = q * n / C::FN, hi = (q + 1) * n / C::FN;
+            constexpr int lo = q * n / FN, hi = (q + 1) * n / FN;
             static_for<hi - lo>([&](auto k) __attribute__((always_inline)) { op(std::integral_constant<int, lo + decltype(k)::value>{}); });
             __builtin_amdgcn_sched_barrier(0);
         });
     };
-    if constexpr (C::WPE == 1)
+    if constexpr (WPE == 1)
         settle();
-    int bufb = 0, nextb = 1, lastb = NB - 1;   // B's buffers of stages kt, kt + 1, and kt + 2 (kt + 1 where there are two)
+    // the buffers of stages kt, kt + 1, and of the last one that is on its way
+    int bufa = 0, nexta = 1, lasta = NA - 1, bufb = 0, nextb = 1, lastb = NB - 1;
     for (int kt = 0; kt < nk; ++kt) {
-        const int buf = kt & 1;
         uint32_t xa0, xa1, xb1, unused;
-        step(buf, bufb, 0, xa0, unused);
-        step(buf, bufb, 1, xa1, xb1);
+        step(bufa, bufb, 0, xa0, unused);
+        step(bufa, bufb, 1, xa1, xb1);
         __builtin_amdgcn_s_setprio(1);
         static_for<F>([&](auto ii) __attribute__((always_inline)) {
-            // two blocks of B in the first rows, and one of A; the last rows have the operations
+            // blocks of B in the first rows, and one of A; the last rows have the operations
             // of those before the barrier too
-            constexpr int i = decltype(ii)::value, nb = 2 * i < F ? 2 : 0, w = AFTER + i, w2 = w + BR;
+            constexpr int i = decltype(ii)::value, nb = 2 * i < F ? PB : 0, w = AFTER + i, w2 = w + BR;
             constexpr int n = Window::n(w), n2 = i >= F - BR ? Window::n(w2) : 0;
             row(ii, fb[0], std::integral_constant<int, nb + 1 + n + n2>{}, [&](auto k) __attribute__((always_inline)) {
                 constexpr int o = decltype(k)::value, q = o - nb - 1;
                 if constexpr (o < nb) {
-                    fb[1][2 * i + o] = b.read(xb1, 2 * i + o);
+                    fb[1][PB * i + o] = b.read(xb1, PB * i + o);
                 } else if constexpr (q < 0) {
                     if constexpr (i == 0)
                         fa[F - 1] = a.read(xa0, F - 1);
                     else
                         fa[i - 1] = a.read(xa1, i - 1);
                 } else if constexpr (q < n) {
-                    window(std::integral_constant<int, w>{}, std::integral_constant<int, q>{}, buf ^ 1, lastb, (kt + 2) * C::BK);
+                    window(std::integral_constant<int, w>{}, std::integral_constant<int, q>{}, lasta, lastb, (kt + 2) * C::BK);
                 } else {
-                    window(std::integral_constant<int, w2>{}, std::integral_constant<int, q - n>{}, buf ^ 1, lastb, (kt + 2) * C::BK);
+                    window(std::integral_constant<int, w2>{}, std::integral_constant<int, q - n>{}, lasta, lastb, (kt + 2) * C::BK);
                 }
             });
         });
@@ -457,9 +456,9 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
         static_for<F>([&](auto ii) __attribute__((always_inline)) {
             constexpr int i = decltype(ii)::value, after = i - BR;   // rows since the barrier
             if constexpr (after == 0) {
-                // stage kt + 1 has landed; B's copies of the one after may be on their way
+                // stage kt + 1 has landed
                 if constexpr (OpA::DMA && OpB::DMA)
-                    __builtin_amdgcn_s_waitcnt(LL_VMCNT(F));
+                    __builtin_amdgcn_s_waitcnt(LL_VMCNT(LATER));
                 else if constexpr (OpA::DMA || OpB::DMA)
                     __builtin_amdgcn_s_waitcnt(LL_VMCNT(0));
                 asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -470,35 +469,35 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
                     if constexpr (i == 0 && o == 0)
                         fa[F - 1] = a.read(xa1, F - 1);
                     else if constexpr (i == 0 && o == 1)
-                        step(buf ^ 1, nextb, 0, xan, xbn);
+                        step(nexta, nextb, 0, xan, xbn);
                     else if constexpr (i == BR - 1 && o == 2)
-                        a.aim((kt + 2) * C::BK, tid);
+                        a.aim((kt + NA) * C::BK, tid);
                     else if constexpr (i == BR - 1 && o == 3)
                         b.aim((kt + NB) * C::BK, tid);
                 });
             } else {
                 // (after the last stage what is read here is of no use)
-                constexpr int nb = 2 * after < F ? 2 : 0, na = after < BR - 1 ? 2 : 1;   // (a block of A of the rows before the barrier)
+                constexpr int nb = 2 * after < F ? PB : 0, na = after < BR - 1 ? 2 : 1;   // (a block of A of the rows before the barrier)
                 row(ii, fb[1], std::integral_constant<int, nb + na + Window::n(after)>{}, [&](auto k) __attribute__((always_inline)) {
                     constexpr int o = decltype(k)::value, q = o - nb - na;
                     if constexpr (o < nb)
-                        fb[0][2 * after + o] = b.read(xbn, 2 * after + o);
+                        fb[0][PB * after + o] = b.read(xbn, PB * after + o);
                     else if constexpr (o == nb)
                         fa[i - 1] = a.read(xan, i - 1);
                     else if constexpr (q < 0)
                         fa[after] = a.read(xan, after);
                     else
-                        window(std::integral_constant<int, after>{}, std::integral_constant<int, q>{}, buf, bufb, (kt + 3) * C::BK);
+                        window(std::integral_constant<int, after>{}, std::integral_constant<int, q>{}, bufa, bufb, (kt + 3) * C::BK);
                 });
             }
         });
         __builtin_amdgcn_s_setprio(0);
-        const int done = bufb;
-        bufb = nextb;
-        nextb = NB == 3 ? lastb : done;
-        lastb = NB == 3 ? done : nextb;
+        const int donea = bufa, doneb = bufb;
+        bufa = nexta, bufb = nextb;
+        nexta = NA == 3 ? lasta : donea, nextb = NB == 3 ? lastb : doneb;
+        lasta = NA == 3 ? donea : nexta, lastb = NB == 3 ? doneb : nextb;
     }
-    if constexpr (C::WPE == 1)
+    if constexpr (WPE == 1)
         settle();
 
     // The write-back, 64 x 64 of the wave's block at a time through its own part of the LDS,
@@ -512,7 +511,7 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     const int rl = lane >> 3, cl = (lane & 7) * 8;
     const void *more = OP == L16_FWD ? p.R : p.beta != 0.0f ? p.C : nullptr;
     const int64_t more_ld = OP == L16_FWD ? p.ldr : p.ldc;
-    constexpr int QN = C::WTN / 64, QUARTERS = C::WTM / 64 * QN;
+    constexpr int QN = WTN / 64, QUARTERS = WTM / 64 * QN;
 #pragma unroll 1
     for (int quarter = 0; quarter < QUARTERS; ++quarter) {
         static_for<QUARTERS>([&](auto qq) __attribute__((always_inline)) {
@@ -527,8 +526,8 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
                 asm volatile("; quarter %0" ::"n"(Q) : "memory");   // (merged branches would index acc, in memory)
             }
         });
-        const int col = n0 + wn * C::WTN + 64 * (quarter % QN) + cl, n = p.N - col;
-        const int row0 = m0 + wm * C::WTM + 64 * (quarter / QN) + rl;
+        const int col = n0 + wn * WTN + 64 * (quarter % QN) + cl, n = p.N - col;
+        const int row0 = m0 + wm * WTM + 64 * (quarter / QN) + rl;
         float bias[8];
         if constexpr (OP == L16_FWD)
             load_row<LL_TYPE_F32, 8>(p.bias + (int64_t)g * p.N + col, p.bias != nullptr ? n : 0, bias);
@@ -572,8 +571,8 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
             }
         };
         // 32 rows at a time where all of them and the 64 columns exist, else eight
-        const int first = m0 + wm * C::WTM + 64 * (quarter / QN);   // of the 64
-        const bool whole_cols = n0 + wn * C::WTN + 64 * (quarter % QN) + 64 <= p.N;
+        const int first = m0 + wm * WTM + 64 * (quarter / QN);   // of the 64
+        const bool whole_cols = n0 + wn * WTN + 64 * (quarter % QN) + 64 <= p.N;
 #pragma unroll 1
         for (int q = 0; q < 8 && first + 8 * q < m_end;) {
             if (whole_cols && first + 8 * q + 32 <= m_end) {
@@ -588,41 +587,184 @@ __global__ void __launch_bounds__(Cfg<BM>::NT) __attribute__((amdgpu_waves_per_e
     }
 }
 
-// ---- launches -------------------------------------------------------------------
+// ---- kernels -----------------------------------------------------------------------
 
-// Whether so many tiles of 256 x 256 (one a CU) take less time than so many of 128 x 128 (two
-// a CU, 0.88 of the large ones' rate).
-inline bool prefer_256(int64_t t256, int64_t t128, int cus)
+// One 128 x 128 tile a workgroup, two workgroups a CU: products that do not fill the CUs with
+// larger ones, and rows off 16 bytes.
+template <int OP, bool BF16, int SA, int SB, bool VEC>
+__global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) l16_small_kernel(L16Params p)
 {
-    const double large = (double)((t256 + cus - 1) / cus), small = (double)((t128 + 2 * cus - 1) / (2 * cus));
-    return large <= small * 0.5 / 0.88;
+    constexpr int BM = 128, NB = Operand<BF16, BM, SB, VEC>::DMA ? 3 : 2;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[tile_lds<BM, BM, 2, NB>()];
+    Job job{0, 0, p.M, 0, 0, p.K, 0};
+    int tm, tn;
+    if constexpr (OP == L16_DW) {
+        const int per = p.tiles_m * p.tiles_n, id = block_index(blockIdx.x, per * p.groups.n);
+        job.g = id / per;
+        tile_at(id - job.g * per, p.tiles_m, p.tiles_n, tm, tn);
+        group_rows(p.groups, p.K, job.g, job.k_begin, job.klen);
+        job.klen -= job.k_begin;
+        job.m0 = tm * BM;
+        job.c_off = (int64_t)job.g * p.stride_c;
+    } else {
+        // rows of tiles of all groups; workgroups past the last have nothing to do
+        Chunk c{};
+        const int total = find_chunk(p.groups, p.M, BM, -1, c) * p.tiles_n;
+        if ((int)blockIdx.x >= total)
+            return;
+        const int id = block_index(blockIdx.x, total);
+        find_chunk(p.groups, p.M, BM, id / p.tiles_n, c);
+        tile_at(id - c.group_first * p.tiles_n, cdiv(c.end - c.begin, BM), p.tiles_n, tm, tn);
+        job.g = c.group;
+        job.m0 = c.begin + tm * BM;
+        job.m_end = c.end;
+    }
+    job.n0 = tn * BM;
+    l16_tile<OP, BF16, BM, BM, 2, 2, NB, SA, SB, VEC>(p, job, lds);
 }
 
-// The products whose groups are of C's rows.
-template <int OP, bool BF16, int BM, int SB, bool VEC>
-hipError_t launch_rows_bm(L16Params p, hipStream_t s)
+// What is left after the rounds in which every CU has a 256 x 256 tile, in tiles of 256 x 256, of
+// 128 x 256 or of 128 x 128, whichever takes the fewest rounds' time: measured, a round of the
+// smaller ones takes 0.58 and 0.41 of a round of the large. `large` of them are left, and `halves`
+// pieces of 128 x 256 beside them.
+__host__ __device__ inline int piece_split(int64_t large, int64_t halves, int cus, bool may_cut, float &cost)
 {
-    p.tiles_n = cdiv(p.N, BM);
-    // every group may end inside a tile
-    const int64_t rows = p.groups.offsets == nullptr ? cdiv(p.M, BM)
-                                                     : (int64_t)(p.M / BM) + (p.groups.n < p.M ? p.groups.n : p.M);
-    const int64_t tiles = rows * p.tiles_n;
-    if (tiles > max_grid_x(Cfg<BM>::NT))
-        return hipErrorInvalidValue;
-    hipLaunchKernelGGL((l16_tile_kernel<OP, BF16, BM, ROWS, SB, VEC>), dim3((unsigned)tiles), dim3(Cfg<BM>::NT), 0, s, p);
+    const auto rounds = [cus](int64_t n) { return (float)((n + cus - 1) / cus); };
+    const float c1 = rounds(large) + 0.58f * rounds(halves), c2 = 0.58f * rounds(2 * large + halves),
+                c4 = 0.41f * rounds(4 * large + 2 * halves);
+    const bool one = !may_cut || (c1 <= c2 && c1 <= c4);
+    cost = one ? c1 : c2 <= c4 ? c2 : c4;
+    return one ? 1 : c2 <= c4 ? 2 : 4;
+}
+
+// Tiles of 256 x 256, one a CU, as many workgroups as there are CUs, each of which takes every
+// gridDim.x-th tile. A group's last rows are a tile of 128 rows where no more are left, and what
+// does not fill a round is cut up (piece_split).
+template <int OP, bool BF16, int SA, int SB>
+__global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(1, 1))) l16_large_kernel(L16Params p)
+{
+    constexpr bool DMA_B = Operand<BF16, 256, SB, true>::DMA;
+    constexpr int NB = DMA_B ? 3 : 2;
+    constexpr int large = tile_lds<256, 256, 2, NB>(), half = tile_lds<128, 256, 3, NB>();
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[large > half ? large : half];
+    const int cus = (int)gridDim.x;
+    const auto count_large = [](int rows) { return (rows + 127) / 256; };
+    const auto count_half = [](int rows) { return (rows & 255) != 0 && (rows & 255) <= 128 ? 1 : 0; };
+    int n_large, n_half = 0;
+    if constexpr (OP == L16_DW) {
+        n_large = p.tiles_m * p.tiles_n * p.groups.n;
+    } else {
+        Chunk c{};
+        n_large = find_chunk_by(p.groups, p.M, count_large, -1, c) * p.tiles_n;
+        n_half = find_chunk_by(p.groups, p.M, count_half, -1, c) * p.tiles_n;
+    }
+    float cost;
+    const int left = n_large % cus, split = piece_split(left, n_half, cus, DMA_B, cost);
+    const int whole = split == 1 ? n_large : n_large - left;   // in one piece
+    const int pieces = (split == 1 ? n_half : 2 * left + n_half) * (split == 4 ? 2 : 1), total = whole + pieces;
+    for (int round = 0; round < total; round += cus) {
+        const int here = min(cus, total - round);
+        if ((int)blockIdx.x >= here)
+            break;
+        const int id = round + block_index(blockIdx.x, here);
+        // the tile, and for a piece its half (of the rows) and quarter (of the columns)
+        const int piece = id - whole, q = split == 4 ? piece / 2 : piece, cut = split == 1 ? 0 : 2 * left;
+        const int tile = piece < 0 ? id : q < cut ? whole + q / 2 : -1;
+        Job job{0, 0, p.M, 0, 0, p.K, 0};
+        int tm = 0, tn = 0;
+        if constexpr (OP == L16_DW) {
+            const int per = p.tiles_m * p.tiles_n;
+            job.g = tile / per;
+            tile_at(tile - job.g * per, p.tiles_m, p.tiles_n, tm, tn);
+            group_rows(p.groups, p.K, job.g, job.k_begin, job.klen);
+            job.klen -= job.k_begin;
+            job.c_off = (int64_t)job.g * p.stride_c;
+            job.m0 = tm * 256;
+        } else {
+            Chunk c{};
+            if (tile >= 0) {
+                find_chunk_by(p.groups, p.M, count_large, tile / p.tiles_n, c);
+                tile_at(tile - c.group_first * p.tiles_n, count_large(c.end - c.begin), p.tiles_n, tm, tn);
+                job.m0 = c.begin + tm * 256;
+            } else {
+                find_chunk_by(p.groups, p.M, count_half, (q - cut) / p.tiles_n, c);
+                tn = (q - cut) % p.tiles_n;
+                job.m0 = c.end - ((c.end - c.begin) & 255);
+            }
+            job.g = c.group;
+            job.m_end = c.end;
+        }
+        job.n0 = tn * 256;
+        if (piece >= 0) {
+            if (tile >= 0)
+                job.m0 += 128 * (q & 1);
+            if (split == 4)
+                job.n0 += 128 * (piece & 1);
+            if (job.m0 >= job.m_end || job.n0 >= p.N)
+                continue;
+        }
+        __syncthreads();   // nobody reads the tile before this one's rows in LDS any more
+        if (piece < 0)
+            l16_tile<OP, BF16, 256, 256, 1, 2, NB, SA, SB, true>(p, job, lds);
+        else if constexpr (DMA_B) {   // (codes decoded on the way take too many registers for three forms)
+            if (split != 4)
+                l16_tile<OP, BF16, 128, 256, 1, 3, NB, SA, SB, true>(p, job, lds);
+            else
+                l16_tile<OP, BF16, 128, 128, 1, 3, NB, SA, SB, true>(p, job, lds);
+        }
+    }
+}
+
+// ---- launches -----------------------------------------------------------------------
+
+// Whether large tiles take less time: n_large and n_half of them and of their halves, against
+// n_small of 128 x 128. Two small ones a CU have 0.88 of the large ones' rate; a tile's beginning
+// and end, under the other workgroup's products or not, are four and nine stages' time.
+inline bool prefer_large(int64_t n_large, int64_t n_half, int64_t n_small, int k, int cus, bool may_cut = true)
+{
+    float rest;
+    piece_split(n_large % cus, n_half, cus, may_cut, rest);
+    const float stages = (float)cdiv(k, Block::BK);
+    return ((float)(n_large / cus) + rest) * (stages + 9.0f) <=
+           (float)((n_small + 2 * cus - 1) / (2 * cus)) * (0.5f / 0.88f) * (stages + 4.0f);
+}
+
+template <int OP, bool BF16, int SA, int SB>
+hipError_t launch_large(L16Params p, int cus, hipStream_t s)
+{
+    p.tiles_m = cdiv(p.M, 256);
+    p.tiles_n = cdiv(p.N, 256);
+    hipLaunchKernelGGL((l16_large_kernel<OP, BF16, SA, SB>), dim3((unsigned)cus), dim3(Block::NT), 0, s, p);
     return hipGetLastError();
 }
 
+template <int OP, bool BF16, int SA, int SB, bool VEC>
+hipError_t launch_small(L16Params p, int64_t rows, hipStream_t s)
+{
+    p.tiles_m = cdiv(p.M, 128);
+    p.tiles_n = cdiv(p.N, 128);
+    const int64_t tiles = rows * p.tiles_n;
+    if (tiles > max_grid_x(Block::NT))
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((l16_small_kernel<OP, BF16, SA, SB, VEC>), dim3((unsigned)tiles), dim3(Block::NT), 0, s, p);
+    return hipGetLastError();
+}
+
+// The products whose groups are of C's rows. (Every group may end inside a tile.)
 template <int OP, bool BF16, int SB>
 hipError_t launch_rows(const L16Params &p, bool vec, int cus, hipStream_t s)
 {
+    const int g = p.groups.n < p.M ? p.groups.n : p.M;
+    const int64_t rows = p.groups.offsets == nullptr ? cdiv(p.M, 128) : (int64_t)(p.M / 128) + g;
     if (!vec)
-        return launch_rows_bm<OP, BF16, 128, SB, false>(p, s);
-    // rows of tiles, the groups taken as equally long
-    const int g = p.groups.n < p.M ? p.groups.n : p.M, each = cdiv(p.M, g);
-    return prefer_256((int64_t)g * cdiv(each, 256) * cdiv(p.N, 256), (int64_t)g * cdiv(each, 128) * cdiv(p.N, 128), cus)
-               ? launch_rows_bm<OP, BF16, 256, SB, true>(p, s)
-               : launch_rows_bm<OP, BF16, 128, SB, true>(p, s);
+        return launch_small<OP, BF16, ROWS, SB, false>(p, rows, s);
+    // the groups taken as equally long; as many large tiles as fit a launch's 32 bits
+    const int each = cdiv(p.M, g), tn = cdiv(p.N, 256);
+    const int64_t n_large = (int64_t)g * ((each + 127) / 256) * tn, n_half = (each & 255) != 0 && (each & 255) <= 128 ? (int64_t)g * tn : 0;
+    if (((int64_t)(p.M / 256) + g) * tn < (1 << 29) &&
+        prefer_large(n_large, n_half, (int64_t)g * cdiv(each, 128) * cdiv(p.N, 128), p.K, cus))
+        return launch_large<OP, BF16, ROWS, SB>(p, cus, s);
+    return launch_small<OP, BF16, ROWS, SB, true>(p, rows, s);
 }
 
 }  // namespace l16
