@@ -273,7 +273,10 @@ int linear16_grad_weight(int M, int N, int K, int type, const uint16_t *DZ, int 
     p.M = N, p.N = K, p.K = M;
     p.ctype = wtype;
     p.beta = beta;
-    const bool vec = dz.vec(N) && (XQ != nullptr || x.vec(K));
+    // codes: rows on 16 bytes (the last piece may be short)
+    const bool vec = dz.vec(N) && (XQ != nullptr ? aligned(XQ, 16) && ldxq % 16 == 0 && xq.ld < (int64_t)1 << 21 &&
+                                                       ldxs < (int64_t)1 << 21
+                                                 : x.vec(K));
     return status(launch_l16_dw(type == LL_TYPE_BF16, p, vec, dev.cus, static_cast<hipStream_t>(stream)));
 }
 

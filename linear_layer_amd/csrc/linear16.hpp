@@ -292,7 +292,8 @@ __device__ __forceinline__ uint32_t mx8_encode4(float v0, float v1, float v2, fl
     return s == 255u ? 0u : __builtin_bit_cast(uint32_t, r);
 }
 
-// The values of four codes under scale byte s.
+// The values of four codes under scale byte s (255: NaN, which the conversion makes of its
+// infinite scale).
 __device__ __forceinline__ void mx8_decode4(uint32_t c, uint32_t s, float *v)
 {
     typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -300,8 +301,29 @@ __device__ __forceinline__ void mx8_decode4(uint32_t c, uint32_t s, float *v)
     const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, sc, false);
     const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, sc, true);
     v[0] = a[0], v[1] = a[1], v[2] = b[0], v[3] = b[1];
-    if (s == 255u)
-        v[0] = v[1] = v[2] = v[3] = __builtin_nanf("");
+}
+
+// The same in 16 bits, two a word, as a factor of a product: what rounding to 8 bits carried past
+// binary16's range (65504 becomes 65536, under a scale of 2^8 or more) is its largest value.
+template <bool BF16>
+__device__ __forceinline__ void mx8_decode4(uint32_t c, uint32_t s, uint32_t &w0, uint32_t &w1)
+{
+    const float sc = __builtin_bit_cast(float, s << 23);
+    if constexpr (BF16) {
+        w0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc, false));
+        w1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, sc, true));
+    } else {
+        w0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, sc, false));
+        w1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(c, sc, true));
+        if (s >= 135u) {
+            const auto held = [](uint32_t w) {
+                w = (w & 0x7fffu) == 0x7c00u ? w - 1u : w;
+                return (w & 0x7fff0000u) == 0x7c000000u ? w - 0x10000u : w;
+            };
+            w0 = held(w0);
+            w1 = held(w1);
+        }
+    }
 }
 
 // The largest of v over groups of four lanes.

@@ -71,6 +71,7 @@ struct Operand {
     const uint8_t *src8, *scales;
     int64_t ld, lds;
     int lim, klen, col0;
+    __amdgpu_buffer_rsrc_t codes, scale_bytes;   // (COLS8)
     uint32_t off[2], cur[2];    // offset of piece 0, and of piece 1 where its swizzle is another; in the stage aimed at
     u32x4 buf;
     u32x4 reg[DMA ? 1 : PIECES];
@@ -101,6 +102,10 @@ struct Operand {
                 const int s = v * C::NT + tid;
                 off[v] = (uint32_t)slot_row(s) * (uint32_t)(2 * ld) + 2 * slot_col(s);
             }
+        } else if constexpr (VEC && SIDE == COLS8) {   // of codes, and of scales
+            const int k = tid / (BM / 16), col = tid % (BM / 16) * 16;
+            off[0] = (uint32_t)k * (uint32_t)ld + col;
+            off[1] = (uint32_t)k * (uint32_t)lds + ((col0 + col) >> 5);
         }
     }
     // The pieces loaded from now on are of the stage at k0 (past the range: zeros).
@@ -114,6 +119,14 @@ struct Operand {
 #pragma unroll
             for (int v = 0; v < SETS; ++v)
                 cur[v] = SIDE == ROWS && slot_col(v * C::NT + tid) >= left ? kPastEnd : off[v];
+        } else if constexpr (VEC && SIDE == COLS8) {
+            // (codes past a row's end are the next row's, or padding: of columns that are not stored)
+            const int left = min(klen - k0, C::BK), n = min(lim, BM);
+            const int last = (col0 + n - 1) >> 5;   // scale of the last column
+            codes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(src8 + (int64_t)k0 * ld), 0,
+                                                      left <= 0 ? 0 : (left - 1) * (int)ld + n, 0x00020000);
+            scale_bytes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(scales + (int64_t)k0 * lds), 0,
+                                                            left <= 0 ? 0 : (left - 1) * (int)lds + last + 1, 0x00020000);
         }
     }
     // Copy J of this wave of the stage aimed at to the stage at LDS address `base`.
@@ -127,7 +140,11 @@ struct Operand {
     template <int J>
     __device__ __forceinline__ void load(int k0, int tid)
     {
-        if constexpr (SIDE == COLS8) {
+        if constexpr (SIDE == COLS8 && VEC) {
+            constexpr int STEP = J * (C::NT / (BM / 16));   // k-rows from piece 0's
+            reg[J] = __builtin_amdgcn_raw_buffer_load_b128(codes, off[0] + STEP * (uint32_t)ld, 0, 0);
+            sc[J] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(scale_bytes, off[1] + STEP * (uint32_t)lds, 0, 0);
+        } else if constexpr (SIDE == COLS8) {
             reg[J] = u32x4{0u, 0u, 0u, 0u};
             sc[J] = 0;
             const int c = J * C::NT + tid, k = k0 + c / (BM / 16), col = c % (BM / 16) * 16;
@@ -158,29 +175,16 @@ struct Operand {
             }
         }
     }
-    template <int J>
+    // (COLS8: half H of it, eight codes.)
+    template <int J, int H = 0>
     __device__ __forceinline__ void store(uint16_t *stage, int tid) const
     {
         if constexpr (SIDE == COLS8) {
             const int c = J * C::NT + tid, k = c / (BM / 16), u = c % (BM / 16) ^ cols_swz(k);
-            u32x4 w[2];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float v[4];
-                mx8_decode4(reg[J][q], sc[J], v);
-                if constexpr (!BF16) {
-                    // a value that rounding to 8 bits carried past binary16's range (65504
-                    // becomes 65536) is its largest
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        v[e] = __builtin_fabsf(v[e]) > 65504.0f ? __builtin_copysignf(65504.0f, v[e]) : v[e];
-                }
-                w[q / 2][2 * (q & 1)] = (uint32_t)from_f32<kType16<BF16>>(v[0]) | (uint32_t)from_f32<kType16<BF16>>(v[1]) << 16;
-                w[q / 2][2 * (q & 1) + 1] = (uint32_t)from_f32<kType16<BF16>>(v[2]) | (uint32_t)from_f32<kType16<BF16>>(v[3]) << 16;
-            }
-            u32x4 *dst = reinterpret_cast<u32x4 *>(stage + k * BM + u * 16);
-            dst[0] = w[0];
-            dst[1] = w[1];
+            uint32_t w[4];
+            mx8_decode4<BF16>(reg[J][2 * H], sc[J], w[0], w[1]);
+            mx8_decode4<BF16>(reg[J][2 * H + 1], sc[J], w[2], w[3]);
+            *reinterpret_cast<u32x4 *>(stage + k * BM + u * 16 + 8 * H) = u32x4{w[0], w[1], w[2], w[3]};
         } else {
             *reinterpret_cast<u32x4 *>(stage + (J * C::NT + tid) * 8) = reg[J];
         }
@@ -329,7 +333,7 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
                 return w >= F / 2 && w < F ? PB : 0;
             if (SB == COLS8 && w >= F)
                 return 0;
-            return (SB == COLS8 && OpB::PIECES == F) || w % 2 == 1 ? 2 : 0;
+            return (SB == COLS8 && OpB::PIECES == F) || w % 2 == 1 ? (SB == COLS8 ? 3 : 2) : 0;
         }
         static constexpr int b_piece(int w) { return SB == COLS8 && OpB::PIECES == F ? w : w / 2; }
         static constexpr int n(int w) { return a(w) + b(w); }
@@ -348,8 +352,8 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
         } else {
             if constexpr (OpB::DMA)
                 b.template copy<(w - F / 2) * PB + q>(base_b + bufb * B_BYTES, wave);
-            else if constexpr (q == 0)
-                b.template store<Window::b_piece(w)>(ring_b[bufb], tid);
+            else if constexpr (q + 1 < Window::b(w))
+                b.template store<Window::b_piece(w), q>(ring_b[bufb], tid);
             else
                 b.template load<Window::b_piece(w)>(k0, tid);
         }
@@ -364,17 +368,17 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
     const int nk = cdiv(klen, C::BK);
     if constexpr (!OpA::DMA)
         static_for<OpA::PIECES>([&](auto j) __attribute__((always_inline)) { a.template load<decltype(j)::value>(0, tid); });
+    constexpr int AHEAD = OpB::DMA ? 0 : 1;   // stages that registers are ahead of copies
+    b.aim(0, tid);
     if constexpr (!OpB::DMA)
         static_for<OpB::PIECES>([&](auto j) __attribute__((always_inline)) { b.template load<decltype(j)::value>(0, tid); });
     // stage 0, and what the rows after a barrier before it would have begun: copies in the order of
     // their need
-    // stage 0, and what the rows after a barrier before it would have begun: copies in the order of
-    // their need
     a.aim(0, tid);
-    b.aim(0, tid);
+    b.aim(AHEAD * C::BK, tid);
     windows(std::integral_constant<int, 0>{}, std::integral_constant<int, ROWS2>{}, 0, 0, C::BK);
     a.aim(C::BK, tid);
-    b.aim(C::BK, tid);
+    b.aim((1 + AHEAD) * C::BK, tid);
     if constexpr (NA == 3) {
         static_for<OpA::PIECES>([&](auto j) __attribute__((always_inline)) { a.template copy<decltype(j)::value>(base_a + A_BYTES, wave); });
         a.aim(2 * C::BK, tid);
@@ -473,7 +477,7 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
                     else if constexpr (i == BR - 1 && o == 2)
                         a.aim((kt + NA) * C::BK, tid);
                     else if constexpr (i == BR - 1 && o == 3)
-                        b.aim((kt + NB) * C::BK, tid);
+                        b.aim((kt + NB + AHEAD) * C::BK, tid);
                 });
             } else {
                 // (after the last stage what is read here is of no use)
@@ -666,7 +670,9 @@ __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(
         const int here = min(cus, total - round);
         if ((int)blockIdx.x >= here)
             break;
-        const int id = round + block_index(blockIdx.x, here);
+        // (another part of each round for a CU: groups' lengths, which weight gradients run over,
+        // even out; an XCD's tiles stay together)
+        const int id = round + (block_index(blockIdx.x, here) + round / cus * (3 * cus / 8)) % here;
         // the tile, and for a piece its half (of the rows) and quarter (of the columns)
         const int piece = id - whole, q = split == 4 ? piece / 2 : piece, cut = split == 1 ? 0 : 2 * left;
         const int tile = piece < 0 ? id : q < cut ? whole + q / 2 : -1;
