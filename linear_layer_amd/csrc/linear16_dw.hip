@@ -13,7 +13,7 @@ static hipError_t launch_dw(const L16Params &p, bool vec, int cus, hipStream_t s
         return launch_small<L16_DW, BF16, COLS, SB, false>(p, rows, s);
     const int64_t n_large = n * cdiv(p.M, 256) * cdiv(p.N, 256);
     const int each = p.K > n ? cdiv(p.K, (int)n) : 1;   // rows of a group
-    if (n_large < (1 << 29) && prefer_large(n_large, 0, rows * cdiv(p.N, 128), each, cus, SB != COLS8))
+    if (n_large < (1 << 29) && prefer_large(n_large, 0, rows * cdiv(p.N, 128), each, cus))
         return launch_large<L16_DW, BF16, COLS, SB>(p, cus, s);
     return launch_small<L16_DW, BF16, COLS, SB, true>(p, rows, s);
 }

@@ -47,15 +47,17 @@ constexpr uint32_t kPastEnd = 0x80000000u;   // past the end of every buffer her
 // byte lds_base + 16 * lane, zeros where they lie past its end. Inline assembly, so that the
 // compiler does not take it for an LDS store that every LDS read must wait for; the caller
 // waits for the copies before the barrier that publishes them. The compiler's hazard checks
-// do not look inside: M0 may be used one wait state after its write. (Four more, for a
-// descriptor that v_readfirstlane might have written just before, would cost the matrix
-// cores as much as all the copies; descriptors here are made by scalar instructions.)
+// do not look inside: M0 may be used a wait state after its write, and a descriptor that a
+// vector instruction wrote (v_readlane, of a spilled one) by a load only five later, but by a
+// scalar instruction at once. Hence the two moves, which are the wait for M0 too.
 __device__ __forceinline__ void lds_buffer_16(const u32x4 &buffer, uint32_t off, uint32_t lds_base)
 {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    const uint64_t lo = (uint64_t)buffer[1] << 32 | buffer[0], hi = (uint64_t)buffer[3] << 32 | buffer[2];
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 s[92:93], %2\n\ts_mov_b64 s[94:95], %3\n\t"
+                 "buffer_load_dwordx4 %1, s[92:95], 0 offen lds"
                  :
-                 : "s"(lds_base), "v"(off), "s"(buffer)
-                 : "memory", "m0");
+                 : "s"(lds_base), "v"(off), "s"(lo), "s"(hi)
+                 : "memory", "m0", "s92", "s93", "s94", "s95");
 }
 
 // Eight values of a matrix of LL_TYPE_F32 or the 16-bit type, the first n of them inside it.

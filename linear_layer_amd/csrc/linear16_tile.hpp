@@ -631,14 +631,13 @@ __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(
 // 128 x 256 or of 128 x 128, whichever takes the fewest rounds' time: measured, a round of the
 // smaller ones takes 0.58 and 0.41 of a round of the large. `large` of them are left, and `halves`
 // pieces of 128 x 256 beside them.
-__host__ __device__ inline int piece_split(int64_t large, int64_t halves, int cus, bool may_cut, float &cost)
+__host__ __device__ inline int piece_split(int64_t large, int64_t halves, int cus, float &cost)
 {
     const auto rounds = [cus](int64_t n) { return (float)((n + cus - 1) / cus); };
     const float c1 = rounds(large) + 0.58f * rounds(halves), c2 = 0.58f * rounds(2 * large + halves),
                 c4 = 0.41f * rounds(4 * large + 2 * halves);
-    const bool one = !may_cut || (c1 <= c2 && c1 <= c4);
-    cost = one ? c1 : c2 <= c4 ? c2 : c4;
-    return one ? 1 : c2 <= c4 ? 2 : 4;
+    cost = c1 <= c2 && c1 <= c4 ? c1 : c2 <= c4 ? c2 : c4;
+    return c1 <= c2 && c1 <= c4 ? 1 : c2 <= c4 ? 2 : 4;
 }
 
 // Tiles of 256 x 256, one a CU, as many workgroups as there are CUs, each of which takes every
@@ -663,7 +662,7 @@ __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(
         n_half = find_chunk_by(p.groups, p.M, count_half, -1, c) * p.tiles_n;
     }
     float cost;
-    const int left = n_large % cus, split = piece_split(left, n_half, cus, DMA_B, cost);
+    const int left = n_large % cus, split = piece_split(left, n_half, cus, cost);
     const int whole = split == 1 ? n_large : n_large - left;   // in one piece
     const int pieces = (split == 1 ? n_half : 2 * left + n_half) * (split == 4 ? 2 : 1), total = whole + pieces;
     for (int round = 0; round < total; round += cus) {
@@ -709,30 +708,30 @@ __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(
             if (job.m0 >= job.m_end || job.n0 >= p.N)
                 continue;
         }
-        __syncthreads();   // nobody reads the tile before this one's rows in LDS any more
+        // nobody reads the tile before this one's rows in LDS any more (its stores may be on their way)
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
         if (piece < 0)
             l16_tile<OP, BF16, 256, 256, 1, 2, NB, SA, SB, true>(p, job, lds);
-        else if constexpr (DMA_B) {   // (codes decoded on the way take too many registers for three forms)
-            if (split != 4)
-                l16_tile<OP, BF16, 128, 256, 1, 3, NB, SA, SB, true>(p, job, lds);
-            else
-                l16_tile<OP, BF16, 128, 128, 1, 3, NB, SA, SB, true>(p, job, lds);
-        }
+        else if (split != 4)
+            l16_tile<OP, BF16, 128, 256, 1, 3, NB, SA, SB, true>(p, job, lds);
+        else
+            l16_tile<OP, BF16, 128, 128, 1, 3, NB, SA, SB, true>(p, job, lds);
     }
 }
 
 // ---- launches -----------------------------------------------------------------------
 
 // Whether large tiles take less time: n_large and n_half of them and of their halves, against
-// n_small of 128 x 128. Two small ones a CU have 0.88 of the large ones' rate; a tile's beginning
-// and end, under the other workgroup's products or not, are four and nine stages' time.
-inline bool prefer_large(int64_t n_large, int64_t n_half, int64_t n_small, int k, int cus, bool may_cut = true)
+// n_small of 128 x 128. Two small ones a CU take 0.62 of a large one's time; beside its stages
+// a tile costs five of them, and the first large one four more, which no other workgroup covers.
+// (Measured, large against small: 4096 x 4096 x 512 33 and 28 us, 2048 x 11008 x 4096 220 and 239,
+// 16 weights' gradients of 4096 x 2048 over 512 rows each 219 and 325.)
+inline bool prefer_large(int64_t n_large, int64_t n_half, int64_t n_small, int k, int cus)
 {
     float rest;
-    piece_split(n_large % cus, n_half, cus, may_cut, rest);
-    const float stages = (float)cdiv(k, Block::BK);
-    return ((float)(n_large / cus) + rest) * (stages + 9.0f) <=
-           (float)((n_small + 2 * cus - 1) / (2 * cus)) * (0.5f / 0.88f) * (stages + 4.0f);
+    piece_split(n_large % cus, n_half, cus, rest);
+    const float stages = (float)cdiv(k, Block::BK) + 5.0f;
+    return ((float)(n_large / cus) + rest) * stages + 4.0f <= (float)((n_small + 2 * cus - 1) / (2 * cus)) * 0.62f * stages;
 }
 
 template <int OP, bool BF16, int SA, int SB>
