@@ -783,6 +783,11 @@ def _packed8(q, M, K, what):
 def mx8_quantize(X, codes, scales, stream=None):
     """Quantise X (float32, float16 or bfloat16; M x K) along its rows into uint8 codes
     and scales. Returns (codes, scales)."""
+    if stream is None:
+        st = _short_calls().mx8_quantize(X, codes, scales)
+        if st is not None:
+            _check(st, "mx8_quantize")
+            return codes, scales
     t = _type_of(X, "X")
     px, M, K, ldx = _mat(X, X.dtype, "X")
     packed = _packed8((codes, scales), M, K, "X")
@@ -792,6 +797,11 @@ def mx8_quantize(X, codes, scales, stream=None):
 
 def mx8_dequantize(codes, scales, Y, stream=None):
     """Y (float32, float16 or bfloat16; M x K) = the values codes and scales stand for."""
+    if stream is None:
+        st = _short_calls().mx8_dequantize(codes, scales, Y)
+        if st is not None:
+            _check(st, "mx8_dequantize")
+            return Y
     t = _type_of(Y, "Y")
     py, M, K, ldy = _mat(Y, Y.dtype, "Y")
     packed = _packed8((codes, scales), M, K, "Y")
@@ -891,6 +901,11 @@ def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None
     all groups stay as they are. A product of few rows and columns gains from a workspace of
     linear16_workspace_size bytes: on the current stream it comes from torch's allocator, with
     ``stream`` given the call runs without one unless it is given too. Returns Y."""
+    if stream is None:
+        st = _short_calls().linear16_nt(X, W, bias, act, R, Y, Z, offsets, workspace)
+        if st is not None:
+            _check(st, "linear16_nt")
+            return Y
     t = _type16_of(X, "X")
     px, M, K, ldx = _mat(X, X.dtype, "X")
     groups, poff = _offsets(offsets)
@@ -929,6 +944,11 @@ def linear16_grad_act(DY, Z, act: int, DZ, dbias=None, offsets=None, workspace=N
     for ACT_NONE). DZ may be DY or Z. dbias takes a workspace (a contiguous device tensor of
     linear16_grad_act_workspace_size bytes); without one it comes from torch's allocator, on
     the current stream only. Returns DZ."""
+    if stream is None:
+        st = _short_calls().linear16_grad_act(DY, Z, act, DZ, dbias, offsets, workspace)
+        if st is not None:
+            _check(st, "linear16_grad_act")
+            return DZ
     torch = _torch()
     t = _type16_of(DZ, "DZ")
     pdz, M, N, lddz = _mat(DZ, DZ.dtype, "DZ")

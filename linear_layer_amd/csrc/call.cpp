@@ -1,6 +1,6 @@
 // Python module linear_layer_amd._call: the argument handling of the 4-bit
-// products' and the residual norms' calls, which in Python takes longer than
-// their small kernels run. Each function takes the tensors and numbers of the
+// products', the residual norms' and the 16-bit layer's calls, which in Python takes
+// longer than their small kernels run. Each function takes the tensors and numbers of the
 // Python function of the same name, enqueues on the current stream of the
 // tensors' device and returns the status of the C call, or None, with nothing
 // enqueued, where an argument is not what the call takes: the Python function
@@ -308,6 +308,201 @@ PyObject *norm_grad(PyObject *const *x)
     });
 }
 
+// X, codes, scales
+PyObject *quantize8(PyObject *const *x)
+{
+    Args a;
+    at::ScalarType type = at::kFloat;
+    const int t = element_type(a, x[0], type);
+    const Mat m(a, x[0], type);
+    const Mat q(a, x[1], at::kByte, m.rows, m.cols), s(a, x[2], at::kByte, m.rows, scale_bytes(m.cols));
+    void *stream = a.stream();
+    return enqueue(a, [&] {
+        return mx8_quantize(m.rows, m.cols, t, m.p, m.ld, static_cast<uint8_t *>(q.p), q.ld, static_cast<uint8_t *>(s.p), s.ld,
+                            stream);
+    });
+}
+
+// codes, scales, Y
+PyObject *dequantize8(PyObject *const *x)
+{
+    Args a;
+    at::ScalarType type = at::kFloat;
+    const int t = element_type(a, x[2], type);
+    const Mat y(a, x[2], type);
+    const Mat q(a, x[0], at::kByte, y.rows, y.cols), s(a, x[1], at::kByte, y.rows, scale_bytes(y.cols));
+    void *stream = a.stream();
+    return enqueue(a, [&] {
+        return mx8_dequantize(y.rows, y.cols, static_cast<uint8_t *>(q.p), q.ld, static_cast<uint8_t *>(s.p), s.ld, t, y.p, y.ld,
+                              stream);
+    });
+}
+
+// Groups of rows: groups + 1 contiguous int32 row numbers, or None for one group.
+struct Groups {
+    int32_t *offsets = nullptr;
+    int n = 1;
+
+    Groups(Args &a, PyObject *o)
+    {
+        if (o == Py_None)
+            return;
+        const at::Tensor *t = a.tensor(o);
+        if (t == nullptr || t->scalar_type() != at::kInt || t->dim() != 1 || t->size(0) < 2 || t->size(0) - 1 > LL_MAX_GROUPS ||
+            t->stride(0) != 1) {   // (no groups at all: the Python code)
+            a.ok = false;
+            return;
+        }
+        offsets = static_cast<int32_t *>(t->data_ptr());
+        n = (int)t->size(0) - 1;
+    }
+    // Contiguous fp32 values, N or n x N; null for None.
+    float *vec(Args &a, PyObject *o, int64_t N) const
+    {
+        if (o == Py_None)
+            return nullptr;
+        const at::Tensor *t = a.tensor(o);
+        const bool two = offsets != nullptr;
+        if (t == nullptr || t->scalar_type() != at::kFloat || t->dim() != (two ? 2 : 1) || (two && t->size(0) != n) ||
+            t->size(-1) != N || !t->is_contiguous()) {
+            a.ok = false;
+            return nullptr;
+        }
+        return static_cast<float *>(t->data_ptr());
+    }
+};
+
+// One weight, or a stack of one for each group.
+struct Weights {
+    void *p = nullptr;
+    int N = 0, K = 0, ld = 1;
+    int64_t stride = 0;
+
+    Weights(Args &a, PyObject *o, at::ScalarType type, const Groups &g)
+    {
+        if (g.offsets == nullptr) {
+            const Mat m(a, o, type);
+            p = m.p, N = m.rows, K = m.cols, ld = m.ld;
+            return;
+        }
+        const at::Tensor *t = a.tensor(o);
+        if (t == nullptr || t->scalar_type() != type || t->dim() != 3 || t->size(0) != g.n) {
+            a.ok = false;
+            return;
+        }
+        const int64_t n = t->size(1), k = t->size(2), s = n > 1 ? t->stride(1) : k;
+        if ((k > 1 && t->stride(2) != 1) || s < k || n > INT32_MAX || s > INT32_MAX) {
+            a.ok = false;
+            return;
+        }
+        p = t->data_ptr(), N = (int)n, K = (int)k, ld = s > 1 ? (int)s : 1;
+        stride = g.n > 1 ? t->stride(0) : 0;
+    }
+};
+
+// A matrix of `type`, a pair (codes, scales) in 8 bits, or None.
+struct Held {
+    Mat m, q, s;
+
+    Held(Args &a, PyObject *o, at::ScalarType type, int64_t M, int64_t N)
+    {
+        if (o == Py_None)
+            return;
+        if (!PyTuple_Check(o)) {
+            m = Mat(a, o, type, M, N);
+            return;
+        }
+        if (PyTuple_GET_SIZE(o) != 2) {
+            a.ok = false;
+            return;
+        }
+        q = Mat(a, PyTuple_GET_ITEM(o, 0), at::kByte, M, N);
+        s = Mat(a, PyTuple_GET_ITEM(o, 1), at::kByte, M, scale_bytes(N));
+    }
+    int ld(const Mat &x, int64_t cols) const { return x.p != nullptr ? x.ld : cols > 1 ? (int)cols : 1; }
+};
+
+// A workspace of at least `need` bytes: the one given, or memory of torch's allocator, in the
+// order of the current stream, so that it may be given back at once.
+struct Room {
+    at::Tensor own;
+    void *p = nullptr;
+    int64_t bytes = 0;
+
+    Room(Args &a, PyObject *o, int64_t need, PyObject *like)
+    {
+        if (o != Py_None) {
+            const at::Tensor *w = a.tensor(o);
+            if (w == nullptr || !w->is_contiguous()) {
+                a.ok = false;
+                return;
+            }
+            p = w->data_ptr();
+            bytes = (int64_t)w->nbytes();
+        } else if (a.ok && need > 0) {
+            own = at::empty({need}, THPVariable_Unpack(like).options().dtype(at::kByte));
+            p = own.data_ptr();
+            bytes = need;
+        }
+    }
+};
+
+int integer(Args &a, PyObject *o)
+{
+    const long v = a.ok ? PyLong_AsLong(o) : 0;
+    if (a.ok && ((v == -1 && PyErr_Occurred()) || v < -1000 || v > 1000))
+        a.fail();
+    return (int)v;
+}
+
+// X, W, bias, act, R, Y, Z, offsets, workspace
+PyObject *linear16(PyObject *const *x)
+{
+    Args a;
+    at::ScalarType type = at::kHalf, out = at::kHalf;
+    const int t = element_type(a, x[0], type), ty = element_type(a, x[5], out);
+    const Mat X(a, x[0], type);
+    const Groups g(a, x[7]);
+    const Weights W(a, x[1], type, g);
+    const Mat Y(a, x[5], out, X.rows, W.N), R(a, x[4], out, X.rows, W.N, true);
+    const Held Z(a, x[6], type, X.rows, W.N);
+    float *bias = g.vec(a, x[2], W.N);
+    const int act = integer(a, x[3]);
+    if (t == LL_TYPE_F32 || (ty != t && ty != LL_TYPE_F32) || W.K != X.cols)
+        a.ok = false;
+    void *stream = a.stream();
+    const Room w(a, x[8], a.ok && x[8] == Py_None ? ll_linear16_workspace_size(X.rows, W.N, X.cols, g.n) : 0, x[0]);
+    return enqueue(a, [&] {
+        return linear16_nt(X.rows, W.N, X.cols, t, static_cast<uint16_t *>(X.p), X.ld, g.n, g.offsets,
+                           static_cast<uint16_t *>(W.p), W.ld, W.stride, bias, act, ty, R.p, R.ld, Y.p, Y.ld,
+                           static_cast<uint16_t *>(Z.m.p), Z.ld(Z.m, W.N), static_cast<uint8_t *>(Z.q.p), Z.ld(Z.q, W.N),
+                           static_cast<uint8_t *>(Z.s.p), Z.ld(Z.s, W.N), w.p, w.bytes, stream);
+    });
+}
+
+// DY, Z, act, DZ, dbias, offsets, workspace
+PyObject *grad_act16(PyObject *const *x)
+{
+    Args a;
+    at::ScalarType type = at::kHalf, in = at::kHalf;
+    const int t = element_type(a, x[3], type), ty = element_type(a, x[0], in);
+    const Mat DZ(a, x[3], type), DY(a, x[0], in, DZ.rows, DZ.cols);
+    const Groups g(a, x[5]);
+    const Held Z(a, x[1], type, DZ.rows, DZ.cols);
+    float *dbias = g.vec(a, x[4], DZ.cols);
+    const int act = integer(a, x[2]);
+    if (t == LL_TYPE_F32 || (ty != t && ty != LL_TYPE_F32))
+        a.ok = false;
+    void *stream = a.stream();
+    const Room w(a, x[6], a.ok && dbias != nullptr ? ll_linear16_grad_act_workspace_size(DZ.rows, DZ.cols, g.n) : 0, x[3]);
+    return enqueue(a, [&] {
+        return linear16_grad_act(DZ.rows, DZ.cols, t, act, ty, DY.p, DY.ld, g.n, g.offsets, static_cast<uint16_t *>(Z.m.p),
+                                 Z.ld(Z.m, DZ.cols), static_cast<uint8_t *>(Z.q.p), Z.ld(Z.q, DZ.cols),
+                                 static_cast<uint8_t *>(Z.s.p), Z.ld(Z.s, DZ.cols), static_cast<uint16_t *>(DZ.p), DZ.ld,
+                                 dbias, w.p, w.bytes, stream);
+    });
+}
+
 #define LL_METHOD(name, n, f) \
     {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(&guarded<n, f>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
@@ -319,6 +514,10 @@ PyMethodDef methods[] = {
     LL_METHOD("gemm_bf16mx4f32_nt", 6, gemm_16mx4<true>),
     LL_METHOD("rmsnorm_residual", 9, norm),
     LL_METHOD("rmsnorm_residual_grad", 15, norm_grad),
+    LL_METHOD("mx8_quantize", 3, quantize8),
+    LL_METHOD("mx8_dequantize", 3, dequantize8),
+    LL_METHOD("linear16_nt", 9, linear16),
+    LL_METHOD("linear16_grad_act", 7, grad_act16),
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_call", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
