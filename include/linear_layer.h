@@ -517,6 +517,15 @@ int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx,
                 uint16_t *Z, int ldz, uint8_t *ZQ, int ldzq, uint8_t *ZS, int ldzs,
                 void *workspace, int64_t workspace_bytes, void *stream);
 int64_t ll_linear16_workspace_size(int M, int N, int K, int groups);
+/* Name of the kernel that a product takes on a device with num_cus compute units
+ * (num_cus <= 0: 256), with rows on 16 bytes (`aligned`) or not: "rows" and
+ * "rows_any" (forward, at most 64 rows a group on average), "small" and
+ * "small_any" (tiles of 128 x 128), "large" (256 x 256 and pieces of them); "" for one
+ * without work or a bad argument. Static string. */
+#define LL_L16_FORWARD 0
+#define LL_L16_GRAD_INPUT 1
+#define LL_L16_GRAD_WEIGHT 2
+const char *ll_linear16_chosen_kernel(int product, int M, int N, int K, int groups, int aligned, int num_cus);
 int64_t ll_linear16_grad_act_workspace_size(int M, int N, int groups);
 int linear16_grad_act(int M, int N, int type, int act, int ytype, const void *DY, int lddy,
                       int groups, const int32_t *offsets,

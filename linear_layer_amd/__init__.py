@@ -67,7 +67,8 @@ __all__ = [
     "mx4_chosen_kernel", "A_MX4", "A_F16", "A_BF16", "rmsnorm_residual", "rmsnorm_residual_grad", "rmsnorm_grad_workspace_size",
     "TYPE_F32", "TYPE_F16", "TYPE_BF16",
     "mx8_quantize", "mx8_dequantize", "mx8_shapes", "linear16_nt", "linear16_grad_act", "linear16_grad_input",
-    "linear16_grad_weight", "linear16_grad_act_workspace_size", "linear16_workspace_size", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "MAX_GROUPS",
+    "linear16_grad_weight", "linear16_grad_act_workspace_size", "linear16_workspace_size",
+    "linear16_chosen_kernel", "L16_FORWARD", "L16_GRAD_INPUT", "L16_GRAD_WEIGHT", "ACT_GELU", "ACT_GELU_TANH", "ACT_SILU", "MAX_GROUPS",
     "library_path", "load", "set_tile", "num_tiles", "tile_name", "chosen_tile",
     "set_split_k", "chosen_split_k", "set_stream_k", "chosen_stream_k",
     "ACT_NONE", "ACT_RELU", "DTYPE_F32", "DTYPE_F16", "PLAN_RELU", "PLAN_B_NK", "PLAN_UNALIGNED",
@@ -78,6 +79,7 @@ OK, ERR_INVALID_VALUE, ERR_NO_DEVICE, ERR_UNSUPPORTED_ARCH, ERR_LAUNCH = 0, 1, 2
 ACT_NONE, ACT_RELU = 0, 1
 ACT_GELU, ACT_GELU_TANH, ACT_SILU = 2, 3, 4   # of linear16_nt and linear16_grad_act
 MAX_GROUPS = 1 << 20   # of rows, in the linear16 calls
+L16_FORWARD, L16_GRAD_INPUT, L16_GRAD_WEIGHT = 0, 1, 2   # products of linear16_chosen_kernel
 DTYPE_F32, DTYPE_F16 = 0, 1
 TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2   # element types of mx4_quantize, mx4_dequantize and the residual norms
 A_MX4, A_F16, A_BF16 = 0, 1, 2   # the forms of A of the 4-bit products
@@ -105,7 +107,8 @@ EXPORTED = ("gemm_f32", "gemm_f16f32", "gemm_bf16f32", "linear_bias_act", "ll_st
             "ll_mx4_chosen_kernel",
             "rmsnorm_residual", "rmsnorm_residual_grad", "ll_rmsnorm_grad_workspace_size",
             "mx8_quantize", "mx8_dequantize", "linear16_nt", "linear16_grad_act", "linear16_grad_input",
-            "linear16_grad_weight", "ll_linear16_grad_act_workspace_size", "ll_linear16_workspace_size")
+            "linear16_grad_weight", "ll_linear16_grad_act_workspace_size", "ll_linear16_workspace_size",
+            "ll_linear16_chosen_kernel")
 
 
 class LinearLayerError(RuntimeError):
@@ -171,6 +174,8 @@ def load():
     lib.mx8_dequantize.argtypes = [i32, i32, vp, i32, vp, i32, i32, vp, i32, vp]
     lib.linear16_nt.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, i64, vp, i32, i32, vp, i32, vp, i32,
                                 vp, i32, vp, i32, vp, i32, vp, i64, vp]
+    lib.ll_linear16_chosen_kernel.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+    lib.ll_linear16_chosen_kernel.restype = ctypes.c_char_p
     lib.ll_linear16_workspace_size.argtypes = [i32, i32, i32, i32]
     lib.ll_linear16_workspace_size.restype = i64
     lib.linear16_grad_act.argtypes = [i32, i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, i32, vp, i32, vp,
@@ -890,6 +895,14 @@ def linear16_workspace_size(M: int, N: int, K: int, groups: int = 1) -> int:
     if n < 0:
         raise ValueError("negative size")
     return n
+
+
+def linear16_chosen_kernel(product: int, M: int, N: int, K: int, groups: int = 1, aligned: bool = True,
+                           num_cus: int = 0) -> str:
+    """Name of the kernel that a product (L16_*) of the layer takes, with rows on 16 bytes
+    or not; "" for one without work."""
+    return load().ll_linear16_chosen_kernel(int(product), int(M), int(N), int(K), int(groups), int(bool(aligned)),
+                                            int(num_cus)).decode()
 
 
 def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None, stream=None):

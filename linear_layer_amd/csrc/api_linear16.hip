@@ -97,6 +97,14 @@ int mx8_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
     return status(launch_mx8_dequantize(type, codes, ldq, scales, lds, Y, ldy, M, K, static_cast<hipStream_t>(stream)));
 }
 
+const char *ll_linear16_chosen_kernel(int product, int M, int N, int K, int groups, int aligned, int num_cus)
+{
+    if (product < LL_L16_FORWARD || product > LL_L16_GRAD_WEIGHT || M <= 0 || N <= 0 || K <= 0 || groups <= 0 ||
+        groups > LL_MAX_GROUPS)
+        return "";
+    return l16_kernel_name(product, M, N, K, groups, aligned != 0, num_cus > 0 ? num_cus : 256);
+}
+
 int64_t ll_linear16_workspace_size(int M, int N, int K, int groups)
 {
     if (M < 0 || N < 0 || K < 0 || groups < 0 || groups > LL_MAX_GROUPS)

@@ -59,6 +59,9 @@ hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, int cus, hip
 hipError_t launch_l16_dx(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 
+// The name of the kernel that one of them takes: M rows, N outputs and K inputs of the layer.
+const char *l16_kernel_name(int op, int M, int N, int K, int groups, bool vec, int cus);
+
 struct ActGradParams {
     const void *DY;             // M x N of LL_TYPE_*
     const uint16_t *Z;          // 16 bits, or

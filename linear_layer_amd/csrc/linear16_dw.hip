@@ -8,12 +8,10 @@ using namespace l16;
 template <bool BF16, int SB>
 static hipError_t launch_dw(const L16Params &p, bool vec, int cus, hipStream_t s)
 {
-    const int64_t n = p.groups.n, rows = n * cdiv(p.M, 128);
+    const int64_t rows = (int64_t)p.groups.n * cdiv(p.M, 128);
     if (!vec)
         return launch_small<L16_DW, BF16, COLS, SB, false>(p, rows, s);
-    const int64_t n_large = n * cdiv(p.M, 256) * cdiv(p.N, 256);
-    const int each = p.K > n ? cdiv(p.K, (int)n) : 1;   // rows of a group
-    if (n_large < (1 << 29) && prefer_large(n_large, 0, rows * cdiv(p.N, 128), each, cus))
+    if (weight_prefers_large(p.M, p.N, p.K, p.groups.n, cus))
         return launch_large<L16_DW, BF16, COLS, SB>(p, cus, s);
     return launch_small<L16_DW, BF16, COLS, SB, true>(p, rows, s);
 }
@@ -23,6 +21,18 @@ hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t 
     if (p.BS != nullptr)
         return bf16 ? launch_dw<true, COLS8>(p, vec, cus, s) : launch_dw<false, COLS8>(p, vec, cus, s);
     return bf16 ? launch_dw<true, COLS>(p, vec, cus, s) : launch_dw<false, COLS>(p, vec, cus, s);
+}
+
+const char *l16_kernel_name(int op, int M, int N, int K, int groups, bool vec, int cus)
+{
+    if (op == L16_FWD && l16_takes_rows(M, groups))
+        return vec ? "rows" : "rows_any";
+    if (!vec)
+        return "small_any";
+    const bool large = op == L16_DW ? weight_prefers_large(N, K, M, groups, cus)
+                                    : op == L16_DX ? rows_prefer_large(M, K, N, groups, cus)
+                                                   : rows_prefer_large(M, N, K, groups, cus);
+    return large ? "large" : "small";
 }
 
 }  // namespace ll

@@ -734,6 +734,21 @@ inline bool prefer_large(int64_t n_large, int64_t n_half, int64_t n_small, int k
     return ((float)(n_large / cus) + rest) * stages + 4.0f <= (float)((n_small + 2 * cus - 1) / (2 * cus)) * 0.62f * stages;
 }
 
+// The same of a product: rows of C by groups (taken as equally long), or groups of the contracted rows.
+inline bool rows_prefer_large(int M, int N, int K, int groups, int cus)
+{
+    const int g = groups < M ? groups : M, each = cdiv(M, g), tn = cdiv(N, 256), last = each & 255;
+    return ((int64_t)(M / 256) + g) * tn < (1 << 29) &&   // (tiles are counted in 32 bits)
+           prefer_large((int64_t)g * ((each + 127) / 256) * tn, last != 0 && last <= 128 ? (int64_t)g * tn : 0,
+                        (int64_t)g * cdiv(each, 128) * cdiv(N, 128), K, cus);
+}
+inline bool weight_prefers_large(int M, int N, int rows, int groups, int cus)
+{
+    const int64_t n_large = (int64_t)groups * cdiv(M, 256) * cdiv(N, 256);
+    return n_large < (1 << 29) &&
+           prefer_large(n_large, 0, (int64_t)groups * cdiv(M, 128) * cdiv(N, 128), rows > groups ? cdiv(rows, groups) : 1, cus);
+}
+
 template <int OP, bool BF16, int SA, int SB>
 hipError_t launch_large(L16Params p, int cus, hipStream_t s)
 {
@@ -763,11 +778,7 @@ hipError_t launch_rows(const L16Params &p, bool vec, int cus, hipStream_t s)
     const int64_t rows = p.groups.offsets == nullptr ? cdiv(p.M, 128) : (int64_t)(p.M / 128) + g;
     if (!vec)
         return launch_small<OP, BF16, ROWS, SB, false>(p, rows, s);
-    // the groups taken as equally long; as many large tiles as fit a launch's 32 bits
-    const int each = cdiv(p.M, g), tn = cdiv(p.N, 256);
-    const int64_t n_large = (int64_t)g * ((each + 127) / 256) * tn, n_half = (each & 255) != 0 && (each & 255) <= 128 ? (int64_t)g * tn : 0;
-    if (((int64_t)(p.M / 256) + g) * tn < (1 << 29) &&
-        prefer_large(n_large, n_half, (int64_t)g * cdiv(each, 128) * cdiv(p.N, 128), p.K, cus))
+    if (rows_prefer_large(p.M, p.N, p.K, p.groups.n, cus))
         return launch_large<OP, BF16, ROWS, SB>(p, cus, s);
     return launch_small<OP, BF16, ROWS, SB, true>(p, rows, s);
 }

@@ -258,3 +258,28 @@ def test_reference_format():
     for t, e in ((448.0, 0), (448.5, 1), (1.75, -8), (1.7501, -7), (0.0, -127), (1e-45, -127), (3e38, 120)):
         assert ref.mx8_quantize(np.array([[t]]))[1][0, 0] == e + 127
     assert ref.mx8_quantize(np.array([[np.inf, 1.0]]))[1][0, 0] == 255
+
+
+def test_kernel_names():
+    k = ll.linear16_chosen_kernel
+    assert k(0, 1, 11008, 4096) == "rows" and k(0, 64, 8, 8, aligned=False) == "rows_any" and k(0, 65, 8, 8) == "small"
+    assert k(0, 640, 64, 64, groups=10) == "rows" and k(1, 1, 64, 64) == "small" and k(1, 1, 64, 64, aligned=False) == "small_any"
+    assert k(0, 8192, 8192, 8192) == k(1, 8192, 8192, 8192) == k(2, 8192, 8192, 8192) == "large"
+    for bad in ((3, 1, 1, 1), (-1, 1, 1, 1), (0, 0, 1, 1), (0, 1, 0, 1), (0, 1, 1, 0), (0, 1, 1, 1, 0), (0, 1, 1, 1, ll.MAX_GROUPS + 1)):
+        assert k(*bad) == ""
+    # sizes at the limits
+    big = 2 ** 31 - 1025
+    for op in (0, 1, 2):
+        for m, n, kk, g in ((big, 1, 1, 1), (1, big, 1, 1), (1, 1, big, 1), (big, big, big, ll.MAX_GROUPS)):
+            assert k(op, m, n, kk, g) in ("rows", "small", "large")
+
+
+def test_forward_workspace():
+    f = ll.linear16_workspace_size
+    assert f(1, 11008, 4096) == 0 and f(0, 64, 64) == 0 and f(500, 64, 11008) == 0 and f(1, 200, 512) == 0
+    n = f(33, 4096, 11008)
+    assert n > 0 and n % (4 * 33 * 4096) == 0 and 2 <= n // (4 * 33 * 4096) <= 16
+    for bad in ((-1, 8, 8), (8, -1, 8), (8, 8, -1), (8, 8, 8, -1), (2 ** 31, 8, 8)):
+        with pytest.raises(ValueError):
+            f(*bad)
+    assert fwd(ws=P["ws"], ws_bytes=-1) == E and fwd(ws=P["ws"] + 4, ws_bytes=1 << 20) == E
