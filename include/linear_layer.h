@@ -481,11 +481,12 @@ int mx8_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
  *   Z       M-by-N of `type`, or NULL: Z as the way back needs it, and / or
  *   ZQ, ZS  the same in MX8 (M-by-N codes, M-by-ceil(N/32) scales), from its
  *           FP32 sums; both or neither.
- *   workspace   NULL, or at least ll_linear16_workspace_size(M, N, K, groups) bytes
- *           (on the current device; 0: none helps), 16-byte aligned, overlapping
- *           nothing; its contents need no preparation. With one, a product of few
- *           rows and columns shares K out over workgroups. Calls that share one
- *           must not overlap in time.
+ *   workspace   NULL, or at least ll_linear16_workspace_size(LL_L16_FORWARD, M, N,
+ *           K, groups) bytes (on the current device; 0: none helps), 16-byte
+ *           aligned, overlapping nothing; its contents need no preparation. With
+ *           one, a product that does not fill the GPU with tiles shares K out
+ *           over workgroups, whose sums a second launch adds in order. Calls that
+ *           share one must not overlap in time.
  * Outputs must not overlap inputs or each other otherwise. K == 0: Z = bias.
  *
  * linear16_grad_act — dZ = dY * act'(Z), and dbias[g] = the sums of dZ (before its
@@ -500,7 +501,7 @@ int mx8_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
  *           need no preparation. Calls that share one must not overlap in time.
  *
  * linear16_grad_input — dX (M-by-K of `xtype`: `type` or LL_TYPE_F32) = dZ
- * (M-by-N of `type`) * W.
+ * (M-by-N of `type`) * W. workspace as linear16_nt's, LL_L16_GRAD_INPUT.
  *
  * linear16_grad_weight — dW = dZ^T * X + beta * dW, N-by-K of `wtype` (`type` or
  * LL_TYPE_F32), lddw >= max(1, K); group g's from its own rows, stride_dw * g elements
@@ -516,7 +517,8 @@ int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx,
                 int ytype, const void *R, int ldr, void *Y, int ldy,
                 uint16_t *Z, int ldz, uint8_t *ZQ, int ldzq, uint8_t *ZS, int ldzs,
                 void *workspace, int64_t workspace_bytes, void *stream);
-int64_t ll_linear16_workspace_size(int M, int N, int K, int groups);
+/* product: LL_L16_FORWARD or LL_L16_GRAD_INPUT; -1 for another or a negative size. */
+int64_t ll_linear16_workspace_size(int product, int M, int N, int K, int groups);
 /* Name of the kernel that a product takes on a device with num_cus compute units
  * (num_cus <= 0: 256), with rows on 16 bytes (`aligned`) or not: "rows" and
  * "rows_any" (forward, at most 64 rows a group on average), "small" and
@@ -535,7 +537,8 @@ int linear16_grad_act(int M, int N, int type, int act, int ytype, const void *DY
 int linear16_grad_input(int M, int N, int K, int type, const uint16_t *DZ, int lddz,
                         int groups, const int32_t *offsets,
                         const uint16_t *W, int ldw, int64_t stride_w,
-                        int xtype, void *DX, int lddx, void *stream);
+                        int xtype, void *DX, int lddx,
+                        void *workspace, int64_t workspace_bytes, void *stream);
 int linear16_grad_weight(int M, int N, int K, int type, const uint16_t *DZ, int lddz,
                          int groups, const int32_t *offsets,
                          const uint16_t *X, int ldx, const uint8_t *XQ, int ldxq, const uint8_t *XS, int ldxs,

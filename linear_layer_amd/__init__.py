@@ -176,11 +176,11 @@ def load():
                                 vp, i32, vp, i32, vp, i32, vp, i64, vp]
     lib.ll_linear16_chosen_kernel.argtypes = [i32, i32, i32, i32, i32, i32, i32]
     lib.ll_linear16_chosen_kernel.restype = ctypes.c_char_p
-    lib.ll_linear16_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.ll_linear16_workspace_size.argtypes = [i32, i32, i32, i32, i32]
     lib.ll_linear16_workspace_size.restype = i64
     lib.linear16_grad_act.argtypes = [i32, i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, i32, vp, i32, vp,
                                       vp, i64, vp]
-    lib.linear16_grad_input.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, i64, i32, vp, i32, vp]
+    lib.linear16_grad_input.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, i64, i32, vp, i32, vp, i64, vp]
     lib.linear16_grad_weight.argtypes = [i32, i32, i32, i32, vp, i32, i32, vp, vp, i32, vp, i32, vp, i32, i32, f32, vp,
                                          i32, i64, vp]
     for f in (lib.mx8_quantize, lib.mx8_dequantize, lib.linear16_nt, lib.linear16_grad_act, lib.linear16_grad_input,
@@ -887,14 +887,25 @@ def _workspace(t):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
-def linear16_workspace_size(M: int, N: int, K: int, groups: int = 1) -> int:
-    """Bytes of workspace that linear16_nt gains from on the current device (0: none)."""
+def linear16_workspace_size(product: int, M: int, N: int, K: int, groups: int = 1) -> int:
+    """Bytes of workspace that linear16_nt (L16_FORWARD) or linear16_grad_input
+    (L16_GRAD_INPUT) gains from on the current device (0: none)."""
     if max(M, N, K) > _INT_MAX or groups > MAX_GROUPS:
         raise ValueError(f"the calls take sizes up to {_INT_MAX} and {MAX_GROUPS} groups")
-    n = load().ll_linear16_workspace_size(int(M), int(N), int(K), int(groups))
+    n = load().ll_linear16_workspace_size(int(product), int(M), int(N), int(K), int(groups))
     if n < 0:
-        raise ValueError("negative size")
+        raise ValueError("negative size, or a product that takes no workspace")
     return n
+
+
+def _shares_workspace(product, M, N, K, groups, workspace, stream, like):
+    """(pointer, bytes, tensor) of the workspace given, or on the current stream of one that
+    the product gains from."""
+    if workspace is None and stream is None:
+        need = load().ll_linear16_workspace_size(product, M, N, K, groups)
+        if need > 0:
+            workspace = _torch().empty(need, dtype=_torch().uint8, device=like.device)
+    return (None, 0, None) if workspace is None else (*_workspace(workspace), workspace)
 
 
 def linear16_chosen_kernel(product: int, M: int, N: int, K: int, groups: int = 1, aligned: bool = True,
@@ -911,7 +922,7 @@ def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None
     None or Y. Z, if given, receives X*W^T + bias: a tensor of X's dtype, or a pair (codes,
     scales) of uint8 tensors (``mx8_shapes``). With ``offsets`` (groups + 1 ascending row
     numbers, int32, on the device) W is groups x N x K, bias groups x N, and rows outside
-    all groups stay as they are. A product of few rows and columns gains from a workspace of
+    all groups stay as they are. A product that does not fill the GPU gains from a workspace of
     linear16_workspace_size bytes: on the current stream it comes from torch's allocator, with
     ``stream`` given the call runs without one unless it is given too. Returns Y."""
     if stream is None:
@@ -931,11 +942,7 @@ def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None
     held, zs = _held(Z, X.dtype, M, N, "Z")
     pb = _group_vec(bias, groups, poff is not None, N, "bias")
     s = _stream(stream, X, W, Y, R, bias, offsets, workspace, *zs)
-    if workspace is None and stream is None and M <= 64 * groups:   # (longer groups gain from none)
-        need = load().ll_linear16_workspace_size(M, N, K, groups)
-        if need > 0:
-            workspace = _torch().empty(need, dtype=_torch().uint8, device=X.device)
-    pws, nws = (None, 0) if workspace is None else _workspace(workspace)
+    pws, nws, workspace = _shares_workspace(L16_FORWARD, M, N, K, groups, workspace, stream, X)
     _check(load().linear16_nt(M, N, K, t, px, ldx, groups, poff, pw, ldw, stride, pb, int(act), ty, pr, ldr, py, ldy,
                               *held, pws, nws, s), "linear16_nt")
     return Y
@@ -983,9 +990,9 @@ def linear16_grad_act(DY, Z, act: int, DZ, dbias=None, offsets=None, workspace=N
     return DZ
 
 
-def linear16_grad_input(DZ, W, DX, offsets=None, stream=None):
+def linear16_grad_input(DZ, W, DX, offsets=None, workspace=None, stream=None):
     """DX = DZ*W: DZ (M x N) and W (N x K, or groups x N x K) in float16 or bfloat16, DX
-    (M x K) of that dtype or float32. Returns DX."""
+    (M x K) of that dtype or float32. workspace: as linear16_nt's. Returns DX."""
     t = _type16_of(DZ, "DZ")
     pdz, M, N, lddz = _mat(DZ, DZ.dtype, "DZ")
     groups, poff = _offsets(offsets)
@@ -994,8 +1001,10 @@ def linear16_grad_input(DZ, W, DX, offsets=None, stream=None):
     pdx, M2, K2, lddx = _mat(DX, DX.dtype, "DX")
     if groups and (N2 != N or M2 != M or K2 != K):
         raise ValueError(f"shape mismatch: DZ {tuple(DZ.shape)}, W {tuple(W.shape)}, DX {tuple(DX.shape)}")
-    _check(load().linear16_grad_input(M, N, K, t, pdz, lddz, groups, poff, pw, ldw, stride, tx, pdx, lddx,
-                                      _stream(stream, DZ, W, DX, offsets)), "linear16_grad_input")
+    s = _stream(stream, DZ, W, DX, offsets, workspace)
+    pws, nws, workspace = _shares_workspace(L16_GRAD_INPUT, M, N, K, groups, workspace, stream, DZ)
+    _check(load().linear16_grad_input(M, N, K, t, pdz, lddz, groups, poff, pw, ldw, stride, tx, pdx, lddx, pws, nws, s),
+           "linear16_grad_input")
     return DX
 
 

@@ -51,6 +51,9 @@ bool groups_ok(const int32_t *offsets, int groups)
 }
 Range groups_range(const int32_t *offsets, int groups) { return vec_range(offsets, (int64_t)groups + 1); }
 
+// Of the sums of so many shares of an M x N result.
+int64_t shares_bytes(int shares, int M, int N) { return shares > 1 ? (int64_t)shares * M * N * 4 : 0; }
+
 int blocks_of(int cols) { return cols / 32 + (cols % 32 != 0); }
 
 }  // namespace
@@ -105,12 +108,14 @@ const char *ll_linear16_chosen_kernel(int product, int M, int N, int K, int grou
     return l16_kernel_name(product, M, N, K, groups, aligned != 0, num_cus > 0 ? num_cus : 256);
 }
 
-int64_t ll_linear16_workspace_size(int M, int N, int K, int groups)
+int64_t ll_linear16_workspace_size(int product, int M, int N, int K, int groups)
 {
-    if (M < 0 || N < 0 || K < 0 || groups < 0 || groups > LL_MAX_GROUPS)
+    if ((product != LL_L16_FORWARD && product != LL_L16_GRAD_INPUT) || M < 0 || N < 0 || K < 0 || groups < 0 ||
+        groups > LL_MAX_GROUPS)
         return -1;
     const Device dev = current_device();
-    return l16_workspace(M, N, K, groups, dev.status == LL_OK ? dev.cus : 256);
+    const int cus = dev.status == LL_OK ? dev.cus : 256;
+    return shares_bytes(l16_shares(product, M, N, K, groups, cus), M, product == LL_L16_FORWARD ? N : K);
 }
 
 int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx, int groups, const int32_t *offsets,
@@ -144,13 +149,14 @@ int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx, int g
     const Device dev = current_device();
     if (dev.status != LL_OK)
         return dev.status;
-    const int64_t need = workspace != nullptr ? l16_workspace(M, N, K, groups, dev.cus) : 0;
+    const int shares = workspace != nullptr ? l16_shares(L16_FWD, M, N, K, groups, dev.cus) : 1;
+    const int64_t need = shares_bytes(shares, M, N);
     const Range ws = {workspace, need};
     if (need > 0 && (workspace_bytes < need || any_overlap(&ws, 1, in, 4) || any_overlap(&ws, 1, out, 4) || overlap(ws, rr)))
         return LL_ERR_INVALID_VALUE;
     L16Params p{};
     p.ws = static_cast<float *>(workspace);
-    p.shares = need > 0 ? l16_row_shares(M, N, K, groups, dev.cus) : 1;
+    p.shares = shares;
     p.A = X;
     p.B = W;
     p.C = Y;
@@ -212,9 +218,10 @@ int linear16_grad_act(int M, int N, int type, int act, int ytype, const void *DY
 }
 
 int linear16_grad_input(int M, int N, int K, int type, const uint16_t *DZ, int lddz, int groups, const int32_t *offsets,
-                        const uint16_t *W, int ldw, int64_t stride_w, int xtype, void *DX, int lddx, void *stream)
+                        const uint16_t *W, int ldw, int64_t stride_w, int xtype, void *DX, int lddx, void *workspace,
+                        int64_t workspace_bytes, void *stream)
 {
-    if (!type16(type) || !out_type(xtype, type) || M < 0 || N < 0 || K < 0 || !groups_ok(offsets, groups) || stride_w < 0)
+    if (workspace_bytes < 0 || !type16(type) || !out_type(xtype, type) || M < 0 || N < 0 || K < 0 || !groups_ok(offsets, groups) || stride_w < 0)
         return LL_ERR_INVALID_VALUE;
     const Mat dz{DZ, lddz, 2}, w{W, ldw, 2}, dx{DX, lddx, type_bytes(xtype)};
     if (!dz.ld_ok(N) || !w.ld_ok(K) || !dx.ld_ok(K))
@@ -226,11 +233,16 @@ int linear16_grad_input(int M, int N, int K, int type, const uint16_t *DZ, int l
         !dz.ok(M, N) || !w.ok(N, K) || wr.bytes < 0 || !dx.ok(M, K))
         return LL_ERR_INVALID_VALUE;
     const Range out[1] = {dx.range(M, K)}, in[3] = {dz.range(M, N), wr, groups_range(offsets, groups)};
-    if (any_overlap(out, 1, in, 3))
+    if (any_overlap(out, 1, in, 3) || (workspace != nullptr && !aligned(workspace, 16)))
         return LL_ERR_INVALID_VALUE;
     const Device dev = current_device();
     if (dev.status != LL_OK)
         return dev.status;
+    const int shares = workspace != nullptr ? l16_shares(L16_DX, M, N, K, groups, dev.cus) : 1;
+    const int64_t need = shares_bytes(shares, M, K);
+    const Range ws = {workspace, need};
+    if (need > 0 && (workspace_bytes < need || any_overlap(&ws, 1, in, 3) || overlap(ws, out[0])))
+        return LL_ERR_INVALID_VALUE;
     L16Params p{};
     p.A = DZ;
     p.B = W;
@@ -240,6 +252,8 @@ int linear16_grad_input(int M, int N, int K, int type, const uint16_t *DZ, int l
     p.groups = Groups{offsets, groups};
     p.M = M, p.N = K, p.K = N;
     p.ctype = xtype;
+    p.ws = static_cast<float *>(workspace);
+    p.shares = shares;
     const bool vec = dz.vec(N) && w.vec(K) && (groups == 1 || stride_w % 8 == 0);
     return status(launch_l16_dx(type == LL_TYPE_BF16, p, vec, dev.cus, static_cast<hipStream_t>(stream)));
 }
@@ -279,6 +293,7 @@ int linear16_grad_weight(int M, int N, int K, int type, const uint16_t *DZ, int 
     p.stride_c = stride_dw;
     p.groups = Groups{offsets, groups};
     p.M = N, p.N = K, p.K = M;
+    p.shares = 1;
     p.ctype = wtype;
     p.beta = beta;
     // codes: rows on 16 bytes (the last piece may be short)

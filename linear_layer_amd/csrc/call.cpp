@@ -471,7 +471,7 @@ PyObject *linear16(PyObject *const *x)
     if (t == LL_TYPE_F32 || (ty != t && ty != LL_TYPE_F32) || W.K != X.cols)
         a.ok = false;
     void *stream = a.stream();
-    const Room w(a, x[8], a.ok && x[8] == Py_None ? ll_linear16_workspace_size(X.rows, W.N, X.cols, g.n) : 0, x[0]);
+    const Room w(a, x[8], a.ok && x[8] == Py_None ? ll_linear16_workspace_size(LL_L16_FORWARD, X.rows, W.N, X.cols, g.n) : 0, x[0]);
     return enqueue(a, [&] {
         return linear16_nt(X.rows, W.N, X.cols, t, static_cast<uint16_t *>(X.p), X.ld, g.n, g.offsets,
                            static_cast<uint16_t *>(W.p), W.ld, W.stride, bias, act, ty, R.p, R.ld, Y.p, Y.ld,

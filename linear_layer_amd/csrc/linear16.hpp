@@ -50,11 +50,15 @@ enum L16Op : int { L16_FWD = 0, L16_DX = 1, L16_DW = 2 };
 
 // `vec`: every row of 16-bit operands in whole 16-byte pieces, on 16 bytes.
 hipError_t launch_l16_fwd(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
-// The forward product of few rows a group (p.shares of K, through p.ws where more than one);
-// how many shares a workspace is worth, and its bytes.
+// The forward product of few rows a group, and in how many shares of K it gains from a
+// workspace.
 bool l16_takes_rows(int M, int groups);
 int l16_row_shares(int M, int N, int K, int groups, int cus);
-int64_t l16_workspace(int M, int N, int K, int groups, int cus);
+// In how many shares of the contracted axis a product (op: forward or input gradient; M rows, N
+// outputs, K inputs of the layer) gains from a workspace of that many times its result in FP32.
+int l16_shares(int op, int M, int N, int K, int groups, int cus);
+// The shares added in order, and the write-back (after a product in p.shares > 1).
+hipError_t launch_l16_join(bool bf16, const L16Params &p, hipStream_t s);
 hipError_t launch_l16_rows(bool bf16, const L16Params &p, bool vec, int cus, hipStream_t s);
 hipError_t launch_l16_dx(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);
 hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t s);

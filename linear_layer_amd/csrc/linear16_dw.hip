@@ -23,6 +23,15 @@ hipError_t launch_l16_dw(bool bf16, L16Params p, bool vec, int cus, hipStream_t 
     return bf16 ? launch_dw<true, COLS>(p, vec, cus, s) : launch_dw<false, COLS>(p, vec, cus, s);
 }
 
+int l16_shares(int op, int M, int N, int K, int groups, int cus)
+{
+    if (op == L16_DW || M == 0 || N == 0 || K == 0 || groups == 0)
+        return 1;
+    if (op == L16_DX)
+        return rows_shares(M, K, N, groups, cus);
+    return l16_takes_rows(M, groups) ? l16_row_shares(M, N, K, groups, cus) : rows_shares(M, N, K, groups, cus);
+}
+
 const char *l16_kernel_name(int op, int M, int N, int K, int groups, bool vec, int cus)
 {
     if (op == L16_FWD && l16_takes_rows(M, groups))

@@ -299,18 +299,24 @@ int l16_row_shares(int M, int N, int K, int groups, int cus)
     return s < 2 ? 1 : s < 16 ? (int)s : 16;
 }
 
-int64_t l16_workspace(int M, int N, int K, int groups, int cus)
+hipError_t launch_l16_join(bool bf16, const L16Params &p, hipStream_t s)
 {
-    const int s = l16_row_shares(M, N, K, groups, cus);
-    return s > 1 ? (int64_t)s * M * N * 4 : 0;
+    const int tiles_n = cdiv(p.N, kCols);
+    const int64_t grid = (p.groups.offsets == nullptr ? cdiv(p.M, 16) : row_chunks(p.M, p.groups.n, 16)) * tiles_n;
+    if (grid > max_grid_x(128))
+        return hipErrorInvalidValue;
+    if (bf16)
+        hipLaunchKernelGGL(l16_join_kernel<true>, dim3((unsigned)grid), dim3(128), 0, s, p, tiles_n);
+    else
+        hipLaunchKernelGGL(l16_join_kernel<false>, dim3((unsigned)grid), dim3(128), 0, s, p, tiles_n);
+    return hipGetLastError();
 }
 
 template <bool BF16, int MT, int NW>
 static hipError_t launch_nw(const L16Params &p, bool vec, int64_t grid, hipStream_t s)
 {
     const int tiles_n = cdiv(p.N, kCols);
-    const int64_t join = (p.groups.offsets == nullptr ? cdiv(p.M, 16) : row_chunks(p.M, p.groups.n, 16)) * tiles_n;
-    if (grid > max_grid_x(64 * NW) || join > max_grid_x(128))
+    if (grid > max_grid_x(64 * NW))
         return hipErrorInvalidValue;
     const dim3 d((unsigned)grid, (unsigned)p.shares), b(64 * NW);
     constexpr int DEPTH = MT == 1 ? 4 : MT == 2 ? 3 : 2;
@@ -318,9 +324,7 @@ static hipError_t launch_nw(const L16Params &p, bool vec, int64_t grid, hipStrea
         hipLaunchKernelGGL((l16_rows_kernel<BF16, MT, NW, DEPTH>), d, b, 0, s, p, tiles_n);
     else
         hipLaunchKernelGGL((l16_rows_any_kernel<BF16, MT, NW>), d, b, 0, s, p, tiles_n);
-    if (p.shares > 1)
-        hipLaunchKernelGGL(l16_join_kernel<BF16>, dim3((unsigned)join), dim3(128), 0, s, p, tiles_n);
-    return hipGetLastError();
+    return p.shares > 1 ? launch_l16_join(BF16, p, s) : hipGetLastError();
 }
 
 // Four waves, one workgroup a CU, where the CUs are not filled; else two waves and two workgroups,

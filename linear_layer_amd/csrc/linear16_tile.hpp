@@ -233,6 +233,7 @@ __device__ __forceinline__ void tile_at(int id, int tiles_m, int tiles_n, int &t
 struct Job {
     int g, m0, m_end, n0, k_begin, klen;
     int64_t c_off;
+    float *part;    // where a share's sums go instead (M x N), or null
 };
 
 // LDS of a tile: the rings, or the write-back's 64 rows of each wave.
@@ -265,7 +266,7 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
     a.ld = p.lda;
     a.lim = m_end - m0;
     a.klen = b.klen = klen;
-    a.src = SA == ROWS ? p.A + (int64_t)m0 * p.lda : p.A + (int64_t)k_begin * p.lda + m0;
+    a.src = SA == ROWS ? p.A + (int64_t)m0 * p.lda + k_begin : p.A + (int64_t)k_begin * p.lda + m0;
     b.ld = p.ldb;
     b.lim = p.N - n0;
     b.col0 = n0;
@@ -275,7 +276,7 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
         b.lds = p.ldbs;
     } else {
         const uint16_t *w = static_cast<const uint16_t *>(p.B) + (OP == L16_DW ? 0 : (int64_t)g * p.stride_b);
-        b.src = SB == ROWS ? w + (int64_t)n0 * p.ldb : w + (int64_t)k_begin * p.ldb + n0;
+        b.src = SB == ROWS ? w + (int64_t)n0 * p.ldb + k_begin : w + (int64_t)k_begin * p.ldb + n0;
     }
 
     f32x4 acc[FM][FN];
@@ -513,7 +514,7 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
     __syncthreads();                           // nobody reads the ring any more
     float *turn = reinterpret_cast<float *>(lds_bytes) + wave * 64 * PITCH;
     const int rl = lane >> 3, cl = (lane & 7) * 8;
-    const void *more = OP == L16_FWD ? p.R : p.beta != 0.0f ? p.C : nullptr;
+    const void *more = job.part != nullptr ? nullptr : OP == L16_FWD ? p.R : p.beta != 0.0f ? p.C : nullptr;
     const int64_t more_ld = OP == L16_FWD ? p.ldr : p.ldc;
     constexpr int QN = WTN / 64, QUARTERS = WTM / 64 * QN;
 #pragma unroll 1
@@ -564,7 +565,10 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
             for (int u = 0; u < U; ++u) {
                 const int row = row0 + 8 * (q + u);
                 const bool live = WHOLE || (row < m_end && n > 0);
-                if constexpr (OP == L16_FWD) {
+                if (OP != L16_DW && job.part != nullptr) {
+                    if (live)
+                        store_row<LL_TYPE_F32, 8>(job.part + (int64_t)row * p.N + col, WHOLE ? 8 : n, v[u]);
+                } else if constexpr (OP == L16_FWD) {
                     finish_fwd<BF16>(p, v[u], bias, r[u], row, col, WHOLE ? 8 : n, live);
                 } else if (live) {
 #pragma unroll
@@ -594,13 +598,14 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
 // ---- kernels -----------------------------------------------------------------------
 
 // One 128 x 128 tile a workgroup, two workgroups a CU: products that do not fill the CUs with
-// larger ones, and rows off 16 bytes.
+// larger ones, and rows off 16 bytes. With shares (of those whose groups are of C's rows) a
+// workgroup has a part of K, and launch_l16_join adds the parts.
 template <int OP, bool BF16, int SA, int SB, bool VEC>
 __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) l16_small_kernel(L16Params p)
 {
     constexpr int BM = 128, NB = Operand<BF16, BM, SB, VEC>::DMA ? 3 : 2;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[tile_lds<BM, BM, 2, NB>()];
-    Job job{0, 0, p.M, 0, 0, p.K, 0};
+    Job job{0, 0, p.M, 0, 0, p.K, 0, nullptr};
     int tm, tn;
     if constexpr (OP == L16_DW) {
         const int per = p.tiles_m * p.tiles_n, id = block_index(blockIdx.x, per * p.groups.n);
@@ -622,6 +627,12 @@ __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(
         job.g = c.group;
         job.m0 = c.begin + tm * BM;
         job.m_end = c.end;
+        if (p.shares > 1) {   // this one's whole stages of K, which may be none
+            const int each = cdiv(cdiv(p.K, Block::BK), p.shares) * Block::BK;
+            job.k_begin = min(p.K, (int)blockIdx.y * each);
+            job.klen = min(p.K - job.k_begin, each);
+            job.part = p.ws + (int64_t)blockIdx.y * p.M * p.N;
+        }
     }
     job.n0 = tn * BM;
     l16_tile<OP, BF16, BM, BM, 2, 2, NB, SA, SB, VEC>(p, job, lds);
@@ -675,7 +686,7 @@ __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(
         // the tile, and for a piece its half (of the rows) and quarter (of the columns)
         const int piece = id - whole, q = split == 4 ? piece / 2 : piece, cut = split == 1 ? 0 : 2 * left;
         const int tile = piece < 0 ? id : q < cut ? whole + q / 2 : -1;
-        Job job{0, 0, p.M, 0, 0, p.K, 0};
+        Job job{0, 0, p.M, 0, 0, p.K, 0, nullptr};
         int tm = 0, tn = 0;
         if constexpr (OP == L16_DW) {
             const int per = p.tiles_m * p.tiles_n;
@@ -749,6 +760,28 @@ inline bool weight_prefers_large(int M, int N, int rows, int groups, int cus)
            prefer_large(n_large, 0, (int64_t)groups * cdiv(M, 128) * cdiv(N, 128), rows > groups ? cdiv(rows, groups) : 1, cus);
 }
 
+// In how many shares of K such a product takes the least time, by the same measure: a share is
+// eight stages at least, and the join costs four stages' time and the sums' way through memory
+// (1.4 us a stage, 5 bytes a ps).
+inline int rows_shares(int M, int N, int K, int groups, int cus)
+{
+    const int g = groups < M ? groups : M;
+    const int64_t tiles = (int64_t)g * cdiv(cdiv(M, g), 128) * cdiv(N, 128);
+    const int stages = cdiv(K, Block::BK);
+    int64_t s = 2 * cus / tiles;
+    s = s < stages / 8 ? s : stages / 8;
+    s = s < 16 ? s : 16;
+    if (s < 2)
+        return 1;
+    const float bytes = 8.0f * (float)s * (float)M * (float)N;
+    const float shared = 0.62f * ((float)cdiv(stages, (int)s) + 5.0f) + 4.0f + bytes * (1e-6f / 5.0f / 1.4f);
+    const int each = cdiv(M, g), tn = cdiv(N, 256), last = each & 255;
+    float rest;
+    piece_split((int64_t)g * ((each + 127) / 256) * tn, last != 0 && last <= 128 ? (int64_t)g * tn : 0, cus, rest);
+    const float large = rest * ((float)stages + 5.0f) + 4.0f, small = 0.62f * ((float)stages + 5.0f);
+    return shared < large && shared < small ? (int)s : 1;
+}
+
 template <int OP, bool BF16, int SA, int SB>
 hipError_t launch_large(L16Params p, int cus, hipStream_t s)
 {
@@ -766,8 +799,9 @@ hipError_t launch_small(L16Params p, int64_t rows, hipStream_t s)
     const int64_t tiles = rows * p.tiles_n;
     if (tiles > max_grid_x(Block::NT))
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((l16_small_kernel<OP, BF16, SA, SB, VEC>), dim3((unsigned)tiles), dim3(Block::NT), 0, s, p);
-    return hipGetLastError();
+    hipLaunchKernelGGL((l16_small_kernel<OP, BF16, SA, SB, VEC>), dim3((unsigned)tiles, (unsigned)(OP == L16_DW ? 1 : p.shares)),
+                       dim3(Block::NT), 0, s, p);
+    return OP != L16_DW && p.shares > 1 ? launch_l16_join(BF16, p, s) : hipGetLastError();
 }
 
 // The products whose groups are of C's rows. (Every group may end inside a tile.)
@@ -778,7 +812,7 @@ hipError_t launch_rows(const L16Params &p, bool vec, int cus, hipStream_t s)
     const int64_t rows = p.groups.offsets == nullptr ? cdiv(p.M, 128) : (int64_t)(p.M / 128) + g;
     if (!vec)
         return launch_small<OP, BF16, ROWS, SB, false>(p, rows, s);
-    if (rows_prefer_large(p.M, p.N, p.K, p.groups.n, cus))
+    if (p.shares == 1 && rows_prefer_large(p.M, p.N, p.K, p.groups.n, cus))
         return launch_large<OP, BF16, ROWS, SB>(p, cus, s);
     return launch_small<OP, BF16, ROWS, SB, true>(p, rows, s);
 }

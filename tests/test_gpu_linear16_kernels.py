@@ -166,7 +166,7 @@ def test_shares_of_the_inner_dimension(M):
     """With a workspace K is shared out where columns are few; equal bits every time, and NaN in
     the workspace before the call goes nowhere."""
     N, K = 200, 11008
-    need = ll.linear16_workspace_size(M, N, K)
+    need = ll.linear16_workspace_size(ll.L16_FORWARD, M, N, K)
     assert need > 0 and need % (4 * M * N) == 0
     x, w, b = randn(1, M, K), randn(2, N, K, scale=K ** -0.5), randn(3, N, t="f32")
     ws = torch.full((need // 4,), float("nan"), device=DEV)
@@ -182,6 +182,52 @@ def test_shares_of_the_inner_dimension(M):
     assert torch.equal(out[0], out[1])
     with pytest.raises(ll.LinearLayerError):
         ll.linear16_nt(x, w, b, ll.ACT_NONE, None, out[0], workspace=ws[:-1])
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("case", [(16, 4096, 1024, None), (130, 8200, 520, None), (200, 4096, 136, [0, 3, 3, 190, 198]),
+                                  (100, 2047, 333, None)], ids=str)
+def test_tiles_in_shares(case, t):
+    """Products of few tiles in shares of their contracted axis, with their write-back; rows on 16
+    bytes and off them."""
+    M, C, N, groups = case      # rows, contracted, columns of the result
+    G = 1 if groups is None else len(groups) - 1
+    dz = randn(1, M, C, t=t)
+    w, wd = stack(2, groups, C, N, t, C ** -0.5)
+    need = ll.linear16_workspace_size(ll.L16_GRAD_INPUT, M, C, N, G)
+    assert need >= 2 * 4 * M * N
+    ws = torch.full((need // 4,), float("nan"), device=DEV)
+    dx, dx2, dx3 = (torch.full((M, N), 7.0, dtype=TYPES[t], device=DEV) for _ in range(3))
+    s = torch.cuda.current_stream()
+    ll.linear16_grad_input(dz, wd, dx, offsets=offsets_of(groups), workspace=ws)
+    ll.linear16_grad_input(dz, wd, dx2, offsets=offsets_of(groups))
+    ll.linear16_grad_input(dz, wd, dx3, offsets=offsets_of(groups), stream=s)      # whole
+    assert torch.equal(dx, dx2)
+    for g, (a, e) in enumerate(spans_of(groups, M)):
+        for v in (dx, dx3):
+            if e > a:
+                close(v[a:e], *both(dz[a:e], w[g]), C, "dx")
+    outside = torch.ones(M, dtype=torch.bool, device=DEV)
+    for a, e in spans_of(groups, M):
+        outside[a:e] = False
+    assert (dx[outside] == 7).all()
+    if M // G > 64:
+        wt = w.transpose(1, 2).contiguous()
+        assert ll.linear16_workspace_size(ll.L16_FORWARD, M, N, C, G) > 0
+        b, r = randn(3, G, N, t="f32"), randn(4, M, N, t=t)
+        y = torch.full((M, N), 7.0, dtype=TYPES[t], device=DEV)
+        q = tuple(torch.zeros(k, dtype=torch.uint8, device=DEV) for k in ll.mx8_shapes(M, N))
+        ll.linear16_nt(dz, wt if groups else wt[0], b if groups else b[0], ll.ACT_RELU, r, y, Z=q, offsets=offsets_of(groups))
+        z8 = ll.mx8_dequantize(*q, torch.empty((M, N), device=DEV)).double()
+        for g, (a, e) in enumerate(spans_of(groups, M)):
+            z, size = both(dz[a:e], w[g])
+            z, size = z + b[g].double(), size + b[g].double().abs()
+            want = z.clamp(min=0) + r[a:e].double()
+            close(y[a:e], want, size + want.abs(), C + 1, "y")
+            # half a step of each value's own, or of the smallest code under its block's scale
+            err = (C + 1) * STEP * size
+            top = torch.nn.functional.pad(z.abs() + err, (0, -N % 32)).view(e - a, -1, 32).amax(2).repeat_interleave(32, 1)[:, :N]
+            assert ((z8[a:e] - z).abs() <= 2.0 ** -4 * (z.abs() + err) + 2.0 ** -9 * top / 448 + err).all()
 
 
 def step(x, ws, b1, dy, offsets, bufs, beta=0.0):
@@ -204,7 +250,8 @@ def step_buffers(M, D, H, G):
     return {"x8": tuple(e(*s, t=u8) for s in ll.mx8_shapes(M, D)), "z8": tuple(e(*s, t=u8) for s in ll.mx8_shapes(M, H)),
             "h": e(M, H), "y": e(M, D, t=torch.bfloat16), "dw2": e(G, D, H, t=f), "dh": e(M, H), "dz": e(M, H),
             "db1": e(G, H, t=f), "dw1": e(G, H, D, t=f), "dx": e(M, D),
-            "ws": e(max(ll.linear16_grad_act_workspace_size(M, H, G), ll.linear16_workspace_size(M, D, H, G), 16), t=u8)}
+            "ws": e(max(ll.linear16_grad_act_workspace_size(M, H, G), ll.linear16_workspace_size(ll.L16_FORWARD, M, D, H, G),
+                         ll.linear16_workspace_size(ll.L16_GRAD_INPUT, M, D, H, G), 16), t=u8)}
 
 
 OUTPUTS = ("h", "y", "dw2", "dh", "dz", "db1", "dw1", "dx")

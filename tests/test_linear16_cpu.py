@@ -42,11 +42,12 @@ def gact(M=4, N=64, type=BF16, ytype=BF16, act=4, groups=1, ws_bytes=1 << 20, **
                                        ws_bytes, None)
 
 
-def gin(M=4, N=64, K=32, type=BF16, xtype=BF16, groups=1, stride=0, **k):
+def gin(M=4, N=64, K=32, type=BF16, xtype=BF16, groups=1, stride=0, ws_bytes=0, **k):
     k.setdefault("offsets", None)
+    k.setdefault("ws", None)
     p, ld = args(k, {"DZ": max(N, 1), "W": max(K, 1), "DX": max(K, 1)})
     return ll.load().linear16_grad_input(M, N, K, type, p["DZ"], ld["DZ"], groups, p["offsets"], p["W"], ld["W"], stride,
-                                         xtype, p["DX"], ld["DX"], None)
+                                         xtype, p["DX"], ld["DX"], p["ws"], ws_bytes, None)
 
 
 def gw(M=4, N=64, K=32, type=BF16, wtype=BF16, beta=0.0, groups=1, stride=None, **k):
@@ -274,12 +275,22 @@ def test_kernel_names():
             assert k(op, m, n, kk, g) in ("rows", "small", "large")
 
 
-def test_forward_workspace():
-    f = ll.linear16_workspace_size
-    assert f(1, 11008, 4096) == 0 and f(0, 64, 64) == 0 and f(500, 64, 11008) == 0 and f(1, 200, 512) == 0
-    n = f(33, 4096, 11008)
-    assert n > 0 and n % (4 * 33 * 4096) == 0 and 2 <= n // (4 * 33 * 4096) <= 16
+def test_workspaces_of_shares():
+    def f(M, N, K, g=1):
+        return ll.linear16_workspace_size(ll.L16_FORWARD, M, N, K, g)
+
+    def d(M, N, K, g=1):
+        return ll.linear16_workspace_size(ll.L16_GRAD_INPUT, M, N, K, g)
+
+    assert f(1, 11008, 4096) == 0 and f(0, 64, 64) == 0 and f(500, 64, 64) == 0 and f(1, 200, 512) == 0
+    assert f(8192, 8192, 8192) == 0 and d(8192, 8192, 8192) == 0 and d(16, 64, 4096) == 0 and d(16, 0, 64) == 0
+    for n, M, N in ((f(33, 4096, 11008), 33, 4096), (f(130, 1024, 11008), 130, 1024), (d(16, 11008, 4096), 16, 4096)):
+        assert n > 0 and n % (4 * M * N) == 0 and 2 <= n // (4 * M * N) <= 16
     for bad in ((-1, 8, 8), (8, -1, 8), (8, 8, -1), (8, 8, 8, -1), (2 ** 31, 8, 8)):
-        with pytest.raises(ValueError):
-            f(*bad)
-    assert fwd(ws=P["ws"], ws_bytes=-1) == E and fwd(ws=P["ws"] + 4, ws_bytes=1 << 20) == E
+        for g in (f, d):
+            with pytest.raises(ValueError):
+                g(*bad)
+    with pytest.raises(ValueError):
+        ll.linear16_workspace_size(ll.L16_GRAD_WEIGHT, 8, 8, 8)
+    for call in (fwd, gin):
+        assert call(ws=P["ws"], ws_bytes=-1) == E and call(ws=P["ws"] + 4, ws_bytes=1 << 20) == E
