@@ -185,6 +185,27 @@ def test_shares_of_the_inner_dimension(M):
 
 
 @pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [1, 20, 50])
+def test_few_rows_at_each_alignment(M, t):
+    """X and W with rows on two, four and sixteen bytes, each with each, at inner dimensions that
+    end inside a load; the values around the rows are NaN and reach nothing."""
+    N = 70
+    for K in (8, 197, 200, 1001):
+        x, w = randn(1, M, K, t=t), randn(2, N, K, t=t)
+        want, size = both(x, w.t())
+        for px, sx, pw, sw in ((1, 1, 1, 0), (0, 1, 2, 2), (2, 0, 3, 1), (4, 2, 0, 0), (1, 0, 8 + -K % 8, 0), (-K % 8, 0, 1, 3)):
+            def laid(a, pad, shift):
+                buf = torch.full((a.shape[0] * (K + pad) + shift + 8,), float("nan"), dtype=TYPES[t], device=DEV)
+                v = torch.as_strided(buf, a.shape, (K + pad, 1), shift)
+                v.copy_(a)
+                return v
+            xs, ws = laid(x, px, sx), laid(w, pw, sw)
+            y = torch.empty((M, N), device=DEV)
+            ll.linear16_nt(xs, ws, None, 0, None, y)
+            close(y, want, size, K, "K %d X +%d@%d W +%d@%d" % (K, px, sx, pw, sw))
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
 @pytest.mark.parametrize("case", [(16, 4096, 1024, None), (130, 8200, 520, None), (200, 4096, 136, [0, 3, 3, 190, 198]),
                                   (100, 2047, 333, None)], ids=str)
 def test_tiles_in_shares(case, t):
