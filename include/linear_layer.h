@@ -280,7 +280,7 @@ int gemm_bf16f32_batched(int trans_b, int M, int N, int K, float alpha,
  * alignment.
  */
 
-/* Element types of mx4_quantize, mx4_dequantize and the residual norms. */
+/* Element types of the microscaled formats, the residual norms and the 16-bit layer. */
 #define LL_TYPE_F32 0
 #define LL_TYPE_F16 1
 #define LL_TYPE_BF16 2
@@ -519,8 +519,9 @@ int linear16_nt(int M, int N, int K, int type, const uint16_t *X, int ldx,
                 void *workspace, int64_t workspace_bytes, void *stream);
 /* product: LL_L16_FORWARD or LL_L16_GRAD_INPUT; -1 for another or a negative size. */
 int64_t ll_linear16_workspace_size(int product, int M, int N, int K, int groups);
-/* Name of the kernel that a product takes on a device with num_cus compute units
- * (num_cus <= 0: 256), with rows on 16 bytes (`aligned`) or not: "rows" and
+/* Name of the kernel that a product without a workspace (with one that shares K out:
+ * "rows" and "rows_any", else "small" and "small_any") takes on a device with num_cus
+ * compute units (num_cus <= 0: 256), with rows on 16 bytes (`aligned`) or not: "rows" and
  * "rows_any" (forward, at most 64 rows a group on average), "small" and
  * "small_any" (tiles of 128 x 128), "large" (256 x 256 and pieces of them); "" for one
  * without work or a bad argument. Static string. */

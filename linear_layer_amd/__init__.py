@@ -81,7 +81,7 @@ ACT_GELU, ACT_GELU_TANH, ACT_SILU = 2, 3, 4   # of linear16_nt and linear16_grad
 MAX_GROUPS = 1 << 20   # of rows, in the linear16 calls
 L16_FORWARD, L16_GRAD_INPUT, L16_GRAD_WEIGHT = 0, 1, 2   # products of linear16_chosen_kernel
 DTYPE_F32, DTYPE_F16 = 0, 1
-TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2   # element types of mx4_quantize, mx4_dequantize and the residual norms
+TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2   # element types of the microscaled formats, the norms and the 16-bit layer
 A_MX4, A_F16, A_BF16 = 0, 1, 2   # the forms of A of the 4-bit products
 PLAN_RELU, PLAN_B_NK, PLAN_UNALIGNED = 0x100, 0x200, 0x400   # flags OR-ed into dtype for chosen_*
 NOALLOC_SCRATCH_BYTES = 65 << 20   # the static workspace of linear_bias_act_noalloc

@@ -24,6 +24,13 @@
 // of a row; the write-back turns them around in LDS to eight a lane, 128 bytes of a row (16
 // bits) in one store instruction, which is also the order that R and bias are read in and
 // in which four lanes hold one block of 32 of Z's 8 bits.
+//
+// Large products are bound by the matrix cores and the power they may draw: bfloat16 8192^3
+// takes 0.76 to 0.82 ms forward (1.34 to 1.46 PFLOP/s), 0.77 for dX (1.43), 0.79 for dW (1.39) and
+// 0.85 to 0.89 with X in 8 bits (1.24 to 1.29), where the library's forward product on the same
+// inputs reaches 1.61 and its product on other than rows 1.38. What else was measured there:
+// operands through registers instead of copies 1.23 to 1.33 PFLOP/s, eight waves of 128 x 64
+// instead of four of 128 x 128 1.33, workgroups set apart over K no gain.
 #pragma once
 
 #include "launch.hpp"
@@ -599,7 +606,8 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
 
 // One 128 x 128 tile a workgroup, two workgroups a CU: products that do not fill the CUs with
 // larger ones, and rows off 16 bytes. With shares (of those whose groups are of C's rows) a
-// workgroup has a part of K, and launch_l16_join adds the parts.
+// workgroup has a part of K, and launch_l16_join adds the parts (dX of 16 x 11008 x 4096 82 us
+// whole, 24 in shares).
 template <int OP, bool BF16, int SA, int SB, bool VEC>
 __global__ void __launch_bounds__(Block::NT) __attribute__((amdgpu_waves_per_eu(2, 2))) l16_small_kernel(L16Params p)
 {
@@ -762,7 +770,9 @@ inline bool weight_prefers_large(int M, int N, int rows, int groups, int cus)
 
 // In how many shares of K such a product takes the least time, by the same measure: a share is
 // eight stages at least, and the join costs four stages' time and the sums' way through memory
-// (1.4 us a stage, 5 bytes a ps).
+// (1.4 us a stage, 5 bytes a ps). Whole and shared: 16 x 1024 over 4096 12.9 and 12.5 us, 130 x 72
+// over 1000 14.8 and 13.2, 512 x 4096 over 4096 38 and 34, 129 x 128 over 16384 120 and 19; whole by the
+// rule at 1024 x 4096 over 4096 and 512 x 4096 over 1024.
 inline int rows_shares(int M, int N, int K, int groups, int cus)
 {
     const int g = groups < M ? groups : M;

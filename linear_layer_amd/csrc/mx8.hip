@@ -1,6 +1,8 @@
 // Microscaled 8-bit floating point, there and back, and the gradient of the layer's
 // activation, which can read its input from it. All are bound by HBM: a lane takes 8 values
-// (16 or 32 bytes, 8 of codes), four neighbouring lanes make a block of 32.
+// (16 or 32 bytes, 8 of codes), four neighbouring lanes make a block of 32. 8192 x 8192 bfloat16
+// there and back: 82 us for 338 MB (4.1 TB/s); the gradient with its sums of 8191 x 4096: 49 us
+// for 169 MB (3.4 TB/s).
 #include "linear16.hpp"
 #include "launch.hpp"
 
