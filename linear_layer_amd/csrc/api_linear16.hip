@@ -103,7 +103,7 @@ int mx8_dequantize(int M, int K, const uint8_t *codes, int ldq, const uint8_t *s
 const char *ll_linear16_chosen_kernel(int product, int M, int N, int K, int groups, int aligned, int num_cus)
 {
     if (product < LL_L16_FORWARD || product > LL_L16_GRAD_WEIGHT || M <= 0 || N <= 0 || K <= 0 || groups <= 0 ||
-        groups > LL_MAX_GROUPS)
+        groups > LL_MAX_GROUPS || M > kL16Most || N > kL16Most || K > kL16Most)
         return "";
     return l16_kernel_name(product, M, N, K, groups, aligned != 0, num_cus > 0 ? num_cus : 256);
 }
@@ -113,6 +113,8 @@ int64_t ll_linear16_workspace_size(int product, int M, int N, int K, int groups)
     if ((product != LL_L16_FORWARD && product != LL_L16_GRAD_INPUT) || M < 0 || N < 0 || K < 0 || groups < 0 ||
         groups > LL_MAX_GROUPS)
         return -1;
+    if (M > kL16Most || N > kL16Most || K > kL16Most)   // (which no product takes)
+        return 0;
     const Device dev = current_device();
     const int cus = dev.status == LL_OK ? dev.cus : 256;
     return shares_bytes(l16_shares(product, M, N, K, groups, cus), M, product == LL_L16_FORWARD ? N : K);

@@ -294,3 +294,18 @@ def test_workspaces_of_shares():
         ll.linear16_workspace_size(ll.L16_GRAD_WEIGHT, 8, 8, 8)
     for call in (fwd, gin):
         assert call(ws=P["ws"], ws_bytes=-1) == E and call(ws=P["ws"] + 4, ws_bytes=1 << 20) == E
+
+
+def test_sizes_no_product_takes():
+    most = 2 ** 31 - 1025
+    for big in (most + 1, 2 ** 31 - 1):
+        for shape in ((big, 8, 8), (8, big, 8), (8, 8, big), (big, big, big)):
+            for product in (ll.L16_FORWARD, ll.L16_GRAD_INPUT, ll.L16_GRAD_WEIGHT):
+                assert ll.linear16_chosen_kernel(product, *shape) == ""
+            assert ll.linear16_workspace_size(ll.L16_FORWARD, *shape) == 0
+            assert ll.linear16_workspace_size(ll.L16_GRAD_INPUT, *shape) == 0
+    for shape in ((most, 8, 8), (8, most, 8), (8, 8, most), (most, most, most)):
+        for product in (ll.L16_FORWARD, ll.L16_GRAD_INPUT, ll.L16_GRAD_WEIGHT):
+            assert ll.linear16_chosen_kernel(product, *shape) != ""
+        for product in (ll.L16_FORWARD, ll.L16_GRAD_INPUT):
+            assert ll.linear16_workspace_size(product, *shape) in (0, 16 * 4 * 8 * 8)
