@@ -1,8 +1,8 @@
 // Microscaled 8-bit floating point, there and back, and the gradient of the layer's
 // activation, which can read its input from it. All are bound by HBM: a lane takes 8 values
 // (16 or 32 bytes, 8 of codes), four neighbouring lanes make a block of 32. 8192 x 8192 bfloat16
-// there and back: 82 us for 338 MB (4.1 TB/s); the gradient with its sums of 8191 x 4096: 49 us
-// for 169 MB (3.4 TB/s).
+// there and back: 82 us for 338 MB (4.1 TB/s); the gradient with its sums of 8191 x 4096: 47 us
+// for 169 MB (3.6 TB/s).
 #include "linear16.hpp"
 #include "launch.hpp"
 
@@ -253,13 +253,13 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradParams p, int step
     }
 }
 
-// A group's chunks added up: 64 columns by 16 shares of the chunks, then the shares in order.
-constexpr int kJoinShares = 16;
-
-__global__ void __launch_bounds__(64 * kJoinShares) act_join_kernel(const float *part, float *dbias, Groups groups, int M,
+// A group's chunks added up: 64 columns by SHARES of the chunks, then the shares in order. (Of 16
+// groups of 8191 rows, 9 chunks each, with 16 shares 51.0 us in all, with 4 46.8.)
+template <int SHARES>
+__global__ void __launch_bounds__(64 * SHARES) act_join_kernel(const float *part, float *dbias, Groups groups, int M,
                                                                     int N, int step, int strips)
 {
-    __shared__ float red[kJoinShares][64];
+    __shared__ float red[SHARES][64];
     Chunk c{0, 0, 0, 0, 0};
     const int g = blockIdx.x / strips;
     find_chunk<true>(groups, M, step, g, c);
@@ -268,14 +268,14 @@ __global__ void __launch_bounds__(64 * kJoinShares) act_join_kernel(const float 
     float sum = 0.0f;
     if (col < N) {
 #pragma unroll 8
-        for (int i = share; i < c.index; i += kJoinShares)
+        for (int i = share; i < c.index; i += SHARES)
             sum += part[(int64_t)(c.group_first + i) * N + col];
     }
     red[share][threadIdx.x % 64] = sum;
     __syncthreads();
     if (share == 0 && col < N) {
 #pragma unroll
-        for (int i = 1; i < kJoinShares; ++i)
+        for (int i = 1; i < SHARES; ++i)
             sum += red[i][threadIdx.x];
         dbias[(int64_t)g * N + col] = sum;
     }
@@ -290,7 +290,7 @@ static hipError_t launch_act_grad_t(const ActGradParams &p, hipStream_t s)
     const int step = act_step(p.M, p.N), strips = cdiv(p.N, lpr * 8);
     const int64_t chunks = p.groups.offsets == nullptr ? cdiv(p.M, step) : act_chunks(p.M, p.N, p.groups.n);
     const int64_t grid = chunks * strips;
-    if (grid > max_grid_x(256) || (int64_t)p.groups.n * cdiv(p.N, 64) > max_grid_x(64 * kJoinShares))
+    if (grid > max_grid_x(256) || (int64_t)p.groups.n * cdiv(p.N, 64) > max_grid_x(1024))
         return hipErrorInvalidValue;
     if (grid > 0) {
         const dim3 d((unsigned)grid);
@@ -301,9 +301,13 @@ static hipError_t launch_act_grad_t(const ActGradParams &p, hipStream_t s)
         else
             hipLaunchKernelGGL((act_grad_kernel<BF16, DYT, Z_8>), d, dim3(256), 0, s, p, step, lpr, strips);
     }
-    if (p.dbias != nullptr)
-        hipLaunchKernelGGL(act_join_kernel, dim3((unsigned)(p.groups.n * cdiv(p.N, 64))), dim3(64 * kJoinShares), 0, s,
-                           p.part, p.dbias, p.groups, p.M, p.N, step, cdiv(p.N, 64));
+    if (p.dbias != nullptr) {
+        const dim3 d((unsigned)(p.groups.n * cdiv(p.N, 64)));
+        if (chunks > (int64_t)16 * p.groups.n)
+            hipLaunchKernelGGL(act_join_kernel<16>, d, dim3(1024), 0, s, p.part, p.dbias, p.groups, p.M, p.N, step, cdiv(p.N, 64));
+        else
+            hipLaunchKernelGGL(act_join_kernel<4>, d, dim3(256), 0, s, p.part, p.dbias, p.groups, p.M, p.N, step, cdiv(p.N, 64));
+    }
     return hipGetLastError();
 }
 
