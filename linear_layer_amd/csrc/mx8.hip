@@ -165,7 +165,7 @@ hipError_t launch_mx8_dequantize(int type, const uint8_t *codes, int64_t ldq, co
 // its 256 / lpr rows at a time from kActRows loads of each in flight; its column sums go to
 // `part`, a row for every chunk, and a second launch adds a group's chunks in order. (Atomics
 // would add them in any order.) Two rows in flight a thread and five waves a SIMD: 8191 x 4096 with Z
-// in 8 bits 52 us (3.3 TB/s); four rows and three waves 71.
+// in 8 bits 47 us with the second launch (3.6 TB/s); four rows and three waves 71.
 constexpr int kActRows = 2;
 
 // Rows of a chunk: 64 (the partial sums then are 1/32 of dZ's bytes); 16 where that leaves CUs
