@@ -127,11 +127,13 @@ struct Operand {
             for (int v = 0; v < SETS; ++v)
                 cur[v] = SIDE == ROWS && slot_col(v * C::NT + tid) >= left ? kPastEnd : off[v];
         } else if constexpr (VEC && SIDE == COLS8) {
-            // (codes past a row's end are the next row's, or padding: of columns that are not stored)
+            // Codes past a row's end are the next row's, or padding: of columns that are not stored. A load is
+            // checked word by word, and a word that is partly past the buffer's end arrives as zero, so the
+            // last row ends with its last column's word (rows are whole words: it has no other row's bytes).
             const int left = min(klen - k0, C::BK), n = min(lim, BM);
             const int last = (col0 + n - 1) >> 5;   // scale of the last column
             codes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(src8 + (int64_t)k0 * ld), 0,
-                                                      left <= 0 ? 0 : (left - 1) * (int)ld + n, 0x00020000);
+                                                      left <= 0 ? 0 : (left - 1) * (int)ld + ((n + 3) & ~3), 0x00020000);
             scale_bytes = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t *>(scales + (int64_t)k0 * lds), 0,
                                                             left <= 0 ? 0 : (left - 1) * (int)lds + last + 1, 0x00020000);
         }
