@@ -115,7 +115,7 @@ __device__ __forceinline__ void finish_fwd(const L16Params &p, float (&v)[8], co
         return;
     if (p.Z != nullptr)
         store_row<kType16<BF16>, 8>(p.Z + row * p.ldz + col, n, v);
-    with_activation(p.act, [&](auto kind) __attribute__((always_inline)) {
+    with_activation(act_for(p.act, p.ctype == LL_TYPE_F32), [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             v[e] = activate<decltype(kind)::value>(v[e]);

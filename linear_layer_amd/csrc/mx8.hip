@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(256) act_grad_kernel(ActGradParams p, int step
                 mx8_decode4((uint32_t)(codes[i] >> 32), scale[i], z[i] + 4);
             }
         }
-        if constexpr (ZF != Z_NONE)
-            with_activation(p.act, [&](auto kind) __attribute__((always_inline)) {
+        if constexpr (ZF != Z_NONE)   // (the sums are FP32, dZ is not)
+            with_activation(act_for(p.act, p.part != nullptr), [&](auto kind) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < kActRows; ++i)
 #pragma unroll

@@ -1,6 +1,8 @@
-"""The 16-bit layer at its edges: codes whose rows end inside a word. References in float64 on
+"""The 16-bit layer at its edges: codes whose rows end inside a word, GELU to FP32. References in float64 on
 the device by torch. Tolerances as in test_gpu_linear16: a sum of n products is off by at most
 n steps of 2^-23 of the sum of their magnitudes, and stored with half a step of its type."""
+import math
+
 import pytest
 
 import linear16_reference as ref
@@ -77,3 +79,52 @@ def test_weight_gradient_from_codes_that_end_inside_a_word(shape, t):
     ll.linear16_grad_weight(dz, q, dw if groups else dw[0], offsets=offsets_of(groups))
     for g, (a, e) in enumerate(spans):
         close(dw[g], *both(dz[a:e], xr[a:e]), M, "dw")
+
+
+H32 = 2.0 ** -24
+
+
+def gelu_grid():
+    """Normal values, and all of [-12, 12]; and where the normal ones end."""
+    z = torch.cat([randn(7, 50000, t="f32"), torch.linspace(-12, 12, 48001, device=DEV), torch.zeros(7, device=DEV)])
+    return z, 50000
+
+
+def parts(z):
+    """The normal distribution function, and its density times |z|, in 64 bits."""
+    return 0.5 * torch.erfc(-z / math.sqrt(2)), z.abs() * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+
+
+@pytest.mark.parametrize("M", [1, 130])
+def test_gelu_to_fp32(M):
+    """Z is the bias alone. From -1 on: the function is 1/2 + z P or 1 - h, six half-steps with the product; on
+    the negative side h's operations are ten of its own and its exponent's three at z^2 / 2 each.
+    In the norm two roundings of at most half a step, evenly spread: 0.82 half-steps."""
+    z, normal = gelu_grid()
+    y = torch.empty((M, z.numel()), device=DEV)
+    zeros = torch.zeros((max(M, z.numel()), 8), device=DEV).bfloat16()
+    ll.linear16_nt(zeros[:M], zeros[:z.numel()], z, ll.ACT_GELU, None, y)
+    zd = z.double()
+    want = zd * parts(zd)[0]
+    tol = H32 * want.abs() * torch.where(zd >= -1, 6.0, 10 + 2 * zd * zd)
+    off = (y.double() - want).abs()
+    assert (off <= tol).all(), (off / tol).nan_to_num().max()
+    rms = (off[:, :normal].norm() / want[:normal].expand(M, -1).norm()).item()
+    assert rms <= H32, rms
+
+
+@pytest.mark.parametrize("ty", ["f16", "f32"])
+def test_gelu_slope_to_fp32(ty):
+    """The bias's gradient of one row is its slope. The function as above, the density's part six half-steps and its
+    exponent's, and their sum."""
+    z = gelu_grid()[0].half()[None]
+    dy = torch.ones_like(z).to(TYPES[ty])
+    db = torch.empty(z.shape[1], device=DEV)
+    dz = ll.linear16_grad_act(dy, z, ll.ACT_GELU, torch.empty_like(z), db)
+    zd = z[0].double()
+    c, d = parts(zd)
+    want = c + torch.where(zd < 0, -d, d)
+    tol = H32 * torch.where(zd >= -1, 6 * c + (6 + 2 * zd * zd) * d, (10 + 2 * zd * zd) * (c + d))
+    off = (db.double() - want).abs()
+    assert (off <= tol).all(), (off / tol).max()
+    assert ((dz[0].double() - want).abs() <= tol + 2.0 ** -11 * want.abs() + 2.0 ** -25).all()
