@@ -54,8 +54,22 @@ __device__ __forceinline__ void mma_acc(const f16x8 &a, const f16x8 &b, f32x4 &c
         asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 // The wait between mma_acc and what else reads its sums (18 wait states at most), and between what
-// wrote them and the first mma_acc.
-__device__ __forceinline__ void settle() { asm volatile("s_nop 15\n\ts_nop 7" ::: "memory"); }
+// wrote them and the first mma_acc. The empty statements before and after it take the sums and give them
+// on, so that the compiler can move none of their writes behind it and none of their reads ahead of it.
+template <int FM, int FN>
+__device__ __forceinline__ void settle(f32x4 (&acc)[FM][FN])
+{
+    const auto tie = [&acc]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                asm volatile("" : "+a"(acc[i][j]));
+    };
+    tie();
+    asm volatile("s_nop 15\n\ts_nop 7" ::: "memory");
+    tie();
+}
 
 // A workgroup: 2 x 2 waves, each with a quarter of its tile; stages of two steps of the MFMA.
 struct Block {
@@ -437,7 +451,7 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
         });
     };
     if constexpr (WPE == 1)
-        settle();
+        settle(acc);
     // the buffers of stages kt, kt + 1, and of the last one that is on its way
     int bufa = 0, nexta = 1, lasta = NA - 1, bufb = 0, nextb = 1, lastb = NB - 1;
     for (int kt = 0; kt < nk; ++kt) {
@@ -512,7 +526,7 @@ __device__ __forceinline__ void l16_tile(const L16Params &p, const Job &job, uin
         lasta = NA == 3 ? donea : nexta, lastb = NB == 3 ? doneb : nextb;
     }
     if constexpr (WPE == 1)
-        settle();
+        settle(acc);
 
     // The write-back, 64 x 64 of the wave's block at a time through its own part of the LDS,
     // a quarter of those rows a turn of a loop: what depends on the quarter is its stores
