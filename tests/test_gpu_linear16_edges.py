@@ -128,3 +128,175 @@ def test_gelu_slope_to_fp32(ty):
     off = (db.double() - want).abs()
     assert (off <= tol).all(), (off / tol).max()
     assert ((dz[0].double() - want).abs() <= tol + 2.0 ** -11 * want.abs() + 2.0 ** -25).all()
+
+
+def test_kept_8_bits_are_the_formats_of_the_calls_own_sums():
+    """Z in 8 bits is to the bit what mx8_quantize makes of the same call's FP32 sums, and a call repeats itself:
+    what another order of sums gives differs from it only where a sum lies next to a border between codes."""
+    M, N, K = 2047, 11008, 4096
+    assert ll.linear16_chosen_kernel(ll.L16_FORWARD, M, N, K) == "large"
+    x, w, b = randn(1, M, K), randn(2, N, K, scale=K ** -0.5), randn(3, N, t="f32", scale=0.2)
+    z = torch.empty((M, N), device=DEV)
+    ll.linear16_nt(x, w, b, ll.ACT_NONE, None, z)
+    want = tuple(torch.empty(s, dtype=torch.uint8, device=DEV) for s in ll.mx8_shapes(M, N))
+    ll.mx8_quantize(z, *want)
+    first = None
+    for i in range(5):
+        y = torch.full((M, N), float("nan"), device=DEV).bfloat16()
+        q = tuple(torch.full(s, 0x7F - i, dtype=torch.uint8, device=DEV) for s in ll.mx8_shapes(M, N))
+        ll.linear16_nt(x, w, b, ll.ACT_GELU, None, y, Z=q)
+        assert torch.equal(q[0], want[0]) and torch.equal(q[1], want[1])
+        assert first is None or torch.equal(y, first)
+        first = y
+    # (the order of sums of the library's FP32 product)
+    other = tuple(torch.empty(s, dtype=torch.uint8, device=DEV) for s in ll.mx8_shapes(M, N))
+    zo = torch.matmul(x.float(), w.float().t()) + b
+    ll.mx8_quantize(zo, *other)
+    va, vb = (ll.mx8_dequantize(*q, torch.empty((M, N), device=DEV)).double() for q in (want, other))
+    differ = va != vb
+    size = (x.double().abs() @ w.double().abs().t() + b.double().abs())[differ]
+    exact = (x.double() @ w.double().t() + b.double())[differ]
+    border = ((va + vb) / 2)[differ]
+    assert ((exact - border).abs() <= (K + 1) * STEP * size).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("shape", [(512, 304, 272, 272, None, "small"), (300, 136, 208, 208, [0, 3, 250, 300], "small"),
+                                   (1000, 136, 200, 208, [5, 5, 390, 999], "small"), (512, 304, 264, 264, None, "small_any"),
+                                   (300, 136, 200, 200, [0, 3, 250, 300], "small_any"), (500, 135, 256, 256, None, "small_any"),
+                                   (1032, 6400, 2000, 2000, None, "large")], ids=str)
+def test_weight_gradient_from_codes_by_kernel(shape, t):
+    """Each kernel over many stages, named by the operands' own alignment; a block that is NaN makes its columns of its
+    group NaN and no others, any code under the scale byte 255 among them."""
+    M, N, K, ld, groups, kernel = shape
+    dz, x = randn(1, M, N, t=t), randn(2, M, K, t=t)
+    q, xr = in_8_bits(x, ld)
+    assert weight_kernel(dz, q, groups) == kernel
+    spans = ref.bounds(groups, M)
+    before = randn(3, len(spans), N, K, t="f32")
+    dw = before.clone()
+
+    def call(q):
+        ll.linear16_grad_weight(dz, q, dw if groups else dw[0], beta=1.0, offsets=offsets_of(groups))
+
+    call(q)
+    clean = dw.clone()
+    for g, (a, e) in enumerate(spans):
+        want, size = both(dz[a:e], xr[a:e])
+        close(dw[g], want + before[g].double(), size + before[g].double().abs(), e - a + 1, "dw")
+    a = spans[-1][0] + 7                      # a row of the last group, its blocks 1 and the last
+    q[1][a, 1] = q[1][a, -1] = 255
+    dw.copy_(before)
+    call(q)
+    nan = torch.zeros(K, dtype=torch.bool, device=DEV)
+    nan[32:64] = nan[(K - 1) // 32 * 32:] = True
+    assert dw[-1][:, nan].isnan().all() and torch.equal(dw[-1][:, ~nan], clean[-1][:, ~nan])
+    assert torch.equal(dw[:-1], clean[:-1])
+
+
+@pytest.mark.parametrize("M", [900, 7000])
+def test_gradients_of_many_groups(M):
+    """Five thousand groups, most of them empty or of a row."""
+    G, N, K = 5000, 40, 64
+    r = torch.Generator().manual_seed(M)
+    off = torch.cat([torch.tensor([0, M - 3]), torch.randint(0, M - 3, (G - 1,), generator=r)]).sort().values.to(torch.int32).to(DEV)
+    group = torch.searchsorted(off[1:].long(), torch.arange(M - 3, device=DEV), right=True)
+    dz, x, w = randn(1, M, N), randn(2, M, K), randn(3, G, N, K)
+    for op in (ll.L16_GRAD_INPUT, ll.L16_GRAD_WEIGHT):
+        assert ll.linear16_chosen_kernel(op, M, N, K, G) == "small"
+    dx = torch.full((M, K), 7.0, device=DEV)
+    ll.linear16_grad_input(dz, w, dx, offsets=off)
+    d = dz[:-3].double()[:, None]
+    close(dx[:-3], torch.matmul(d, w[group].double())[:, 0], torch.matmul(d.abs(), w[group].double().abs())[:, 0], N, "dx")
+    assert (dx[-3:] == 7).all()
+    outer = dz[:-3].double()[:, :, None] * x[:-3].double()[:, None, :]
+    want, size = (torch.zeros((G, N, K), dtype=torch.float64, device=DEV).index_add_(0, group, v) for v in (outer, outer.abs()))
+    most = int(torch.bincount(group).max())
+    dw = torch.full((G, N, K), float("nan"), device=DEV)
+    ll.linear16_grad_weight(dz, x, dw, offsets=off)
+    close(dw, want, size, most, "dw")
+    db, out = torch.full((G, N), float("nan"), device=DEV), torch.full((M, N), 7.0, device=DEV).bfloat16()
+    ll.linear16_grad_act(dz, x[:, :N].contiguous(), ll.ACT_RELU, out, db, offsets=off)
+    slope = (x[:-3, :N] > 0).double()
+    v = dz[:-3].double() * slope
+    assert torch.equal(out[:-3].double(), v) and (out[-3:] == 7).all()
+    want, size = (torch.zeros((G, N), dtype=torch.float64, device=DEV).index_add_(0, group, u) for u in (v, v.abs()))
+    close(db, want, size, most, "dbias")
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("align", [16, 4, 2])
+@pytest.mark.parametrize("case", [(1, 200, 4097, None), (33, 130, 8200, None), (64, 72, 4104, None), (2, 64, 8192, [0, 1, 2]),
+                                  (70, 200, 8200, [3, 20, 20, 61]), (120, 64, 4104, [0, 64, 120])], ids=str)
+def test_few_rows_in_shares(case, align, t):
+    """Few rows a group, the inner dimension in shares, with all of the write-back; rows on 16, 4 and 2 bytes."""
+    M, N, K, groups = case
+    if align == 16:
+        K = K // 8 * 8
+    G = 1 if groups is None else len(groups) - 1
+    assert ll.linear16_chosen_kernel(ll.L16_FORWARD, M, N, K, G, align == 16) == ("rows" if align == 16 else "rows_any")
+    need = ll.linear16_workspace_size(ll.L16_FORWARD, M, N, K, G)
+    assert need >= 2 * 4 * M * N
+    # rows that begin and lie 16, 4 and 2 bytes apart, NaN around them
+    shift, ld = {16: (0, K + 8), 4: (2, (K + 5) // 4 * 4 + 2), 2: (1, K + 2 + K % 2 + 1)}[align]
+
+    def laid(a):
+        v = torch.full((*a.shape[:-1], ld), float("nan"), dtype=a.dtype, device=DEV)[..., shift:shift + K]
+        v.copy_(a)
+        return v
+
+    x, w = laid(randn(1, M, K, t=t)), laid(randn(2, G, N, K, t=t, scale=K ** -0.5))
+    for v in (x, w):
+        assert (v.data_ptr() | 2 * v.stride(-2)) % 16 % (2 * align) == align % 16
+    b, r = randn(3, G, N, t="f32"), randn(4, M, N, t=t)
+    ws = torch.full((need // 4,), float("nan"), device=DEV)
+    y = torch.full((M, N), 7.0, dtype=TYPES[t], device=DEV)
+    q = tuple(torch.full(s, 0xA5, dtype=torch.uint8, device=DEV) for s in ll.mx8_shapes(M, N))
+    off = offsets_of(groups)
+    ll.linear16_nt(x, w if groups else w[0], b if groups else b[0], ll.ACT_RELU, r, y, Z=q, offsets=off, workspace=ws)
+    y2 = torch.full_like(y, 7.0)
+    ll.linear16_nt(x, w if groups else w[0], b if groups else b[0], ll.ACT_RELU, r, y2, offsets=off)
+    assert torch.equal(y, y2)
+    outside = torch.ones(M, dtype=torch.bool, device=DEV)
+    values = ll.mx8_dequantize(*q, torch.empty((M, N), device=DEV)).double()
+    for g, (a, e) in enumerate(ref.bounds(groups, M)):
+        outside[a:e] = False
+        if a == e:
+            continue
+        z, size = both(x[a:e].t(), w[g].t())
+        z, size = z + b[g].double(), size + b[g].double().abs()
+        want = z.clamp(min=0) + r[a:e].double()
+        close(y[a:e], want, size + want.abs(), K + 2, "y")
+        err = (K + 1) * STEP * size
+        top = torch.nn.functional.pad(z.abs() + err, (0, -N % 32)).view(e - a, -1, 32).amax(2).repeat_interleave(32, 1)[:, :N]
+        assert ((values[a:e] - z).abs() <= 2.0 ** -4 * (z.abs() + err) + 2.0 ** -9 * top / 448 + err).all()
+    assert (y[outside] == 7).all() and (q[0][outside] == 0xA5).all() and (q[1][outside] == 0xA5).all()
+
+
+@pytest.mark.parametrize("act", ["relu", "gelu", "silu"])
+@pytest.mark.parametrize("groups", [None, [2, 30, 30, 97]])
+@pytest.mark.parametrize("eight", [False, True])
+def test_bias_gradient_alone(act, groups, eight):
+    """The C call without DZ: the sums are to the bit those of the call that writes it."""
+    M, N = 100, 203
+    dy, z = randn(1, M, N), randn(2, M, N)
+    G = 1 if groups is None else len(groups) - 1
+    off = offsets_of(groups)
+    held, zq = z, (None, None)
+    if eight:
+        held = zq = tuple(torch.empty(s, dtype=torch.uint8, device=DEV) for s in ll.mx8_shapes(M, N))
+        ll.mx8_quantize(z, *zq)
+    kind = getattr(ll, "ACT_" + act.upper())
+    want = torch.empty((G, N) if groups else (N,), device=DEV)
+    ll.linear16_grad_act(dy, held, kind, torch.empty_like(dy), want, offsets=off)
+    got = torch.full_like(want, float("nan"))
+    ws = torch.empty(ll.linear16_grad_act_workspace_size(M, N, G), dtype=torch.uint8, device=DEV)
+
+    def at(v):
+        return None if v is None else v.data_ptr()
+
+    status = ll.load().linear16_grad_act(M, N, ll.TYPE_BF16, kind, ll.TYPE_BF16, at(dy), N, G, at(off), None if eight else at(z), N,
+                                         at(zq[0]), N, at(zq[1]), (N + 31) // 32, None, N, at(got), at(ws), ws.numel(),
+                                         torch.cuda.current_stream().cuda_stream)
+    assert status == ll.OK
+    assert torch.equal(got, want)
