@@ -887,12 +887,20 @@ def _workspace(t):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _c_ints(*numbers):
+    """Numbers as the calls take them. (ctypes would pass on the lower 32 bits of others.)"""
+    got = tuple(int(n) for n in numbers)
+    if any(not -_INT_MAX <= n <= _INT_MAX for n in got):
+        raise ValueError(f"the calls take numbers up to {_INT_MAX}, got {got}")
+    return got
+
+
 def linear16_workspace_size(product: int, M: int, N: int, K: int, groups: int = 1) -> int:
     """Bytes of workspace that linear16_nt (L16_FORWARD) or linear16_grad_input
     (L16_GRAD_INPUT) gains from on the current device (0: none)."""
-    if max(M, N, K) > _INT_MAX or groups > MAX_GROUPS:
-        raise ValueError(f"the calls take sizes up to {_INT_MAX} and {MAX_GROUPS} groups")
-    n = load().ll_linear16_workspace_size(int(product), int(M), int(N), int(K), int(groups))
+    if groups > MAX_GROUPS:
+        raise ValueError(f"the calls take up to {MAX_GROUPS} groups")
+    n = load().ll_linear16_workspace_size(*_c_ints(product, M, N, K, groups))
     if n < 0:
         raise ValueError("negative size, or a product that takes no workspace")
     return n
@@ -912,8 +920,7 @@ def linear16_chosen_kernel(product: int, M: int, N: int, K: int, groups: int = 1
                            num_cus: int = 0) -> str:
     """Name of the kernel that a product (L16_*) of the layer takes, with rows on 16 bytes
     or not; "" for one without work."""
-    return load().ll_linear16_chosen_kernel(int(product), int(M), int(N), int(K), int(groups), int(bool(aligned)),
-                                            int(num_cus)).decode()
+    return load().ll_linear16_chosen_kernel(*_c_ints(product, M, N, K, groups, bool(aligned), num_cus)).decode()
 
 
 def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None, stream=None):
@@ -943,16 +950,16 @@ def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None
     pb = _group_vec(bias, groups, poff is not None, N, "bias")
     s = _stream(stream, X, W, Y, R, bias, offsets, workspace, *zs)
     pws, nws, workspace = _shares_workspace(L16_FORWARD, M, N, K, groups, workspace, stream, X)
-    _check(load().linear16_nt(M, N, K, t, px, ldx, groups, poff, pw, ldw, stride, pb, int(act), ty, pr, ldr, py, ldy,
+    _check(load().linear16_nt(M, N, K, t, px, ldx, groups, poff, pw, ldw, stride, pb, *_c_ints(act), ty, pr, ldr, py, ldy,
                               *held, pws, nws, s), "linear16_nt")
     return Y
 
 
 def linear16_grad_act_workspace_size(M: int, N: int, groups: int = 1) -> int:
     """Bytes of workspace linear16_grad_act needs for dbias."""
-    if M > _INT_MAX or N > _INT_MAX or groups > MAX_GROUPS:
-        raise ValueError(f"the calls take sizes up to {_INT_MAX} and {MAX_GROUPS} groups")
-    n = load().ll_linear16_grad_act_workspace_size(int(M), int(N), int(groups))
+    if groups > MAX_GROUPS:
+        raise ValueError(f"the calls take up to {MAX_GROUPS} groups")
+    n = load().ll_linear16_grad_act_workspace_size(*_c_ints(M, N, groups))
     if n < 0:
         raise ValueError("negative size")
     return n
@@ -985,7 +992,7 @@ def linear16_grad_act(DY, Z, act: int, DZ, dbias=None, offsets=None, workspace=N
                 raise ValueError("dbias on a stream that is given needs a workspace")
             workspace = torch.empty(linear16_grad_act_workspace_size(M, N, groups), dtype=torch.uint8, device=DZ.device)
         pws, nws = _workspace(workspace)
-    _check(load().linear16_grad_act(M, N, t, int(act), ty, pdy, lddy, groups, poff, *held, pdz, lddz, pb, pws, nws, s),
+    _check(load().linear16_grad_act(M, N, t, *_c_ints(act), ty, pdy, lddy, groups, poff, *held, pdz, lddz, pb, pws, nws, s),
            "linear16_grad_act")
     return DZ
 

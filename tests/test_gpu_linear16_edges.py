@@ -300,3 +300,15 @@ def test_bias_gradient_alone(act, groups, eight):
                                          torch.cuda.current_stream().cuda_stream)
     assert status == ll.OK
     assert torch.equal(got, want)
+
+
+def test_an_activation_past_a_c_int():
+    """Refused, not cut to its lower 32 bits."""
+    x, w = randn(1, 4, 32), randn(2, 8, 32)
+    y = torch.full((4, 8), 7.0, device=DEV).bfloat16()
+    for act in (2 ** 32, 2 ** 32 + 1, -2 ** 32 + 4, 2 ** 40):
+        with pytest.raises(ValueError):
+            ll.linear16_nt(x, w, None, act, None, y)
+        with pytest.raises(ValueError):
+            ll.linear16_grad_act(y, y, act, y)
+    assert (y == 7).all()

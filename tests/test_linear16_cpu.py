@@ -309,3 +309,24 @@ def test_sizes_no_product_takes():
             assert ll.linear16_chosen_kernel(product, *shape) != ""
         for product in (ll.L16_FORWARD, ll.L16_GRAD_INPUT):
             assert ll.linear16_workspace_size(product, *shape) in (0, 16 * 4 * 8 * 8)
+
+
+def test_numbers_past_a_c_int():
+    """Refused, not cut to their lower 32 bits."""
+    for wide in (2 ** 31, 2 ** 32 + 64, -2 ** 32 + 64):
+        for i in range(5):
+            shape = [64, 64, 64, 1, 256]
+            shape[i] = wide
+            *shape, cus = shape
+            with pytest.raises(ValueError):
+                ll.linear16_chosen_kernel(ll.L16_FORWARD, *shape, num_cus=cus)
+            if i < 4:
+                with pytest.raises(ValueError):
+                    ll.linear16_workspace_size(ll.L16_FORWARD, *shape)
+            if i < 3:
+                with pytest.raises(ValueError):
+                    ll.linear16_grad_act_workspace_size(*(shape[:2] + shape[3:] if i < 2 else (64, 64, wide)))
+        with pytest.raises(ValueError):
+            ll.linear16_chosen_kernel(wide, 64, 64, 64)
+        with pytest.raises(ValueError):
+            ll.linear16_workspace_size(wide, 64, 64, 64)
