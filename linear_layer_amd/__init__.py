@@ -931,7 +931,8 @@ def linear16_nt(X, W, bias, act: int, R, Y, Z=None, offsets=None, workspace=None
     numbers, int32, on the device) W is groups x N x K, bias groups x N, and rows outside
     all groups stay as they are. A product that does not fill the GPU gains from a workspace of
     linear16_workspace_size bytes: on the current stream it comes from torch's allocator, with
-    ``stream`` given the call runs without one unless it is given too. Returns Y."""
+    ``stream`` given the call runs without one unless it is given too, which for few rows takes
+    longer and adds in another order. ACT_RELU maps NaN to 0, as it does z <= 0. Returns Y."""
     if stream is None:
         st = _short_calls().linear16_nt(X, W, bias, act, R, Y, Z, offsets, workspace)
         if st is not None:

@@ -1,9 +1,9 @@
 // The tile kernel of the 16-bit layer and its gradients: forward, input gradient and
 // weight gradient, dense or by groups of rows.
 //
-// A workgroup computes BM x BM of C on v_mfma_f32_16x16x32 with FP32 sums, over stages of
-// 64 of the contracted axis in a ring of two LDS buffers. An operand lies in memory in one
-// of two ways:
+// A workgroup computes BM x BN of C on v_mfma_f32_16x16x32 with FP32 sums, over stages of
+// 64 of the contracted axis in rings of two or three LDS buffers, one for each operand. An operand
+// lies in memory in one of three ways:
 //   ROWS   the contracted axis is contiguous (X and W of the forward product, dZ of the
 //          input gradient): BM rows of 128 bytes a stage, their 16-byte chunks XORed by
 //          (row / 2) % 8, read with 128-bit LDS reads;
@@ -25,8 +25,10 @@
 // bits) in one store instruction, which is also the order that R and bias are read in and
 // in which four lanes hold one block of 32 of Z's 8 bits.
 //
-// Large products are bound by the matrix cores and the power they may draw: bfloat16 8192^3
-// takes 0.76 to 0.82 ms forward (1.34 to 1.46 PFLOP/s), 0.77 for dX (1.43), 0.79 for dW (1.39) and
+// Products of many whole rounds of large tiles are bound by the matrix cores and the power they may
+// draw; others by rounds that do not fill and by tiles' first loads and write-backs, which nothing
+// covers (matrix cores busy 32 to 55 % of the cycles). bfloat16 8192^3
+// takes 0.76 to 0.82 ms forward (1.34 to 1.46 PFLOP/s), 0.77 for dX (1.43), 0.79 to 0.83 for dW (1.32 to 1.39) and
 // 0.85 to 0.89 with X in 8 bits (1.24 to 1.29), where the library's forward product on the same
 // inputs reaches 1.61 and its product on other than rows 1.38. What else was measured there:
 // operands through registers instead of copies 1.23 to 1.33 PFLOP/s, eight waves of 128 x 64

@@ -1,6 +1,8 @@
-"""The 16-bit layer at its edges: codes whose rows end inside a word, GELU to FP32. References in float64 on
-the device by torch. Tolerances as in test_gpu_linear16: a sum of n products is off by at most
-n steps of 2^-23 of the sum of their magnitudes, and stored with half a step of its type."""
+"""The 16-bit layer at its edges: codes whose rows end inside a word, codes by kernel, NaN blocks,
+GELU to FP32, kept 8 bits against the call's own sums, the gradients of many groups, few rows in
+shares, the bias's gradient alone. References in float64 on the device by torch. Tolerances as in
+test_gpu_linear16: a sum of n products is off by at most n steps of 2^-23 of the sum of their
+magnitudes, and stored with half a step of its type."""
 import math
 
 import pytest
