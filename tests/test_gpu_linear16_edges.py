@@ -314,3 +314,35 @@ def test_an_activation_past_a_c_int():
         with pytest.raises(ValueError):
             ll.linear16_grad_act(y, y, act, y)
     assert (y == 7).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M", [40, 300])
+def test_empty_axes_by_group(M, t):
+    """Sums of nothing are zeros (and the bias, or beta's part) in the rows of groups, and rows outside stay."""
+    N, K, groups = 72, 40, [3, 20, 20, M - 5]
+    off = offsets_of(groups)
+    b = randn(3, 3, N, t="f32")
+    y = torch.full((M, N), 7.0, dtype=TYPES[t], device=DEV)
+    q = tuple(torch.full(s, 0xA5, dtype=torch.uint8, device=DEV) for s in ll.mx8_shapes(M, N))
+    none = torch.empty((M, 0), dtype=TYPES[t], device=DEV)
+    ll.linear16_nt(none, torch.empty((3, N, 0), dtype=TYPES[t], device=DEV), b, ll.ACT_RELU, None, y, Z=q, offsets=off)
+    z = ll.mx8_dequantize(*q, torch.empty((M, N), device=DEV))
+    for g, (a, e) in enumerate(ref.bounds(groups, M)):
+        row = tuple(torch.empty(s, dtype=torch.uint8, device=DEV) for s in ll.mx8_shapes(1, N))
+        ll.mx8_quantize(b[g:g + 1], *row)
+        assert torch.equal(y[a:e], b[g].clamp(min=0).to(TYPES[t]).expand(e - a, N))
+        assert torch.equal(z[a:e], ll.mx8_dequantize(*row, torch.empty((1, N), device=DEV)).expand(e - a, N))
+    dx = torch.full((M, K), 7.0, dtype=TYPES[t], device=DEV)
+    ll.linear16_grad_input(none, torch.empty((3, 0, K), dtype=TYPES[t], device=DEV), dx, offsets=off)
+    outside = torch.ones(M, dtype=torch.bool, device=DEV)
+    outside[3:M - 5] = False
+    assert (dx[~outside] == 0).all()
+    for v in (y, dx):
+        assert (v[outside] == 7).all()
+    assert (q[0][outside] == 0xA5).all() and (q[1][outside] == 0xA5).all()
+    for beta in (0.0, 0.5):
+        dw = torch.full((3, N, K), 3.0, device=DEV)
+        ll.linear16_grad_weight(torch.empty((0, N), dtype=TYPES[t], device=DEV), torch.empty((0, K), dtype=TYPES[t], device=DEV), dw,
+                                beta=beta, offsets=torch.zeros(4, dtype=torch.int32, device=DEV))
+        assert (dw == 3 * beta).all()
